@@ -14,6 +14,10 @@ fallback.  Build with ``python bit_block_quant_amd/build.py`` (or ``__graft_entr
     W      = qblk.dequant(blocks, qblk.SB4, m, k, torch.float32)
     xq, s  = qblk.quantize_act_i8(X)             # W4A8: int8 tokens + fp32 scales
     Y      = qblk.gemm_w4a8(qblk.quantize(w, qblk.W4G128), m, k, xq, s)
+    wq, ws = qblk.quantize_f8(w)                  # 8-bit floats, a scale per 128 x 128
+    Y      = qblk.linear_f8(X, wq, ws)            # X: (n, k) f32/f16/bf16 -> (n, m) of X's type
+    Y      = qblk.ffn_f8(X, w13, s13, w2, s2)     # gated feed-forward layer
+    Y, ids, weights = qblk.moe(qblk.SB4, X, logits, gate_up, down, inter, top_k)
 """
 import ctypes as C
 import os
@@ -31,6 +35,7 @@ _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 STATUS = {
     0: "QBLK_OK", 1: "QBLK_ERR_NULL", 2: "QBLK_ERR_SHAPE", 3: "QBLK_ERR_DTYPE",
     4: "QBLK_ERR_ALIGN", 5: "QBLK_ERR_UNSUPPORTED", 6: "QBLK_ERR_LAUNCH", 7: "QBLK_ERR_FORMAT",
+    8: "QBLK_ERR_WORKSPACE",
 }
 
 # every symbol include/qblk.h declares
@@ -39,6 +44,8 @@ EXPORTS = (
     "qblk_quantize_q4_0_ref", "qblk_quantize_sb4", "qblk_quantize_q4_k", "qblk_quantize_w4g128",
     "qblk_quantize_act_i8", "qblk_dequant", "qblk_gemv", "qblk_gemv_batch", "qblk_gemm", "qblk_gemm_w4a8",
     "qblk_set_deterministic", "qblk_deterministic", "qblk_status_string", "qblk_version",
+    "qblk_quantize_f8", "qblk_quantize_act_f8", "qblk_gemm_f8", "qblk_gemm_f8_workspace", "qblk_linear_f8",
+    "qblk_linear_f8_workspace", "qblk_ffn_f8", "qblk_ffn_f8_workspace", "qblk_moe", "qblk_moe_workspace",
 )
 
 
@@ -72,6 +79,18 @@ def _load():
               "qblk_quantize_w4g128", "qblk_quantize_act_i8", "qblk_dequant", "qblk_gemv", "qblk_gemm",
               "qblk_gemm_w4a8"):
         getattr(L, f).restype = i32
+    sz = C.c_size_t
+    L.qblk_quantize_f8.argtypes = L.qblk_quantize_act_f8.argtypes = [p, i32, i64, i64, p, p, p]
+    L.qblk_gemm_f8.argtypes = [p, p, i64, i64, p, p, i64, p, i32, p, sz, p]
+    L.qblk_linear_f8.argtypes = [p, p, i64, i64, p, i32, i64, p, i32, p, sz, p]
+    L.qblk_ffn_f8.argtypes = [p, p, p, p, i64, i64, p, i32, i64, p, i32, p, sz, p]
+    L.qblk_moe.argtypes = [p, p]
+    L.qblk_gemm_f8_workspace.argtypes = L.qblk_linear_f8_workspace.argtypes = [i64, i64, i64]
+    L.qblk_ffn_f8_workspace.argtypes, L.qblk_moe_workspace.argtypes = [i64, i64, i64], [p]
+    for f in ("qblk_quantize_f8", "qblk_quantize_act_f8", "qblk_gemm_f8", "qblk_linear_f8", "qblk_ffn_f8", "qblk_moe"):
+        getattr(L, f).restype = i32
+    for f in ("qblk_gemm_f8_workspace", "qblk_linear_f8_workspace", "qblk_ffn_f8_workspace", "qblk_moe_workspace"):
+        getattr(L, f).restype = sz
     L.qblk_status_string.argtypes, L.qblk_status_string.restype = [i32], C.c_char_p
     L.qblk_version.argtypes, L.qblk_version.restype = [], C.c_char_p
     L.qblk_set_deterministic.argtypes, L.qblk_set_deterministic.restype = [i32], i32
@@ -318,3 +337,172 @@ def gemm_w4a8(blocks, m, k, xq, scale, out=None, stream=None):
     _check(_lib.qblk_gemm_w4a8(_ptr(blocks), m, k, _ptr(xq), _ptr(scale), n, _ptr(out), _stream(stream)),
            "qblk_gemm_w4a8")
     return out
+
+
+# ------------------------------------------- 8-bit floats, blocks of 128
+F8 = torch.float8_e4m3fn
+_F8_IN = (F8, torch.uint8)  # codes as floats or as their bytes
+
+
+def _need_f8(codes, scale, name, device=None):
+    """A matrix of e4m3 codes (rows, k) with its scales; returns (device, rows, k)."""
+    dev = _need(codes, name, _F8_IN, ndim=2, device=device)
+    rows, k = codes.shape
+    if k % 128:
+        raise ValueError(f"{name}: the number of columns must be a multiple of 128, got {k}")
+    _need(scale, f"{name} scale", (torch.float32,), numel=-(-rows // 128) * (k // 128), device=dev)
+    return dev, rows, k
+
+
+def _workspace(work, nbytes, dev):
+    """The caller's workspace, checked, or a new one of nbytes."""
+    if work is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _need(work, "workspace", (torch.uint8,), min_numel=nbytes, device=dev)
+    return work
+
+
+def _nbytes(work):
+    return work.numel() if work is not None else 0
+
+
+def _out(out, shape, dtype, dev):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(out, "out", _FLOAT_IN, numel=shape[0] * shape[1], device=dev)
+    return out
+
+
+def quantize_f8(w, out=None, scale=None, stream=None):
+    """8-bit weights: (rows, k) f32/f16/bf16 -> (e4m3 codes (rows, k), fp32 scales (ceil(rows/128), k/128))."""
+    dev = _need(w, "w", _FLOAT_IN, ndim=2)
+    rows, k = w.shape
+    if out is None:
+        out = torch.empty((rows, k), dtype=F8, device=w.device)
+    if scale is None:
+        scale = torch.empty((-(-rows // 128), k // 128), dtype=torch.float32, device=w.device)
+    _need_f8(out, scale, "out", dev)
+    _need(out, "out", numel=rows * k)
+    _need_current(dev)
+    _check(_lib.qblk_quantize_f8(_ptr(w), _dtype(w), rows, k, _ptr(out), _ptr(scale), _stream(stream)),
+           "qblk_quantize_f8")
+    return out, scale
+
+
+def quantize_act_f8(x, out=None, scale=None, stream=None):
+    """8-bit activations: (n, k) f32/f16/bf16 -> (e4m3 codes (n, k), fp32 scales (n, k/128))."""
+    dev = _need(x, "x", _FLOAT_IN, ndim=2)
+    n, k = x.shape
+    if k % 128:
+        raise ValueError(f"x: the number of columns must be a multiple of 128, got {k}")
+    if out is None:
+        out = torch.empty((n, k), dtype=F8, device=x.device)
+    if scale is None:
+        scale = torch.empty((n, k // 128), dtype=torch.float32, device=x.device)
+    _need(out, "out", _F8_IN, numel=n * k, device=dev)
+    _need(scale, "scale", (torch.float32,), numel=n * (k // 128), device=dev)
+    _need_current(dev)
+    _check(_lib.qblk_quantize_act_f8(_ptr(x), _dtype(x), n, k, _ptr(out), _ptr(scale), _stream(stream)),
+           "qblk_quantize_act_f8")
+    return out, scale
+
+
+def gemm_f8(wq, ws, xq, xs, dtype=torch.float32, out=None, workspace=None, stream=None):
+    """Y (n, m) = X W^T from the codes and scales of both (quantize_f8, quantize_act_f8)."""
+    dev, m, k = _need_f8(wq, ws, "wq")
+    _need(xq, "xq", _F8_IN, ndim=2, dim1=k, device=dev)
+    n = xq.shape[0]
+    _need(xs, "xs", (torch.float32,), numel=n * (k // 128), device=dev)
+    out = _out(out, (n, m), dtype, dev)
+    work = _workspace(workspace, _lib.qblk_gemm_f8_workspace(m, k, n), dev)
+    _need_current(dev)
+    _check(_lib.qblk_gemm_f8(_ptr(wq), _ptr(ws), m, k, _ptr(xq), _ptr(xs), n, _ptr(out), _dtype(out), _ptr(work),
+                             _nbytes(work), _stream(stream)), "qblk_gemm_f8")
+    return out
+
+
+def linear_f8(x, wq, ws, dtype=None, out=None, workspace=None, stream=None):
+    """Y (n, m) = X W^T with X (n, k) f32/f16/bf16, quantized per token and 128
+    columns on the way, and W as quantize_f8 gives it; Y of X's type unless said."""
+    dev, m, k = _need_f8(wq, ws, "wq")
+    _need(x, "x", _FLOAT_IN, ndim=2, dim1=k, device=dev)
+    n = x.shape[0]
+    out = _out(out, (n, m), dtype or x.dtype, dev)
+    work = _workspace(workspace, _lib.qblk_linear_f8_workspace(m, k, n), dev)
+    _need_current(dev)
+    _check(_lib.qblk_linear_f8(_ptr(wq), _ptr(ws), m, k, _ptr(x), _dtype(x), n, _ptr(out), _dtype(out), _ptr(work),
+                               _nbytes(work), _stream(stream)), "qblk_linear_f8")
+    return out
+
+
+def ffn_f8(x, w13, s13, w2, s2, dtype=None, out=None, workspace=None, stream=None):
+    """A gated feed-forward layer, y = W2 (silu(Wg x) * (Wu x)): x (n, hidden),
+    w13 (2*inter, hidden) with the rows of Wg first, w2 (hidden, inter), both as
+    quantize_f8 gives them.  Returns (n, hidden), of x's type unless said."""
+    dev, rows, hidden = _need_f8(w13, s13, "w13")
+    _need_f8(w2, s2, "w2", dev)
+    inter = w2.shape[1]
+    if rows != 2 * inter or w2.shape[0] != hidden:
+        raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not make a gated layer")
+    _need(x, "x", _FLOAT_IN, ndim=2, dim1=hidden, device=dev)
+    n = x.shape[0]
+    out = _out(out, (n, hidden), dtype or x.dtype, dev)
+    work = _workspace(workspace, _lib.qblk_ffn_f8_workspace(hidden, inter, n), dev)
+    _need_current(dev)
+    _check(_lib.qblk_ffn_f8(_ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), hidden, inter, _ptr(x), _dtype(x), n, _ptr(out),
+                            _dtype(out), _ptr(work), _nbytes(work), _stream(stream)), "qblk_ffn_f8")
+    return out
+
+
+# --------------------------------------------------- mixture of experts
+class _Moe(C.Structure):
+    """qblk_moe_t"""
+    _fields_ = [("fmt", C.c_int), ("n", C.c_int64), ("hidden", C.c_int64), ("inter", C.c_int64),
+                ("experts", C.c_int), ("top_k", C.c_int), ("x", C.c_void_p), ("xt", C.c_int),
+                ("logits", C.c_void_p), ("renorm", C.c_int), ("weight_scale", C.c_float),
+                ("gate_up", C.c_void_p), ("down", C.c_void_p), ("ids", C.c_void_p), ("weights", C.c_void_p),
+                ("y", C.c_void_p), ("yt", C.c_int), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
+def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1.0, experts=None, ids=None,
+        weights=None, dtype=None, out=None, workspace=None, stream=None):
+    """A mixture-of-experts layer for a few tokens out of packed 4-bit experts.
+
+    x (n, hidden) f16/bf16; logits (n, experts) fp32, from which each token's
+    top_k experts and their weights are taken; gate_up: experts x 2*inter rows
+    of hidden weights (per expert the gate rows, then the up rows) and down:
+    experts x hidden rows of inter weights, packed as quantize() does.  With
+    logits=None, give experts, ids (n, top_k) int32 and weights (n, top_k) fp32
+    of a router of your own (an id outside [0, experts) counts for nothing).
+    Returns (y (n, hidden) of x's type unless said, ids, weights)."""
+    _need_dims(inter=inter, top_k=top_k)
+    dev = _need(x, "x", (torch.float16, torch.bfloat16), ndim=2)
+    n, hidden = x.shape
+    if logits is not None:
+        _need(logits, "logits", (torch.float32,), ndim=2, device=dev)
+        if logits.shape[0] != n:
+            raise ValueError(f"logits: {logits.shape[0]} rows for {n} tokens")
+        if experts is not None and experts != logits.shape[1]:
+            raise ValueError(f"logits: {logits.shape[1]} columns for {experts} experts")
+        experts = logits.shape[1]
+    elif experts is None or ids is None or weights is None:
+        raise ValueError("without logits, experts, ids and weights are needed")
+    else:
+        _need_dims(experts=experts)
+    if ids is None:
+        ids = torch.empty((n, top_k), dtype=torch.int32, device=x.device)
+    if weights is None:
+        weights = torch.empty((n, top_k), dtype=torch.float32, device=x.device)
+    _need(ids, "ids", (torch.int32,), numel=n * top_k, device=dev)
+    _need(weights, "weights", (torch.float32,), numel=n * top_k, device=dev)
+    _need(gate_up, "gate_up", (torch.uint8,), min_numel=_packed(fmt, experts * 2 * inter, hidden), device=dev)
+    _need(down, "down", (torch.uint8,), min_numel=_packed(fmt, experts * hidden, inter), device=dev)
+    out = _out(out, (n, hidden), dtype or x.dtype, dev)
+    a = _Moe(fmt, n, hidden, inter, experts, top_k, _ptr(x).value, _DT[x.dtype], _ptr(logits).value, int(renorm),
+             weight_scale, _ptr(gate_up).value, _ptr(down).value, _ptr(ids).value, _ptr(weights).value,
+             _ptr(out).value, _dtype(out))
+    work = _workspace(workspace, _lib.qblk_moe_workspace(C.byref(a)), dev)
+    a.workspace, a.workspace_bytes = _ptr(work).value, _nbytes(work)
+    _need_current(dev)
+    _check(_lib.qblk_moe(C.byref(a), _stream(stream)), "qblk_moe")
+    return out, ids, weights

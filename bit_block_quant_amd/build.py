@@ -29,7 +29,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqblk.so")
 HBMREF_LIB = os.path.join(HERE, "libqblk_hbmref.so")
-SOURCES = ["qblk_abi.hip", "qblk_quant.hip", "qblk_gemv.hip", "qblk_gemm.hip", "qblk_w4a8.hip"]
+SOURCES = ["qblk_abi.hip", "qblk_quant.hip", "qblk_gemv.hip", "qblk_gemm.hip", "qblk_w4a8.hip",
+           "qblk_ffn_abi.hip", "qblk_f8.hip", "qblk_moe.hip"]
 HBMREF_SOURCES = ["hbm_read.hip"]
 ARCH = "gfx950"
 OBJ_DIR = os.path.join(HERE, "_build")

@@ -35,6 +35,24 @@ hipError_t launch_gemm(int fmt, const void* blocks, int64_t m, int64_t k, const 
                        int64_t n, float* y, hipStream_t s);
 hipError_t launch_fill_zero(float* y, int64_t n, hipStream_t s);
 
+// 8-bit products with a scale for each block of 128; sizes positive, `work`
+// of at least the bytes the matching _workspace function gives
+hipError_t launch_quantize_f8(const void* w, int wt, int64_t rows, int64_t k, uint8_t* codes, float* scale,
+                              hipStream_t s);
+hipError_t launch_quantize_act_f8(const void* x, int xt, int64_t n, int64_t k, uint8_t* xq, float* scale,
+                                  hipStream_t s);
+int64_t gemm_f8_workspace(int64_t m, int64_t k, int64_t n);
+hipError_t launch_gemm_f8(const uint8_t* w, const float* ws, int64_t m, int64_t k, const uint8_t* xq,
+                          const float* xs, int64_t n, void* y, int yt, void* work, hipStream_t s);
+int64_t linear_f8_workspace(int64_t m, int64_t k, int64_t n);
+hipError_t launch_linear_f8(const uint8_t* w, const float* ws, int64_t m, int64_t k, const void* x, int xt,
+                            int64_t n, void* y, int yt, void* work, hipStream_t s);
+int64_t ffn_f8_workspace(int64_t hidden, int64_t inter, int64_t n);
+hipError_t launch_ffn_f8(const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2, int64_t hidden,
+                         int64_t inter, const void* x, int xt, int64_t n, void* y, int yt, void* work,
+                         hipStream_t s);
+hipError_t launch_zero_bytes(void* y, int64_t bytes, hipStream_t s);
+
 // A dispatch packet counts its work-items in 32 bits per grid dimension, so
 // one launch covers at most 2^32 - 1 threads along x.  Launchers whose grid
 // grows with the data run it in pieces of whole workgroups:

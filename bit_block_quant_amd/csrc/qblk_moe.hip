@@ -1,0 +1,595 @@
+// qblk_moe.hip -- a mixture-of-experts layer for a few tokens, straight out of
+// the packed 4-bit experts, in two kernels on gfx950.
+//
+//   route     the top_k experts of a token by logit (ties: the lowest index;
+//             -inf and NaN never taken), softmax weights in fp32
+//   k_moe_up  h[p] = silu(G_e x) * (U_e x) for every pair p of a token and one
+//             of its experts e
+//   k_moe_down  y[t] = sum_j w[t,j] D_e h[(t,j)]
+//
+// Both are bound by the packed bytes of the experts that are reached.  The
+// tokens of one expert are gathered into a matrix-core tile of up to 16, so an
+// expert's weights are read once for all of them; the codes are decoded into
+// registers in the operand layout of the 16x16x32 matrix instructions.
+//
+// Layout.  Four units of 32 weights of a row are one 16-byte load each in the
+// four lane quarters; a 4 x 4 exchange between the quarters (v_permlane swaps)
+// turns them into one unit per register with its four dwords over the
+// quarters, which is a matrix operand: quarter q holds weights 4q..4q+3 (low
+// nibbles) and 16+4q..16+4q+3 (high).  The other operand is read from memory
+// in that order.  A code byte 0..15 is the e4m3 number code * 2^-9 as it
+// stands (subnormals below 8, the first binade from 8 on), so one conversion
+// with scale 2^9 gives two exact codes as f16 or bf16.
+//
+// Sums.  Codes and activations are exact in the operands, products and sums
+// fp32.  The offset of the format (-8, or the affine formats' own) multiplies
+// sum(x) of the unit, which a matrix product with a constant operand gives in
+// the layout of the result.  h is carried as two bf16 parts (hi + lo, 2^-17
+// relative), which is half the size of what a third part would make it and
+// ahead of every 16-bit result.
+#include "qblk_device.h"
+#include "qblk_launch.h"
+#include "qblk_moe.h"
+
+namespace qblk {
+namespace {
+
+typedef __bf16 bf16x2_n __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_n __attribute__((ext_vector_type(8)));
+typedef half_t half8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kUpWaves = 8;     // waves that share the columns of one tile
+constexpr int kDownWaves = 16;  // waves that share the experts of one tile
+constexpr uint32_t kLo4 = 0x0F0F0F0Fu;
+
+// The routing of one piece, in LDS or in the workspace: experts with at least
+// one pair are slots 0 .. active-1 in order of their index; slot s owns
+// list[off[s] .. off[s+1]).
+struct Table {
+  int active;
+  int expert[kMoeMaxExperts];
+  int off[kMoeMaxExperts + 1];
+  int list[kMoeMaxPairs];
+};
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __builtin_expf(-g)) * u; }
+
+// ------------------------------------------------------------ the operands
+// 16-bit operand types of the matrix cores
+template <bool F16>
+struct Op;
+template <>
+struct Op<true> {
+  typedef half8_t v8;
+  static __device__ __forceinline__ uint32_t two(uint32_t codes, bool hi) {
+    const half2_t p = hi ? __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 512.0f, true))
+                         : __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 512.0f, false));
+    return __builtin_bit_cast(uint32_t, p);
+  }
+  static __device__ __forceinline__ float4_t mma(u32x4 a, u32x4 b, float4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static constexpr uint32_t one2 = 0x3C003C00u, minus8 = 0xC800C800u;
+};
+template <>
+struct Op<false> {
+  typedef bf16x8_n v8;
+  static __device__ __forceinline__ uint32_t two(uint32_t codes, bool hi) {
+    const bf16x2_n p = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 512.0f, true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 512.0f, false);
+    return __builtin_bit_cast(uint32_t, p);
+  }
+  static __device__ __forceinline__ float4_t mma(u32x4 a, u32x4 b, float4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static constexpr uint32_t one2 = 0x3F803F80u, minus8 = 0xC100C100u;
+};
+
+template <bool F16>
+__device__ __forceinline__ u32x4 codes8_op(uint32_t t) {
+  const uint32_t lo = t & kLo4, hi = (t >> 4) & kLo4;
+  return u32x4{Op<F16>::two(lo, false), Op<F16>::two(lo, true), Op<F16>::two(hi, false), Op<F16>::two(hi, true)};
+}
+
+// reg d of quarter q -> reg q of quarter d
+__device__ __forceinline__ void quarters4x4(uint32_t v[4]) {
+#pragma unroll
+  for (int d = 0; d < 2; d++) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v[d], v[d + 2], false, false);
+    v[d] = r[0];
+    v[d + 2] = r[1];
+  }
+#pragma unroll
+  for (int d = 0; d < 4; d += 2) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v[d], v[d + 1], false, false);
+    v[d] = r[0];
+    v[d + 1] = r[1];
+  }
+}
+
+// ------------------------------------------------------------- the formats
+// 256 weights (8 units) of one row per lane row: what is loaded, and unit u's
+// scale and offset.  `units` is the number of units of a row (Q4_0 rows may
+// end inside a step; every other format has whole super-blocks).
+template <int FMT>
+struct Step;
+
+template <>
+struct Step<QBLK_SB4> {
+  static constexpr bool affine = false;
+  uint32_t raw[2][4], h[3];
+  __device__ __forceinline__ void load(const uint8_t* row, int sb, int q, int) {
+    const uint8_t* p = row + static_cast<int64_t>(sb) * 138;
+    load16_a2(p + 10 + 16 * q, raw[0]);
+    load16_a2(p + 74 + 16 * q, raw[1]);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const u32x3_a4 v = *reinterpret_cast<const u32x3_a4*>(a & ~uintptr_t(3));
+    const uint32_t sh = static_cast<uint32_t>(a & 3u);
+    h[0] = __builtin_amdgcn_alignbyte(v.y, v.x, sh);
+    h[1] = __builtin_amdgcn_alignbyte(v.z, v.y, sh);
+    h[2] = v.z >> (8 * sh);
+  }
+  __device__ __forceinline__ float scale(int u) const {
+    const uint32_t w = h[(u + 2) >> 2];
+    const int c = static_cast<int8_t>(w >> (8 * ((u + 2) & 3)));
+    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(c);
+  }
+  __device__ __forceinline__ float offset(int) const { return 0.0f; }
+  __device__ __forceinline__ void finish(int, int, int) {}
+};
+
+template <>
+struct Step<QBLK_SB4_AFFINE> {
+  static constexpr bool affine = true;
+  uint32_t raw[2][4], h[5];
+  __device__ __forceinline__ void load(const uint8_t* row, int sb, int q, int) {
+    const uint8_t* p = row + static_cast<int64_t>(sb) * 148;  // a multiple of 4: every field is dword aligned
+    const u32x4_a4 a = *reinterpret_cast<const u32x4_a4*>(p + 20 + 16 * q);
+    const u32x4_a4 b = *reinterpret_cast<const u32x4_a4*>(p + 84 + 16 * q);
+    const u32x4_a4 c = *reinterpret_cast<const u32x4_a4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      raw[0][i] = a[i];
+      raw[1][i] = b[i];
+      h[i] = c[i];
+    }
+    h[4] = *reinterpret_cast<const uint32_t*>(p + 16);
+  }
+  __device__ __forceinline__ float scale(int u) const {
+    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(static_cast<int8_t>(h[1 + (u >> 2)] >> (8 * (u & 3))));
+  }
+  __device__ __forceinline__ float offset(int u) const {
+    return f16_bits_to_f32(h[0] >> 16) * static_cast<float>(static_cast<int8_t>(h[3 + (u >> 2)] >> (8 * (u & 3))));
+  }
+  __device__ __forceinline__ void finish(int, int, int) {}
+};
+
+template <>
+struct Step<QBLK_Q4_K> {
+  static constexpr bool affine = true;
+  uint32_t raw[2][4], h[4];
+  __device__ __forceinline__ void load(const uint8_t* row, int sb, int q, int) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(sb) * 144);  // 16-byte aligned
+    const u32x4 a = p[1 + q], b = p[5 + q], c = p[0];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      raw[0][i] = a[i];
+      raw[1][i] = b[i];
+      h[i] = c[i];
+    }
+  }
+  __device__ __forceinline__ float scale(int u) const {
+    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(q4k_scale6(h[1], h[2], u));
+  }
+  __device__ __forceinline__ float offset(int u) const {
+    return -(f16_bits_to_f32(h[0] >> 16) * static_cast<float>(q4k_min6(h[2], h[3], u)));
+  }
+  __device__ __forceinline__ void finish(int, int, int) {}
+};
+
+template <>
+struct Step<QBLK_Q4_0> {
+  static constexpr bool affine = false;
+  uint32_t raw[2][4], d[4];
+  __device__ __forceinline__ void load(const uint8_t* row, int sb, int q, int units) {
+    uint32_t s[2];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const int u = 8 * sb + 4 * j + q;
+      const uint8_t* p = row + static_cast<int64_t>(u < units ? u : units - 1) * 18;
+      load16_a2(p + 2, raw[j]);
+      s[j] = load_u16(p);
+    }
+    d[0] = s[0];
+    d[1] = s[1];
+  }
+  // the scales of all eight units to every quarter; a unit past the row's end scales by zero
+  __device__ __forceinline__ void finish(int sb, int q, int units) {
+    const uint32_t a = 8 * sb + q < units ? d[0] : 0u, b = 8 * sb + 4 + q < units ? d[1] : 0u;
+    d[0] = d[1] = d[2] = d[3] = a | (b << 16);
+    quarters4x4(d);
+  }
+  __device__ __forceinline__ float scale(int u) const {
+    return f16_bits_to_f32(u < 4 ? d[u & 3] & 0xffffu : d[u & 3] >> 16);
+  }
+  __device__ __forceinline__ float offset(int) const { return 0.0f; }
+};
+
+// acc += (the step's 16 rows) x (16 gathered token rows): PARTS operands a[part][unit]
+template <int FMT, bool F16, int PARTS>
+__device__ __forceinline__ void mul_unit(const Step<FMT>& w, int u, uint32_t codes, const u32x4 (&a)[PARTS],
+                                         const float4_t& xs, float4_t& acc) {
+  const u32x4 b = codes8_op<F16>(codes);
+  float4_t p = Step<FMT>::affine ? float4_t{0, 0, 0, 0} : xs;
+#pragma unroll
+  for (int i = 0; i < PARTS; i++) p = Op<F16>::mma(a[i], b, p);
+  const float s = w.scale(u);
+  if constexpr (Step<FMT>::affine) {
+    const float o = w.offset(u);
+#pragma unroll
+    for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(o, xs[i], __builtin_fmaf(s, p[i], acc[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(s, p[i], acc[i]);
+  }
+}
+
+// sum(x) of the unit per token (times -8 for the formats whose offset that is)
+template <int FMT, bool F16, int PARTS>
+__device__ __forceinline__ float4_t unit_sum(const u32x4 (&a)[PARTS]) {
+  const uint32_t c = Step<FMT>::affine ? Op<F16>::one2 : Op<F16>::minus8;
+  float4_t p = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < PARTS; i++) p = Op<F16>::mma(a[i], u32x4{c, c, c, c}, p);
+  return p;
+}
+
+// ---------------------------------------------------------------- routing
+// One token's experts by one wave: lane l looks at experts l, l + 64, ...
+__device__ void route_token(const float* __restrict__ logits, int experts, int top_k, int renorm, float wscale,
+                            int lane, int* ids, int32_t* __restrict__ out_ids, float* __restrict__ out_w) {
+  constexpr int PER = kMoeMaxExperts / 64;
+  const float none = -__builtin_huge_valf();
+  float v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    v[i] = none;
+    if (64 * i < experts) {
+      const int e = 64 * i + lane;
+      const float l = e < experts ? logits[e] : none;
+      v[i] = l > none ? __builtin_fminf(l, 3.402823466e38f) : none;  // NaN is never taken
+    }
+  }
+  float top = none, sum = 0.0f, mine = 0.0f;
+  int id = -1;
+  for (int j = 0; j < top_k; j++) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < PER; i++)
+      if (64 * i < experts) m = __builtin_fmaxf(m, v[i]);
+    m = group_max<kWave>(m);
+    if (j == 0) {
+      top = m;
+      if (!renorm && m > none) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+          if (64 * i < experts) s += v[i] > none ? __builtin_expf(v[i] - top) : 0.0f;
+#pragma unroll
+        for (int x = 1; x < kWave; x <<= 1) s += __shfl_xor(s, x, kWave);
+        sum = s;
+      }
+    }
+    int e = -1;
+    if (m > none) {
+#pragma unroll
+      for (int i = 0; i < PER; i++)
+        if (64 * i < experts && e < 0) {
+          const uint64_t hit = __builtin_amdgcn_ballot_w64(v[i] == m);
+          if (hit != 0) {
+            const int at = __builtin_ctzll(hit);
+            e = 64 * i + at;
+            if (lane == at) v[i] = none;
+          }
+        }
+      const float p = __builtin_expf(m - top);
+      if (renorm) sum += p;
+      if (lane == j) {
+        id = e;
+        mine = p;
+      }
+    }
+  }
+  if (lane < top_k) {
+    ids[lane] = id;
+    if (out_ids != nullptr) {
+      out_ids[lane] = id;
+      out_w[lane] = id >= 0 ? mine / sum * wscale : 0.0f;
+    }
+  }
+}
+
+// The table from ids (pairs of them, in LDS); all threads of the workgroup.
+__device__ void build_table(const int* ids, int pairs, int experts, Table& t, int* cursor) {
+  for (int e = threadIdx.x; e < experts; e += blockDim.x) cursor[e] = 0;
+  __syncthreads();
+  for (int p = threadIdx.x; p < pairs; p += blockDim.x)
+    if (ids[p] >= 0) atomicAdd(&cursor[ids[p]], 1);
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int slots = 0, total = 0;
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+      const int e = e0 + lane;
+      const int c = e < experts ? cursor[e] : 0;
+      int run = c;  // inclusive sum over the lanes
+#pragma unroll
+      for (int x = 1; x < kWave; x <<= 1) {
+        const int o = __shfl_up(run, x, kWave);
+        if (lane >= x) run += o;
+      }
+      const uint64_t some = __builtin_amdgcn_ballot_w64(c > 0);
+      if (c > 0) {
+        const int s = slots + __popcll(some & ((uint64_t(1) << lane) - 1));
+        t.expert[s] = e;
+        t.off[s] = total + run - c;
+        cursor[e] = total + run - c;
+      }
+      slots += __popcll(some);
+      total += __shfl(run, 63, kWave);
+    }
+    if (lane == 0) {
+      t.active = slots;
+      t.off[slots] = total;
+    }
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < pairs; p += blockDim.x)
+    if (ids[p] >= 0) t.list[atomicAdd(&cursor[ids[p]], 1)] = p;
+  __syncthreads();
+}
+
+// --------------------------------------------------------------- gate, up
+// A workgroup takes tiles of 16 gate rows and the 16 up rows that go with
+// them, for all tokens of one expert; its waves split the columns (wave w
+// takes 256-column steps w, w + 8, ...) and their sums meet in LDS.
+// Workgroups are persistent, so the routing is worked out once in each rather
+// than by a launch of its own.
+template <int FMT, bool F16>
+__global__ __launch_bounds__(kUpWaves* kWave) void k_moe_up(MoeArgs a) {
+  __shared__ Table table;
+  __shared__ int ids[kMoeMaxPairs];
+  __shared__ int cursor[kMoeMaxExperts];
+  __shared__ float4_t red[kUpWaves][2][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int pairs = a.n * a.top_k;
+
+  if (a.logits != nullptr) {
+    for (int t = wave; t < a.n; t += kUpWaves)
+      route_token(a.logits + static_cast<int64_t>(t) * a.experts, a.experts, a.top_k, a.renorm, a.wscale, lane,
+                  ids + t * a.top_k, blockIdx.x == 0 ? a.ids + t * a.top_k : nullptr, a.weights + t * a.top_k);
+  } else {
+    for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
+      const int e = a.ids[p];
+      ids[p] = e >= 0 && e < a.experts ? e : -1;
+    }
+  }
+  __syncthreads();
+  build_table(ids, pairs, a.experts, table, cursor);
+  if (blockIdx.x == 0) {
+    Table* t = static_cast<Table*>(a.table);
+    for (int s = threadIdx.x; s <= table.active; s += blockDim.x) {
+      if (s < table.active) t->expert[s] = table.expert[s];
+      t->off[s] = table.off[s];
+    }
+    for (int p = threadIdx.x; p < table.off[table.active]; p += blockDim.x) t->list[p] = table.list[p];
+    if (threadIdx.x == 0) t->active = table.active;
+  }
+
+  const int tiles = a.inter / 16, steps = (a.hidden + 255) / 256, units = a.hidden / 32;
+  const int64_t tasks = static_cast<int64_t>(table.active) * tiles;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
+    const int64_t row = static_cast<int64_t>(table.expert[slot]) * 2 * a.inter + 16 * tile + r;
+    const uint8_t* gate = a.gate_up + row * a.up_row_bytes;
+    const uint8_t* up = gate + static_cast<int64_t>(a.inter) * a.up_row_bytes;
+    const int first = table.off[slot], count = table.off[slot + 1] - first;
+    for (int c0 = 0; c0 < count; c0 += 16) {
+      const bool live = c0 + r < count;  // the other lanes' rows of the tile are zero
+      const int pair = table.list[first + (live ? c0 + r : 0)];
+      const uint8_t* x = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(pair / a.top_k) * a.hidden * 2 + 8 * q;
+      float4_t ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
+      for (int sb = wave; sb < steps; sb += kUpWaves) {
+        Step<FMT> g, v;
+        g.load(gate, sb, q, units);
+        v.load(up, sb, q, units);
+        u32x4 xa[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+          xa[u] = u32x4{0, 0, 0, 0};
+          if (live && 8 * sb + u < units) {
+            const u32x2 l0 = *reinterpret_cast<const u32x2*>(x + (8 * sb + u) * 64);
+            const u32x2 l1 = *reinterpret_cast<const u32x2*>(x + (8 * sb + u) * 64 + 32);
+            xa[u] = u32x4{l0.x, l0.y, l1.x, l1.y};
+          }
+        }
+        g.finish(sb, q, units);
+        v.finish(sb, q, units);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          quarters4x4(g.raw[j]);
+          quarters4x4(v.raw[j]);
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            const u32x4 op[1] = {xa[4 * j + u]};
+            const float4_t xs = unit_sum<FMT, F16, 1>(op);
+            mul_unit<FMT, F16, 1>(g, 4 * j + u, g.raw[j][u], op, xs, ga);
+            mul_unit<FMT, F16, 1>(v, 4 * j + u, v.raw[j][u], op, xs, ua);
+          }
+        }
+      }
+      red[wave][0][lane] = ga;
+      red[wave][1][lane] = ua;
+      __syncthreads();
+      // lane (row r, quarter q) of the sums holds tokens 4q .. 4q+3
+      if (threadIdx.x < 256) {
+        const int tok = threadIdx.x >> 4, rr = threadIdx.x & 15;
+        if (c0 + tok < count) {
+          float gs = 0.0f, us = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kUpWaves; w++) {
+            gs += red[w][0][(tok >> 2) * 16 + rr][tok & 3];
+            us += red[w][1][(tok >> 2) * 16 + rr][tok & 3];
+          }
+          const float h = silu_mul(gs, us);
+          const uint16_t hi = f32_to_bf16_bits(h);
+          const float rest = h - bf16_bits_to_f32(hi);
+          const int col = 16 * tile + rr;
+          // four hi, four lo, ... : one 16-byte load per lane in k_moe_down
+          uint16_t* out = reinterpret_cast<uint16_t*>(a.h) +
+                          (static_cast<int64_t>(table.list[first + c0 + tok]) * a.inter + (col & ~3)) * 2 + (col & 3);
+          out[0] = hi;
+          out[4] = __builtin_isfinite(rest) ? f32_to_bf16_bits(rest) : 0;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// -------------------------------------------------------------------- down
+// A workgroup owns 16 rows of y for every token.  Its waves take the pairs of
+// (expert, slice of the columns); each writes its fp32 sums per pair to a
+// slot of its own in LDS, and at the end y is put together from the slots in
+// the order of the token's experts: no atomics, no second pass over memory.
+template <int FMT>
+__global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int max_slices) {
+  extern __shared__ __align__(16) float slots[];  // [slice][pair][16]
+  const Table* table = static_cast<const Table*>(a.table);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int pairs = a.n * a.top_k;
+  const int active = table->active;
+  const int steps = (a.inter + 255) / 256, units = a.inter / 32;
+  // slices: as many as give every wave work, evenly
+  int slices = active > 0 ? (2 * kDownWaves + active - 1) / active : 1;
+  slices = slices < max_slices ? slices : max_slices;
+  slices = slices < steps ? slices : steps;
+  const int per = (steps + slices - 1) / slices;
+  slices = (steps + per - 1) / per;
+  const int row0 = blockIdx.x * 16;
+
+  for (int task = wave; task < active * slices; task += kDownWaves) {
+    const int slot = task / slices, slice = task - slot * slices;
+    const int first = table->off[slot], count = table->off[slot + 1] - first;
+    const uint8_t* w = a.down + (static_cast<int64_t>(table->expert[slot]) * a.hidden + row0 + r) * a.down_row_bytes;
+    const int sb1 = (slice + 1) * per < steps ? (slice + 1) * per : steps;
+    for (int c0 = 0; c0 < count; c0 += 16) {
+      const bool live = c0 + r < count;
+      const int pair = table->list[first + (live ? c0 + r : 0)];
+      const uint8_t* h = reinterpret_cast<const uint8_t*>(a.h) + static_cast<int64_t>(pair) * a.inter * 4 + 16 * q;
+      float4_t acc = {0, 0, 0, 0};
+      for (int sb = slice * per; sb < sb1; sb++) {
+        Step<FMT> s;
+        s.load(w, sb, q, units);
+        s.finish(sb, q, units);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          u32x4 ha[4][2];
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            ha[u][0] = ha[u][1] = u32x4{0, 0, 0, 0};
+            const int at = 8 * sb + 4 * j + u;
+            if (live && at < units) {
+              ha[u][0] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128);
+              ha[u][1] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128 + 64);
+            }
+          }
+          quarters4x4(s.raw[j]);
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            const u32x4 op[2] = {u32x4{ha[u][0].x, ha[u][0].y, ha[u][1].x, ha[u][1].y},
+                                 u32x4{ha[u][0].z, ha[u][0].w, ha[u][1].z, ha[u][1].w}};
+            const float4_t xs = unit_sum<FMT, false, 2>(op);
+            mul_unit<FMT, false, 2>(s, 4 * j + u, s.raw[j][u], op, xs, acc);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (c0 + 4 * q + i < count)
+          slots[(slice * pairs + table->list[first + c0 + 4 * q + i]) * 16 + r] = acc[i];
+    }
+  }
+  __syncthreads();
+  for (int o = threadIdx.x; o < a.n * 16; o += kDownWaves * kWave) {
+    const int t = o >> 4, rr = o & 15;
+    float y = 0.0f;
+    for (int j = 0; j < a.top_k; j++) {
+      const int p = t * a.top_k + j;
+      const int e = a.ids[p];
+      if (e < 0 || e >= a.experts) continue;
+      float sum = 0.0f;
+      for (int s = 0; s < slices; s++) sum += slots[(s * pairs + p) * 16 + rr];
+      y = __builtin_fmaf(a.weights[p], sum, y);
+    }
+    const int64_t at = static_cast<int64_t>(t) * a.hidden + row0 + rr;
+    if (a.yt == QBLK_F32)
+      static_cast<float*>(a.y)[at] = y;
+    else
+      static_cast<uint16_t*>(a.y)[at] = a.yt == QBLK_F16 ? f32_to_f16_bits(y) : f32_to_bf16_bits(y);
+  }
+}
+
+template <int FMT>
+hipError_t run(const MoeArgs& a, hipStream_t s) {
+  const int64_t reach = static_cast<int64_t>(a.n) * a.top_k < a.experts ? static_cast<int64_t>(a.n) * a.top_k : a.experts;
+  const int64_t tasks = reach * (a.inter / 16);
+  const int64_t most = static_cast<int64_t>(cu_count()) * 3;
+  const unsigned grid = static_cast<unsigned>(tasks < most ? tasks : most);
+  if (a.xt == QBLK_F16)
+    k_moe_up<FMT, true><<<grid, kUpWaves * kWave, 0, s>>>(a);
+  else
+    k_moe_up<FMT, false><<<grid, kUpWaves * kWave, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int pairs = a.n * a.top_k;
+  const int max_slices = kMoeMaxPairs / pairs < 2 * kDownWaves ? kMoeMaxPairs / pairs : 2 * kDownWaves;
+  const size_t lds = static_cast<size_t>(max_slices) * pairs * 64;
+  log_launch("moe fmt=%d n=%d top_k=%d experts=%d hidden=%d inter=%d up grid=%u down grid=%d slices<=%d", FMT, a.n,
+             a.top_k, a.experts, a.hidden, a.inter, grid, a.hidden / 16, max_slices);
+  k_moe_down<FMT><<<dim3(static_cast<unsigned>(a.hidden / 16)), kDownWaves * kWave, lds, s>>>(a, max_slices);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t moe_table_bytes() { return static_cast<int64_t>((sizeof(Table) + 255) / 256 * 256); }
+
+hipError_t launch_moe(int fmt, const MoeArgs& all, int64_t n, hipStream_t s) {
+  const int64_t per = kMoeMaxPairs / all.top_k;
+  const int64_t ybytes = all.yt == QBLK_F32 ? 4 : 2;
+  for (int64_t t0 = 0; t0 < n; t0 += per) {
+    MoeArgs a = all;
+    a.n = static_cast<int>(n - t0 < per ? n - t0 : per);
+    a.x = static_cast<const uint8_t*>(all.x) + t0 * all.hidden * 2;
+    a.y = static_cast<uint8_t*>(all.y) + t0 * all.hidden * ybytes;
+    if (all.logits != nullptr) a.logits = all.logits + t0 * all.experts;
+    a.ids = all.ids + t0 * all.top_k;
+    a.weights = all.weights + t0 * all.top_k;
+    hipError_t e;
+    switch (fmt) {
+      case QBLK_Q4_0: e = run<QBLK_Q4_0>(a, s); break;
+      case QBLK_SB4: e = run<QBLK_SB4>(a, s); break;
+      case QBLK_SB4_AFFINE: e = run<QBLK_SB4_AFFINE>(a, s); break;
+      default: e = run<QBLK_Q4_K>(a, s); break;
+    }
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace qblk

@@ -122,7 +122,8 @@ typedef enum {
   QBLK_ERR_ALIGN = 4,       /* a data pointer is not 16-byte aligned    */
   QBLK_ERR_UNSUPPORTED = 5, /* format/type combination not implemented  */
   QBLK_ERR_LAUNCH = 6,      /* the kernel launch failed                 */
-  QBLK_ERR_FORMAT = 7       /* unknown format                           */
+  QBLK_ERR_FORMAT = 7,      /* unknown format                           */
+  QBLK_ERR_WORKSPACE = 8    /* the workspace is smaller than the call needs */
 } qblk_status_t;
 
 typedef void* qblk_stream_t; /* hipStream_t */
@@ -262,6 +263,121 @@ qblk_status_t qblk_set_deterministic(int on);
 
 /* 1 when reproducible products are on (qblk_set_deterministic), else 0. */
 int qblk_deterministic(void);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point with a scale for each block of 128: the format for the
+ * matrices that 4 bits are too few for (dense feed-forward layers, shared
+ * experts, the output head).  Codes are OCP e4m3 (4 exponent bits, 3 mantissa
+ * bits, largest value 448, no infinities), one byte each, row-major; a scale
+ * covers 128 x 128 weights (wscale[r/128][c/128], ceil(rows/128) x k/128
+ * fp32), or 128 columns of one token (xscale[t][c/128], n x k/128 fp32).
+ * Rule: scale = max|v| / 448 in fp32; code = e4m3(clamp(v / scale, +-448)),
+ * round to nearest even, both divisions IEEE fp32; a zero scale gives code 0.
+ * k must be a multiple of 128 (QBLK_ERR_SHAPE), a matrix at most 2^26 rows.
+ *
+ * The products: Y[t,r] = sum_g xscale[t,g] wscale[r/128,g] *
+ * (sum over the 128 columns of g of code * code), Y n x m row-major of type
+ * yt in {F32, F16, BF16}, one rounding at the end.  Sums over groups are fp32
+ * in a fixed order, so equal inputs give bitwise equal outputs.  Up to 64
+ * tokens the sum inside a group is fp32 too.  Beyond, it is formed by the fp8
+ * matrix instructions, which keep a group's sum to about 2^-17 of
+ * sum|code * code| (2^-13 where the codes of one group differ by many orders
+ * of magnitude).
+ *
+ * Workspaces (also of the calls below) are device memory owned by the caller,
+ * 16-byte aligned, of at least the bytes that the call's _workspace function
+ * gives (0: none needed, NULL is fine; it also gives 0 for sizes the call
+ * rejects).  They hold no state between calls and may be shared by calls on
+ * the same stream. */
+
+/* Quantize w (rows x k, type wt in {F32, F16, BF16}). */
+qblk_status_t qblk_quantize_f8(const void* w, qblk_dtype_t wt, int64_t rows,
+                               int64_t k, uint8_t* codes, float* scale,
+                               qblk_stream_t stream);
+
+/* Quantize the n rows (tokens) of x (n x k, type xt). */
+qblk_status_t qblk_quantize_act_f8(const void* x, qblk_dtype_t xt, int64_t n,
+                                   int64_t k, uint8_t* xq, float* scale,
+                                   qblk_stream_t stream);
+
+/* Y = X W^T with W (m x k) and X (n x k) given as codes and scales (several
+ * products of one X then share its quantization). */
+size_t qblk_gemm_f8_workspace(int64_t m, int64_t k, int64_t n);
+qblk_status_t qblk_gemm_f8(const uint8_t* w, const float* wscale, int64_t m,
+                           int64_t k, const uint8_t* xq, const float* xscale,
+                           int64_t n, void* y, qblk_dtype_t yt,
+                           void* workspace, size_t workspace_bytes,
+                           qblk_stream_t stream);
+
+/* The same with X given as values of type xt, quantized by the call by the
+ * rule of qblk_quantize_act_f8. */
+size_t qblk_linear_f8_workspace(int64_t m, int64_t k, int64_t n);
+qblk_status_t qblk_linear_f8(const uint8_t* w, const float* wscale, int64_t m,
+                             int64_t k, const void* x, qblk_dtype_t xt,
+                             int64_t n, void* y, qblk_dtype_t yt,
+                             void* workspace, size_t workspace_bytes,
+                             qblk_stream_t stream);
+
+/* A gated feed-forward layer: H = silu(Wg X) * (Wu X) in fp32, Y = W2 H, with X
+ * and H quantized per token and 128 columns.  w13 is (2*inter) x hidden, the
+ * inter rows of Wg before those of Wu; w2 is hidden x inter; hidden and inter
+ * are multiples of 128; X and Y are n x hidden.  silu(v) = v / (1 + exp(-v)). */
+size_t qblk_ffn_f8_workspace(int64_t hidden, int64_t inter, int64_t n);
+qblk_status_t qblk_ffn_f8(const uint8_t* w13, const float* s13,
+                          const uint8_t* w2, const float* s2, int64_t hidden,
+                          int64_t inter, const void* x, qblk_dtype_t xt,
+                          int64_t n, void* y, qblk_dtype_t yt,
+                          void* workspace, size_t workspace_bytes,
+                          qblk_stream_t stream);
+
+/* A mixture-of-experts layer for a few tokens, out of packed 4-bit experts:
+ *
+ *   Y[t] = sum_j weights[t,j] * D_e (silu(G_e X[t]) * (U_e X[t])),  e = ids[t,j]
+ *
+ * gate_up holds experts x (2*inter) rows of hidden weights (per expert the
+ * inter rows of G before those of U), down experts x hidden rows of inter
+ * weights, both packed in fmt (QBLK_Q4_0, QBLK_SB4, QBLK_SB4_AFFINE or
+ * QBLK_Q4_K; hidden and inter multiples of its block).  X is n x hidden of
+ * type xt in {F16, BF16}, Y n x hidden of type yt.
+ *
+ * Routing.  With logits (n x experts fp32) the call chooses each token's
+ * top_k experts itself, in descending order of the logit, equal logits in
+ * order of the expert, and writes ids (n x top_k) and weights: the softmax of
+ * the logits over the chosen experts (renorm != 0) or over all of them
+ * (renorm = 0), times weight_scale.  A logit of -infinity or NaN takes its
+ * expert out; where fewer than top_k are left the remaining ids are -1 with
+ * weight 0, and a token with none gets Y = 0.  (+infinity counts as the
+ * largest finite value.)  With logits = NULL, ids and weights are inputs from
+ * a router of the caller's; ids outside [0, experts) contribute nothing.
+ *
+ * Products are formed from the exact codes and 16-bit activations, sums are
+ * fp32, the intermediate keeps 16 mantissa bits; the order of the sums is fixed,
+ * so equal inputs give bitwise equal outputs.  Each token depends on its own
+ * row of X and its own experts only.  experts <= 512, top_k <= 32.  Tokens
+ * beyond 1024/top_k run as further launches; from some hundred tokens on,
+ * one matrix product per expert is the better tool.  ids, weights and Y are
+ * written when n and hidden are positive (for inter = 0 only Y, as zeros). */
+typedef struct {
+  int fmt; /* a qblk_format_t; plain ints, so that any value can be refused */
+  int64_t n, hidden, inter;
+  int experts, top_k;
+  const void* x;
+  int xt; /* a qblk_dtype_t */
+  const float* logits; /* or NULL */
+  int renorm;
+  float weight_scale;
+  const void* gate_up;
+  const void* down;
+  int32_t* ids;   /* n x top_k: written with logits, else read */
+  float* weights; /* n x top_k: likewise */
+  void* y;
+  int yt; /* a qblk_dtype_t */
+  void* workspace;
+  size_t workspace_bytes;
+} qblk_moe_t;
+
+size_t qblk_moe_workspace(const qblk_moe_t* args); /* reads the sizes and fmt only */
+qblk_status_t qblk_moe(const qblk_moe_t* args, qblk_stream_t stream);
 
 /* Static English text for a status code (never NULL). */
 const char* qblk_status_string(qblk_status_t st);
