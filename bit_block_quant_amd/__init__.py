@@ -498,11 +498,11 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
     _need(gate_up, "gate_up", (torch.uint8,), min_numel=_packed(fmt, experts * 2 * inter, hidden), device=dev)
     _need(down, "down", (torch.uint8,), min_numel=_packed(fmt, experts * hidden, inter), device=dev)
     out = _out(out, (n, hidden), dtype or x.dtype, dev)
-    a = _Moe(fmt, n, hidden, inter, experts, top_k, _ptr(x).value, _DT[x.dtype], _ptr(logits).value, int(renorm),
-             weight_scale, _ptr(gate_up).value, _ptr(down).value, _ptr(ids).value, _ptr(weights).value,
-             _ptr(out).value, _dtype(out))
+    a = _Moe(fmt, n, hidden, inter, experts, top_k)  # the sizes decide the workspace
     work = _workspace(workspace, _lib.qblk_moe_workspace(C.byref(a)), dev)
-    a.workspace, a.workspace_bytes = _ptr(work).value, _nbytes(work)
+    a.x, a.xt, a.logits, a.renorm, a.weight_scale = _ptr(x), _DT[x.dtype], _ptr(logits), int(renorm), weight_scale
+    a.gate_up, a.down, a.ids, a.weights = _ptr(gate_up), _ptr(down), _ptr(ids), _ptr(weights)
+    a.y, a.yt, a.workspace, a.workspace_bytes = _ptr(out), _dtype(out), _ptr(work), _nbytes(work)
     _need_current(dev)
     _check(_lib.qblk_moe(C.byref(a), _stream(stream)), "qblk_moe")
     return out, ids, weights
