@@ -141,29 +141,6 @@ __global__ __launch_bounds__(256) void k_quant_act_f8(const void* __restrict__ x
   }
 }
 
-// h = silu(gate) * up of the fp32 rows [gate | up] (2i each), quantized likewise.
-__global__ __launch_bounds__(256) void k_silu_quant_f8(const float* __restrict__ gu, int64_t group0, int64_t groups,
-                                                       int i, uint8_t* __restrict__ hq, float* __restrict__ scale) {
-  int64_t g = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-  const bool on = g < groups;
-  g = group0 + (on ? g : groups - 1);
-  const int l = threadIdx.x & 15;
-  const int per = i / kGroup;
-  const int64_t t = g / per;
-  const int64_t at = t * 2 * i + (g - t * per) * kGroup + 8 * l;
-  float a[8], b[8], v[8];
-  load8<QBLK_F32>(gu, at, a);
-  load8<QBLK_F32>(gu, at + i, b);
-#pragma unroll
-  for (int j = 0; j < 8; j++) v[j] = silu_mul(a[j], b[j]);
-  uint32_t code[2];
-  const float s = quant_group(v, code);
-  if (on) {
-    *reinterpret_cast<u32x2*>(hq + g * kGroup + 8 * l) = u32x2{code[0], code[1]};
-    if (l == 0) scale[g] = s;
-  }
-}
-
 // ---------------------------------------------------------- weight codes
 // One workgroup per 128 x 128 block; a thread holds 64 of its values in
 // registers between the maximum and the codes, so the block is read once.
@@ -380,6 +357,246 @@ __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restri
   }
 }
 
+// ------------------------------------------------------------ many tokens
+// Bound by the fp8 matrix cores.  A workgroup of 8 waves owns 256 rows x 64 NT
+// tokens; a group of 128 columns is one stage in LDS (32 KB + 8 NT KB, two
+// stages) and one K=128 matrix instruction per 16 x 16 tile, whose result is
+// scaled by sx[t,g] * sw[r,g] into the fp32 accumulators: four multiply-adds
+// per lane beside 32 matrix-core cycles.  Waves are 2 (rows) x 4 (tokens);
+// wave row a holds rows 64a..64a+63 of the tile's first and second 128-row
+// halves, so that for GATE, where the halves are 128 gate rows and their 128
+// up rows, a lane holds both factors of silu(gate) * up.
+//
+// LDS layout: 128 bytes per row, the row's 16-byte chunk c at c ^ (row & 7),
+// so that the 16 rows of an operand read hit 8 different chunk columns.  The
+// stages are filled by loads straight to LDS, which write 64 x 16 consecutive
+// bytes: the exchange of chunks is made on the global address.
+typedef int int8v __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void glob_void;
+
+constexpr int kTileRows = 256;
+
+template <int NT>
+struct Stage {
+  uint8_t a[kTileRows * kGroup];
+  uint8_t b[64 * NT * kGroup];
+};
+
+__device__ __forceinline__ int8v frag(const uint8_t* base, int row, int q) {
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * kGroup + (((2 * q) ^ (row & 7)) << 4));
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(base + row * kGroup + (((2 * q + 1) ^ (row & 7)) << 4));
+  return int8v{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
+               static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
+}
+
+struct TileArgs {
+  const uint8_t* w;
+  const float* ws;
+  const uint8_t* xq;
+  const float* xs;
+  void* y;        // n x m (GATE: codes of h, n x up)
+  float* hs;      // GATE: scales of h
+  float* part;    // split K: partial sums, [split][n][m]
+  int m, k, n, yt, up, row_tiles, tok_tiles, groups_per_split;
+};
+
+template <int NT, bool GATE, bool SPLIT>
+__global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  Stage<NT>* const st = reinterpret_cast<Stage<NT>*>(lds);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int G = p.k / kGroup;
+
+  // Workgroups go to the 8 XCDs in turn; each XCD takes a run of consecutive
+  // tiles (token tiles fastest), so that its L2 holds the few row tiles and
+  // the token tiles that its 32 CUs work on together.
+  const int tiles = p.row_tiles * p.tok_tiles;
+  const int b = blockIdx.x, xcd = b & 7;
+  const int tile = xcd * (tiles >> 3) + (xcd < (tiles & 7) ? xcd : (tiles & 7)) + (b >> 3);
+  const int rt = tile / p.tok_tiles, tt = tile - rt * p.tok_tiles;
+  const int row0 = rt * (GATE ? 128 : kTileRows), t0 = tt * 64 * NT;
+  const int g0 = SPLIT ? blockIdx.y * p.groups_per_split : 0;
+  const int g1 = SPLIT ? (g0 + p.groups_per_split < G ? g0 + p.groups_per_split : G) : G;
+
+  // what this lane copies: 16-byte chunks of 4 rows of A and NT of B per stage
+  const uint8_t* ap[4];
+  const uint8_t* bp[NT];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int row = 64 * i + 8 * wave + (lane >> 3);
+    int64_t at = GATE ? (row < 128 ? row0 + row : static_cast<int64_t>(p.up) + row0 + row - 128) : row0 + row;
+    if (at > p.m - 1) at = p.m - 1;
+    ap[i] = p.w + at * p.k + (((lane & 7) ^ (row & 7)) << 4);
+  }
+#pragma unroll
+  for (int i = 0; i < NT; i++) {
+    const int row = 64 * i + 8 * wave + (lane >> 3);
+    const int64_t at = t0 + row < p.n ? t0 + row : p.n - 1;
+    bp[i] = p.xq + at * p.k + (((lane & 7) ^ (row & 7)) << 4);
+  }
+  auto copy = [&](Stage<NT>& s, int g) {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      __builtin_amdgcn_global_load_lds((glob_void*)(ap[i] + static_cast<int64_t>(g) * kGroup),
+                                       (lds_void*)(s.a + (64 * i + 8 * wave) * kGroup), 16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+      __builtin_amdgcn_global_load_lds((glob_void*)(bp[i] + static_cast<int64_t>(g) * kGroup),
+                                       (lds_void*)(s.b + (64 * i + 8 * wave) * kGroup), 16, 0, 0);
+  };
+
+  const int wm = wave & 1, wn = wave >> 1;
+  const float* sxp[NT];
+#pragma unroll
+  for (int j = 0; j < NT; j++) {
+    const int tok = t0 + (wn * NT + j) * 16 + r;
+    sxp[j] = p.xs + static_cast<int64_t>(tok < p.n ? tok : p.n - 1) * G;
+  }
+  const float* swp[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    int64_t row = GATE ? row0 + static_cast<int64_t>(h) * p.up : row0 + 128 * h;
+    if (row > p.m - 1) row = p.m - 1;
+    swp[h] = p.ws + row / kGroup * G;
+  }
+
+  float4_t acc[8][NT];
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+#pragma unroll
+    for (int j = 0; j < NT; j++) acc[i][j] = float4_t{0, 0, 0, 0};
+
+  float sx[NT], sw[2];
+  copy(st[0], g0);
+#pragma unroll
+  for (int j = 0; j < NT; j++) sx[j] = sxp[j][g0];
+  sw[0] = swp[0][g0];
+  sw[1] = swp[1][g0];
+  for (int g = g0; g < g1; g++) {
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);  // the next scales are loaded behind the barrier, which waits for loads
+    const int gn = g + 1 < g1 ? g + 1 : g;
+    Stage<NT>& cur = st[(g - g0) & 1];
+    if (g + 1 < g1) copy(st[(g - g0 + 1) & 1], gn);
+    float sxn[NT], swn[2];
+#pragma unroll
+    for (int j = 0; j < NT; j++) sxn[j] = sxp[j][gn];
+    swn[0] = swp[0][gn];
+    swn[1] = swp[1][gn];
+    int8v bf[NT];
+#pragma unroll
+    for (int j = 0; j < NT; j++) bf[j] = frag(cur.b, (wn * NT + j) * 16 + r, q);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int8v af = frag(cur.a, (i >> 2) * 128 + wm * 64 + (i & 3) * 16 + r, q);
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        float4_t c = {0, 0, 0, 0};
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf[j], c, 0, 0, 0, 0, 0, 0);
+        const float s = sx[j] * sw[i >> 2];
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(c[e], s, acc[i][j][e]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; j++) sx[j] = sxn[j];
+    sw[0] = swn[0];
+    sw[1] = swn[1];
+  }
+
+  if constexpr (GATE) {
+    // h = silu(gate) * up; a group of 128 columns is the tile's rows: its
+    // maximum over this lane's 16, the four quarters and the two wave rows
+    float top[NT];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      float a = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          acc[i][j][e] = silu_mul(acc[i][j][e], acc[i + 4][j][e]);
+          a = __builtin_fmaxf(a, __builtin_fabsf(acc[i][j][e]));
+        }
+      a = __builtin_fmaxf(a, __shfl_xor(a, 16, kWave));
+      top[j] = __builtin_fmaxf(a, __shfl_xor(a, 32, kWave));
+    }
+    float* m2 = reinterpret_cast<float*>(lds);  // [2][64 NT]
+    __syncthreads();
+    if (q == 0) {
+#pragma unroll
+      for (int j = 0; j < NT; j++) m2[wm * 64 * NT + (wn * NT + j) * 16 + r] = top[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const int in = (wn * NT + j) * 16 + r, tok = t0 + in;
+      const float s = __builtin_fmaxf(m2[in], m2[64 * NT + in]) / kF8Max;
+      float v[16];
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[4 * i + e] = acc[i][j][e];
+      codes_f8<16>(v, s, c);
+      if (tok < p.n) {
+        uint8_t* out = static_cast<uint8_t*>(p.y) + static_cast<int64_t>(tok) * p.up + row0 + wm * 64 + 4 * q;
+#pragma unroll
+        for (int i = 0; i < 4; i++) *reinterpret_cast<uint32_t*>(out + 16 * i) = c[i];
+        if (wm == 0 && q == 0) p.hs[static_cast<int64_t>(tok) * (p.up / kGroup) + row0 / kGroup] = s;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const int tok = t0 + (wn * NT + j) * 16 + r;
+      if (tok >= p.n) continue;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const int row = row0 + (i >> 2) * 128 + wm * 64 + (i & 3) * 16 + 4 * q;
+        if (row >= p.m) continue;
+        const int64_t at = static_cast<int64_t>(tok) * p.m + row;
+        const bool whole = row + 4 <= p.m && (p.m & 3) == 0;  // 4 consecutive values, aligned
+        if (SPLIT || p.yt == QBLK_F32) {
+          float* y = SPLIT ? p.part + static_cast<int64_t>(blockIdx.y) * p.n * p.m : static_cast<float*>(p.y);
+          if (whole) {
+            *reinterpret_cast<float4_t*>(y + at) = acc[i][j];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              if (row + e < p.m) y[at + e] = acc[i][j][e];
+          }
+        } else {
+          uint16_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) h[e] = p.yt == QBLK_F16 ? f32_to_f16_bits(acc[i][j][e]) : f32_to_bf16_bits(acc[i][j][e]);
+          uint16_t* y = static_cast<uint16_t*>(p.y) + at;
+          if (whole) {
+            *reinterpret_cast<u32x2*>(y) = u32x2{h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16)};
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              if (row + e < p.m) y[e] = h[e];
+          }
+        }
+      }
+    }
+  }
+}
+
+// y = the sum of the splits' partial products, in their order
+__global__ __launch_bounds__(256) void k_f8_join(const float* __restrict__ part, int64_t first, int64_t count,
+                                                 int64_t stride, int splits, void* __restrict__ y, int yt) {
+  int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= count) return;
+  i += first;
+  float v = 0.0f;
+  for (int s = 0; s < splits; s++) v += part[s * stride + i];
+  store_y(y, i, v, yt);
+}
+
 // LDS of k_f8_few: the waves' partial sums, or the quantized x before them
 constexpr int kFewWaves = 8;
 size_t few_lds(int T, int NR, bool codes, int n, int k) {
@@ -422,6 +639,77 @@ hipError_t few_values(const uint8_t* w, const float* ws, int64_t m, int64_t k, c
     default: return few<1, NR, GATE, QBLK_BF16>(w, ws, m, k, x, nullptr, n, y, yt, up_row, s);
   }
 }
+
+// The tile kernel's shape for a product: tokens per tile and splits of K.
+struct Plan {
+  int nt, splits, per;  // 64 nt tokens; groups per split
+};
+
+Plan tile_plan(int64_t m, int64_t k, int64_t n, bool gate) {
+  Plan best{4, 1, static_cast<int>(k / kGroup)};
+  const int64_t rt = (m + kTileRows - 1) / kTileRows, G = k / kGroup;
+  const int cus = cu_count();
+  double cost = 1e30;
+  for (int nt = 1; nt <= 4; nt *= 2) {
+    const int64_t tiles = rt * ((n + 64 * nt - 1) / (64 * nt));
+    for (int sp = 1; sp <= 8; sp *= 2) {
+      if (sp > 1 && (gate || G / sp < 4)) break;
+      const int64_t per = (G + sp - 1) / sp;
+      const int64_t rounds = (tiles * sp + cus - 1) / cus;
+      // us: a stage of a tile (matrix cores, or the copies where nt is small), a tile's start and end, the partial sums
+      const double stage = nt == 4 ? 1.2 : nt == 2 ? 0.75 : 0.55;
+      const double c = rounds * (per * stage + 4.0) + (sp > 1 ? 3.0 + 2.0 * sp * n * m * 4 / 4.0e6 : 0.0);
+      if (c < cost) {
+        cost = c;
+        best = Plan{nt, sp, static_cast<int>(per)};
+      }
+    }
+  }
+  best.splits = static_cast<int>((G + best.per - 1) / best.per);
+  return best;
+}
+
+template <int NT, bool GATE, bool SPLIT>
+hipError_t tile_go(const TileArgs& a, int splits, hipStream_t s) {
+  constexpr size_t lds = 2 * sizeof(Stage<NT>);
+  static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(k_f8_tile<NT, GATE, SPLIT>),
+                                                        hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (allowed != hipSuccess) return allowed;
+  k_f8_tile<NT, GATE, SPLIT><<<dim3(static_cast<unsigned>(a.row_tiles * a.tok_tiles), static_cast<unsigned>(splits)), 512,
+                              lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool GATE, bool SPLIT>
+hipError_t tile_nt(int nt, const TileArgs& a, int splits, hipStream_t s) {
+  switch (nt) {
+    case 1: return tile_go<1, GATE, SPLIT>(a, splits, s);
+    case 2: return tile_go<2, GATE, SPLIT>(a, splits, s);
+    default: return tile_go<4, GATE, SPLIT>(a, splits, s);
+  }
+}
+
+// Y (or, for `up` > 0, the codes and scales of H) by the tile kernel
+hipError_t tile_product(const uint8_t* w, const float* ws, int64_t m, int64_t k, const uint8_t* xq, const float* xs,
+                        int64_t n, void* y, int yt, int64_t up, float* hs, void* work, hipStream_t s) {
+  const Plan plan = tile_plan(m, k, n, up > 0);
+  TileArgs a{w, ws, xq, xs, y, hs, static_cast<float*>(work), static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt,
+             static_cast<int>(up), static_cast<int>((m + kTileRows - 1) / kTileRows),
+             static_cast<int>((n + 64 * plan.nt - 1) / (64 * plan.nt)), plan.per};
+  log_launch("f8 tile%s m=%lld k=%lld n=%lld tokens=%d splits=%d", up > 0 ? " gate" : "", (long long)m, (long long)k,
+             (long long)n, 64 * plan.nt, plan.splits);
+  if (up > 0) return tile_nt<true, false>(plan.nt, a, 1, s);
+  if (plan.splits == 1) return tile_nt<false, false>(plan.nt, a, 1, s);
+  const hipError_t e = tile_nt<false, true>(plan.nt, a, plan.splits, s);
+  if (e != hipSuccess) return e;
+  return in_pieces(m * n, 256, 256, [&](int64_t first, int64_t c) {
+    k_f8_join<<<dim3(static_cast<unsigned>((c + 255) / 256)), 256, 0, s>>>(a.part, first, c, m * n, plan.splits, y, yt);
+    return hipGetLastError();
+  });
+}
+
+// Products up to this many tokens run k_f8_few.
+constexpr int64_t kFewTokens = 64;
 
 // Whether a product quantizes its x inside every workgroup.
 bool fused_quant(int64_t n, int64_t k) { return n <= 4 && n * k <= 32768; }
@@ -474,11 +762,16 @@ hipError_t launch_zero_bytes(void* y, int64_t bytes, hipStream_t s) {
   });
 }
 
-int64_t gemm_f8_workspace(int64_t, int64_t, int64_t) { return 0; }
+int64_t gemm_f8_workspace(int64_t m, int64_t k, int64_t n) {
+  if (n <= kFewTokens) return 0;
+  const Plan p = tile_plan(m, k, n, false);
+  return p.splits > 1 ? align256(p.splits * n * m * 4) : 0;
+}
 
 hipError_t launch_gemm_f8(const uint8_t* w, const float* ws, int64_t m, int64_t k, const uint8_t* xq,
-                          const float* xs, int64_t n, void* y, int yt, void*, hipStream_t s) {
-  return few_codes<false>(w, ws, m, k, xq, xs, n, y, yt, 0, s);
+                          const float* xs, int64_t n, void* y, int yt, void* work, hipStream_t s) {
+  if (n <= kFewTokens) return few_codes<false>(w, ws, m, k, xq, xs, n, y, yt, 0, s);
+  return tile_product(w, ws, m, k, xq, xs, n, y, yt, 0, nullptr, work, s);
 }
 
 int64_t linear_f8_workspace(int64_t m, int64_t k, int64_t n) {
@@ -496,8 +789,10 @@ hipError_t launch_linear_f8(const uint8_t* w, const float* ws, int64_t m, int64_
   return launch_gemm_f8(w, ws, m, k, xq, xs, n, y, yt, xq + code_bytes(n, k), s);
 }
 
-// ffn workspace: h in fp32, then what its two products need, one after the other
+// ffn workspace: few tokens: h in fp32, then what its two products need, one
+// after the other; else the codes of x, those of h, and the second product's
 int64_t ffn_f8_workspace(int64_t h, int64_t i, int64_t n) {
+  if (n > kFewTokens) return code_bytes(n, h) + code_bytes(n, i) + gemm_f8_workspace(h, i, n);
   const int64_t up = fused_quant(n, h) ? 0 : code_bytes(n, h);
   const int64_t down = linear_f8_workspace(h, i, n);
   return align256(n * i * 4) + (up > down ? up : down);
@@ -505,9 +800,19 @@ int64_t ffn_f8_workspace(int64_t h, int64_t i, int64_t n) {
 
 hipError_t launch_ffn_f8(const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2, int64_t h,
                          int64_t i, const void* x, int xt, int64_t n, void* y, int yt, void* work, hipStream_t s) {
+  hipError_t e;
+  if (n > kFewTokens) {
+    uint8_t* xq = static_cast<uint8_t*>(work);
+    float* xs = reinterpret_cast<float*>(xq + align256(n * h));
+    uint8_t* hq = xq + code_bytes(n, h);
+    float* hs = reinterpret_cast<float*>(hq + align256(n * i));
+    e = launch_quantize_act_f8(x, xt, n, h, xq, xs, s);
+    if (e == hipSuccess) e = tile_product(w13, s13, 2 * i, h, xq, xs, n, hq, 0, i, hs, nullptr, s);
+    if (e != hipSuccess) return e;
+    return launch_gemm_f8(w2, s2, h, i, hq, hs, n, y, yt, hq + code_bytes(n, i), s);
+  }
   float* mid = static_cast<float*>(work);
   uint8_t* rest = static_cast<uint8_t*>(work) + align256(n * i * 4);
-  hipError_t e;
   if (fused_quant(n, h)) {
     e = few_values<true>(w13, s13, 2 * i, h, x, xt, n, mid, QBLK_F32, i, s);
   } else {
