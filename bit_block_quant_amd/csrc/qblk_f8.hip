@@ -485,21 +485,43 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
     for (int j = 0; j < NT; j++) sxn[j] = sxp[j][gn];
     swn[0] = swp[0][gn];
     swn[1] = swp[1][gn];
-    int8v bf[NT];
+    // Software pipeline over the 8 row tiles: while the matrix cores work on
+    // tile i, its successor's operand is read and tile i - 1 is scaled.
+    float sc[2][NT];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      sc[0][j] = sx[j] * sw[0];
+      sc[1][j] = sx[j] * sw[1];
+    }
+    int8v bf[NT], af[2];
+    float4_t c[2][NT];
+    auto arow = [&](int i) { return (i >> 2) * 128 + wm * 64 + (i & 3) * 16 + r; };
+    auto scale = [&](int i, int j) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(c[i & 1][j][e], sc[i >> 2][j], acc[i][j][e]);
+    };
+    af[0] = frag(cur.a, arow(0), q);
 #pragma unroll
     for (int j = 0; j < NT; j++) bf[j] = frag(cur.b, (wn * NT + j) * 16 + r, q);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const int8v af = frag(cur.a, (i >> 2) * 128 + wm * 64 + (i & 3) * 16 + r, q);
+      if (i + 1 < 8) af[(i + 1) & 1] = frag(cur.a, arow(i + 1), q);
 #pragma unroll
       for (int j = 0; j < NT; j++) {
-        float4_t c = {0, 0, 0, 0};
-        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf[j], c, 0, 0, 0, 0, 0, 0);
-        const float s = sx[j] * sw[i >> 2];
-#pragma unroll
-        for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(c[e], s, acc[i][j][e]);
+        c[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i & 1], bf[j], float4_t{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+        if (i > 0) scale(i - 1, j);
       }
+      // two LDS reads, then each matrix instruction with the four multiply-adds of a finished tile behind it
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int j = 0; j < NT; j++) scale(7, j);
 #pragma unroll
     for (int j = 0; j < NT; j++) sx[j] = sxn[j];
     sw[0] = swn[0];
