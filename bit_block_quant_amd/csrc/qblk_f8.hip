@@ -382,10 +382,23 @@ struct Stage {
   uint8_t a[kTileRows * kGroup];
   uint8_t b[64 * NT * kGroup];
 };
+// sx * sw of 4 groups, for the two row halves and every token
+template <int NT>
+struct Scales {
+  float s[2][4][64 * NT];
+};
+template <int NT>
+struct TileLds {
+  Stage<NT> st[2];
+  Scales<NT> sc[2];
+};
 
+// Operand of a K=128 matrix instruction: lane (row r, quarter q) gives the
+// row's chunks q and q + 4 (both operands in the same order).
 __device__ __forceinline__ int8v frag(const uint8_t* base, int row, int q) {
-  const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * kGroup + (((2 * q) ^ (row & 7)) << 4));
-  const u32x4 hi = *reinterpret_cast<const u32x4*>(base + row * kGroup + (((2 * q + 1) ^ (row & 7)) << 4));
+  const int key = (row >> 1) & 7;
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * kGroup + ((q ^ key) << 4));
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(base + row * kGroup + (((q + 4) ^ key) << 4));
   return int8v{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
                static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
 }
@@ -404,7 +417,8 @@ struct TileArgs {
 template <int NT, bool GATE, bool SPLIT>
 __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
   extern __shared__ __align__(16) uint8_t lds[];
-  Stage<NT>* const st = reinterpret_cast<Stage<NT>*>(lds);
+  Stage<NT>* const st = reinterpret_cast<TileLds<NT>*>(lds)->st;
+  Scales<NT>* const scl = reinterpret_cast<TileLds<NT>*>(lds)->sc;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int G = p.k / kGroup;
@@ -415,45 +429,49 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
   const int tiles = p.row_tiles * p.tok_tiles;
   const int b = blockIdx.x, xcd = b & 7;
   const int tile = xcd * (tiles >> 3) + (xcd < (tiles & 7) ? xcd : (tiles & 7)) + (b >> 3);
-  const int rt = tile / p.tok_tiles, tt = tile - rt * p.tok_tiles;
+  const int band = tile / (8 * p.row_tiles), in_band = tile - band * 8 * p.row_tiles;
+  const int wide = p.tok_tiles - 8 * band < 8 ? p.tok_tiles - 8 * band : 8;
+  const int rt = in_band / wide, tt = 8 * band + in_band - rt * wide;
   const int row0 = rt * (GATE ? 128 : kTileRows), t0 = tt * 64 * NT;
   const int g0 = SPLIT ? blockIdx.y * p.groups_per_split : 0;
   const int g1 = SPLIT ? (g0 + p.groups_per_split < G ? g0 + p.groups_per_split : G) : G;
 
-  // what this lane copies: 16-byte chunks of 4 rows of A and NT of B per stage
-  const uint8_t* ap[4];
-  const uint8_t* bp[NT];
+  // What this lane copies per stage: a 16-byte chunk of 4 rows of A and NT of
+  // B, as 32-bit offsets from the tile's first row (of the up half for GATE).
+  // Rows past the matrix repeat its last one; their results are not stored.
+  const int64_t second = GATE ? static_cast<int64_t>(p.up) + row0 : row0;
+  const uint8_t* abase[2] = {p.w + static_cast<int64_t>(row0) * p.k, p.w + second * p.k};
+  const uint8_t* bbase = p.xq + static_cast<int64_t>(t0) * p.k;
+  uint32_t ao[4], bo[NT];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const int row = 64 * i + 8 * wave + (lane >> 3);
-    int64_t at = GATE ? (row < 128 ? row0 + row : static_cast<int64_t>(p.up) + row0 + row - 128) : row0 + row;
-    if (at > p.m - 1) at = p.m - 1;
-    ap[i] = p.w + at * p.k + (((lane & 7) ^ (row & 7)) << 4);
+    int at = GATE ? row & 127 : row;
+    if (!GATE && at > p.m - 1 - row0) at = p.m - 1 - row0;
+    ao[i] = static_cast<uint32_t>(at) * static_cast<uint32_t>(p.k) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
   }
 #pragma unroll
   for (int i = 0; i < NT; i++) {
     const int row = 64 * i + 8 * wave + (lane >> 3);
-    const int64_t at = t0 + row < p.n ? t0 + row : p.n - 1;
-    bp[i] = p.xq + at * p.k + (((lane & 7) ^ (row & 7)) << 4);
+    const int at = t0 + row < p.n ? row : p.n - 1 - t0;
+    bo[i] = static_cast<uint32_t>(at) * static_cast<uint32_t>(p.k) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
   }
-  auto copy = [&](Stage<NT>& s, int g) {
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-      __builtin_amdgcn_global_load_lds((glob_void*)(ap[i] + static_cast<int64_t>(g) * kGroup),
+  // chunk i of 4 + NT: the rows of A, then those of B
+  auto copy = [&](Stage<NT>& s, int g, int i) {
+    const int64_t at = static_cast<int64_t>(g) * kGroup;
+    if (i < 4)
+      __builtin_amdgcn_global_load_lds((glob_void*)((i < 2 ? abase[0] : abase[1]) + at + ao[i & 3]),
                                        (lds_void*)(s.a + (64 * i + 8 * wave) * kGroup), 16, 0, 0);
-#pragma unroll
-    for (int i = 0; i < NT; i++)
-      __builtin_amdgcn_global_load_lds((glob_void*)(bp[i] + static_cast<int64_t>(g) * kGroup),
-                                       (lds_void*)(s.b + (64 * i + 8 * wave) * kGroup), 16, 0, 0);
+    else if (i < 4 + NT)
+      __builtin_amdgcn_global_load_lds((glob_void*)(bbase + at + bo[i - 4]),
+                                       (lds_void*)(s.b + (64 * (i - 4) + 8 * wave) * kGroup), 16, 0, 0);
   };
 
   const int wm = wave & 1, wn = wave >> 1;
-  const float* sxp[NT];
-#pragma unroll
-  for (int j = 0; j < NT; j++) {
-    const int tok = t0 + (wn * NT + j) * 16 + r;
-    sxp[j] = p.xs + static_cast<int64_t>(tok < p.n ? tok : p.n - 1) * G;
-  }
+  // Scales, 4 groups at a time: a thread takes the tokens and groups
+  // threadIdx.x + 512 u of [token][4], loads early in one run of 4 stages and
+  // leaves the products with both row halves' scales in LDS for the next.
+  constexpr int kPer = (NT + 1) / 2;
   const float* swp[2];
 #pragma unroll
   for (int h = 0; h < 2; h++) {
@@ -461,6 +479,26 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
     if (row > p.m - 1) row = p.m - 1;
     swp[h] = p.ws + row / kGroup * G;
   }
+  float xv[kPer], wv[2];
+  auto scales_load = [&](int g) {
+    const int gg = g + (threadIdx.x & 3) < g1 ? g + (threadIdx.x & 3) : g1 - 1;
+#pragma unroll
+    for (int u = 0; u < kPer; u++) {
+      int tok = t0 + (((threadIdx.x + 512 * u) >> 2) & (64 * NT - 1));
+      if (tok > p.n - 1) tok = p.n - 1;
+      xv[u] = p.xs[static_cast<int64_t>(tok) * G + gg];
+    }
+    wv[0] = swp[0][gg];
+    wv[1] = swp[1][gg];
+  };
+  auto scales_store = [&](Scales<NT>& s) {
+#pragma unroll
+    for (int u = 0; u < kPer; u++) {
+      const int tok = ((threadIdx.x + 512 * u) >> 2) & (64 * NT - 1);  // 64 tokens: both halves of the threads write the same
+      s.s[0][threadIdx.x & 3][tok] = xv[u] * wv[0];
+      s.s[1][threadIdx.x & 3][tok] = xv[u] * wv[1];
+    }
+  };
 
   float4_t acc[8][NT];
 #pragma unroll
@@ -468,65 +506,90 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
 #pragma unroll
     for (int j = 0; j < NT; j++) acc[i][j] = float4_t{0, 0, 0, 0};
 
-  float sx[NT], sw[2];
-  copy(st[0], g0);
+  // Software pipeline.  Within a stage: while the matrix cores work on row
+  // tile i, its successor's operand is read from LDS and tile i - 1 is scaled.
+  // Across stages: at the last row tile every operand of the stage is in
+  // registers, so one barrier there frees its buffer for the copies two
+  // stages on and shows the next stage's, whose first operands are read
+  // behind the last matrix instructions.
+  int8v bf[NT], af[2];
+  float4_t c[2][NT];
+  float sc[2][NT];
+  auto arow = [&](int i) { return (i >> 2) * 128 + wm * 64 + (i & 3) * 16 + r; };
+  auto scale = [&](int i, int j) {
 #pragma unroll
-  for (int j = 0; j < NT; j++) sx[j] = sxp[j][g0];
-  sw[0] = swp[0][g0];
-  sw[1] = swp[1][g0];
+    for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(c[i & 1][j][e], sc[i >> 2][j], acc[i][j][e]);
+  };
+  scales_load(g0);
+#pragma unroll
+  for (int i = 0; i < 4 + NT; i++) copy(st[0], g0, i);
+  scales_store(scl[0]);
+  __syncthreads();
+  copy(st[1], g0 + 1 < g1 ? g0 + 1 : g0, 0);
+  copy(st[1], g0 + 1 < g1 ? g0 + 1 : g0, 1);
+  af[0] = frag(st[0].a, arow(0), q);
+#pragma unroll
+  for (int j = 0; j < NT; j++) bf[j] = frag(st[0].b, (wn * NT + j) * 16 + r, q);
   for (int g = g0; g < g1; g++) {
-    __syncthreads();
-    __builtin_amdgcn_sched_barrier(0);  // the next scales are loaded behind the barrier, which waits for loads
-    const int gn = g + 1 < g1 ? g + 1 : g;
-    Stage<NT>& cur = st[(g - g0) & 1];
-    if (g + 1 < g1) copy(st[(g - g0 + 1) & 1], gn);
-    float sxn[NT], swn[2];
-#pragma unroll
-    for (int j = 0; j < NT; j++) sxn[j] = sxp[j][gn];
-    swn[0] = swp[0][gn];
-    swn[1] = swp[1][gn];
-    // Software pipeline over the 8 row tiles: while the matrix cores work on
-    // tile i, its successor's operand is read and tile i - 1 is scaled.
-    float sc[2][NT];
+    const int step = g - g0;
+    Stage<NT>& cur = st[step & 1];
+    Stage<NT>& nxt = st[(step + 1) & 1];
+    const int gn = g + 1 < g1 ? g + 1 : g1 - 1, gc = g + 2 < g1 ? g + 2 : g1 - 1;
 #pragma unroll
     for (int j = 0; j < NT; j++) {
-      sc[0][j] = sx[j] * sw[0];
-      sc[1][j] = sx[j] * sw[1];
+      sc[0][j] = scl[(step >> 2) & 1].s[0][step & 3][(wn * NT + j) * 16 + r];
+      sc[1][j] = scl[(step >> 2) & 1].s[1][step & 3][(wn * NT + j) * 16 + r];
     }
-    int8v bf[NT], af[2];
-    float4_t c[2][NT];
-    auto arow = [&](int i) { return (i >> 2) * 128 + wm * 64 + (i & 3) * 16 + r; };
-    auto scale = [&](int i, int j) {
-#pragma unroll
-      for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(c[i & 1][j][e], sc[i >> 2][j], acc[i][j][e]);
-    };
-    af[0] = frag(cur.a, arow(0), q);
-#pragma unroll
-    for (int j = 0; j < NT; j++) bf[j] = frag(cur.b, (wn * NT + j) * 16 + r, q);
+    if ((step & 3) == 0) scales_load(g + 4 < g1 ? g + 4 : g1 - 1);
+    if ((step & 3) == 2) scales_store(scl[((step >> 2) + 1) & 1]);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      if (i + 1 < 8) af[(i + 1) & 1] = frag(cur.a, arow(i + 1), q);
+      if (i + 1 < 8) {
+        af[(i + 1) & 1] = frag(cur.a, arow(i + 1), q);
+      } else {
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int j = 0; j < NT; j++) {
         c[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i & 1], bf[j], float4_t{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
         if (i > 0) scale(i - 1, j);
+        if (i + 1 == 8) bf[j] = frag(nxt.b, (wn * NT + j) * 16 + r, q);
       }
-      // two LDS reads, then each matrix instruction with the four multiply-adds of a finished tile behind it
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      // Each matrix instruction with the four multiply-adds of a finished tile
+      // behind it; the LDS reads after the first (before it they would be
+      // waited for together with the operand it needs).  The copies are spread
+      // over four row tiles: issued at once they hold up the waves' issue.
+      if (i + 1 < 8) {
+        if (i < 3) {
+          copy(nxt, gn, 2 * i + 2);
+          copy(nxt, gn, 2 * i + 3);
+        }
 #pragma unroll
-      for (int j = 0; j < NT; j++) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        for (int j = 0; j < NT; j++) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if (j == 0) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          if (j < 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+      } else {
+        af[0] = frag(nxt.a, arow(0), q);
+        copy(cur, gc, 0);
+        copy(cur, gc, 1);
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int j = 0; j < NT; j++) scale(7, j);
-#pragma unroll
-    for (int j = 0; j < NT; j++) sx[j] = sxn[j];
-    sw[0] = swn[0];
-    sw[1] = swn[1];
   }
+  __syncthreads();  // the last copies have landed: LDS may be used again, and left
 
   if constexpr (GATE) {
     // h = silu(gate) * up; a group of 128 columns is the tile's rows: its
@@ -693,7 +756,7 @@ Plan tile_plan(int64_t m, int64_t k, int64_t n, bool gate) {
 
 template <int NT, bool GATE, bool SPLIT>
 hipError_t tile_go(const TileArgs& a, int splits, hipStream_t s) {
-  constexpr size_t lds = 2 * sizeof(Stage<NT>);
+  constexpr size_t lds = sizeof(TileLds<NT>);
   static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(k_f8_tile<NT, GATE, SPLIT>),
                                                         hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (allowed != hipSuccess) return allowed;
