@@ -358,11 +358,11 @@ __device__ void build_table(const int* ids, int pairs, int experts, Table& t, in
 // Workgroups are persistent, so the routing is worked out once in each rather
 // than by a launch of its own.
 template <int FMT, bool F16>
-__global__ __launch_bounds__(kUpWaves* kWave) void k_moe_up(MoeArgs a) {
+__global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   __shared__ Table table;
   __shared__ int ids[kMoeMaxPairs];
   __shared__ int cursor[kMoeMaxExperts];
-  __shared__ float4_t red[kUpWaves][2][64];
+  __shared__ float4_t red[2][kUpWaves][2][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int pairs = a.n * a.top_k;
@@ -391,21 +391,33 @@ __global__ __launch_bounds__(kUpWaves* kWave) void k_moe_up(MoeArgs a) {
 
   const int tiles = a.inter / 16, steps = (a.hidden + 255) / 256, units = a.hidden / 32;
   const int64_t tasks = static_cast<int64_t>(table.active) * tiles;
-  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+  const bool busy = wave < steps;
+  const int64_t up_off = static_cast<int64_t>(a.inter) * a.up_row_bytes;
+  auto gate_row = [&](int64_t task) {
     const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
-    const int64_t row = static_cast<int64_t>(table.expert[slot]) * 2 * a.inter + 16 * tile + r;
-    const uint8_t* gate = a.gate_up + row * a.up_row_bytes;
-    const uint8_t* up = gate + static_cast<int64_t>(a.inter) * a.up_row_bytes;
+    return a.gate_up + (static_cast<int64_t>(table.expert[slot]) * 2 * a.inter + 16 * tile + r) * a.up_row_bytes;
+  };
+  int64_t task = blockIdx.x;
+  if (task >= tasks) return;
+  // Every step's weights are loaded while the step before it is multiplied,
+  // across tiles too.
+  const uint8_t* gate = gate_row(task);
+  Step<FMT> g, v;
+  if (busy) {
+    g.load(gate, wave, q, units);
+    v.load(gate + up_off, wave, q, units);
+  }
+  int buf = 0;
+  for (; task < tasks; task += gridDim.x) {
+    const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
     const int first = table.off[slot], count = table.off[slot + 1] - first;
-    for (int c0 = 0; c0 < count; c0 += 16) {
+    const uint8_t* next_gate = task + gridDim.x < tasks ? gate_row(task + gridDim.x) : gate;
+    for (int c0 = 0; c0 < count; c0 += 16, buf ^= 1) {
       const bool live = c0 + r < count;  // the other lanes' rows of the tile are zero
       const int pair = table.list[first + (live ? c0 + r : 0)];
       const uint8_t* x = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(pair / a.top_k) * a.hidden * 2 + 8 * q;
       float4_t ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
       for (int sb = wave; sb < steps; sb += kUpWaves) {
-        Step<FMT> g, v;
-        g.load(gate, sb, q, units);
-        v.load(up, sb, q, units);
         u32x4 xa[8];
 #pragma unroll
         for (int u = 0; u < 8; u++) {
@@ -416,6 +428,12 @@ __global__ __launch_bounds__(kUpWaves* kWave) void k_moe_up(MoeArgs a) {
             xa[u] = u32x4{l0.x, l0.y, l1.x, l1.y};
           }
         }
+        const bool more = sb + kUpWaves < steps;
+        const uint8_t* ng = more || c0 + 16 < count ? gate : next_gate;
+        const int nsb = more ? sb + kUpWaves : wave;
+        Step<FMT> g2, v2;
+        g2.load(ng, nsb, q, units);
+        v2.load(ng + up_off, nsb, q, units);
         g.finish(sb, q, units);
         v.finish(sb, q, units);
 #pragma unroll
@@ -430,10 +448,12 @@ __global__ __launch_bounds__(kUpWaves* kWave) void k_moe_up(MoeArgs a) {
             mul_unit<FMT, F16, 1>(v, 4 * j + u, v.raw[j][u], op, xs, ua);
           }
         }
+        g = g2;
+        v = v2;
       }
-      red[wave][0][lane] = ga;
-      red[wave][1][lane] = ua;
-      __syncthreads();
+      red[buf][wave][0][lane] = ga;
+      red[buf][wave][1][lane] = ua;
+      __syncthreads();  // the other buffer's readers are past it by the next one
       // lane (row r, quarter q) of the sums holds tokens 4q .. 4q+3
       if (threadIdx.x < 256) {
         const int tok = threadIdx.x >> 4, rr = threadIdx.x & 15;
@@ -441,8 +461,8 @@ __global__ __launch_bounds__(kUpWaves* kWave) void k_moe_up(MoeArgs a) {
           float gs = 0.0f, us = 0.0f;
 #pragma unroll
           for (int w = 0; w < kUpWaves; w++) {
-            gs += red[w][0][(tok >> 2) * 16 + rr][tok & 3];
-            us += red[w][1][(tok >> 2) * 16 + rr][tok & 3];
+            gs += red[buf][w][0][(tok >> 2) * 16 + rr][tok & 3];
+            us += red[buf][w][1][(tok >> 2) * 16 + rr][tok & 3];
           }
           const float h = silu_mul(gs, us);
           const uint16_t hi = f32_to_bf16_bits(h);
@@ -455,8 +475,8 @@ __global__ __launch_bounds__(kUpWaves* kWave) void k_moe_up(MoeArgs a) {
           out[4] = __builtin_isfinite(rest) ? f32_to_bf16_bits(rest) : 0;
         }
       }
-      __syncthreads();
     }
+    gate = next_gate;
   }
 }
 
@@ -468,11 +488,23 @@ __global__ __launch_bounds__(kUpWaves* kWave) void k_moe_up(MoeArgs a) {
 template <int FMT>
 __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int max_slices) {
   extern __shared__ __align__(16) float slots[];  // [slice][pair][16]
-  const Table* table = static_cast<const Table*>(a.table);
+  __shared__ Table table;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int pairs = a.n * a.top_k;
-  const int active = table->active;
+  {
+    // all of the table at once: it is read by one round trip, not by three
+    const Table* t = static_cast<const Table*>(a.table);
+    const int most = pairs < a.experts ? pairs : a.experts;
+    if (threadIdx.x == 0) table.active = t->active;
+    for (int i = threadIdx.x; i <= most; i += kDownWaves * kWave) {
+      table.expert[i < most ? i : 0] = t->expert[i < most ? i : 0];
+      table.off[i] = t->off[i];
+    }
+    for (int i = threadIdx.x; i < pairs; i += kDownWaves * kWave) table.list[i] = t->list[i];
+    __syncthreads();
+  }
+  const int active = table.active;
   const int steps = (a.inter + 255) / 256, units = a.inter / 32;
   // slices: as many as give every wave work, evenly
   int slices = active > 0 ? (2 * kDownWaves + active - 1) / active : 1;
@@ -480,49 +512,63 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
   slices = slices < steps ? slices : steps;
   const int per = (steps + slices - 1) / slices;
   slices = (steps + per - 1) / per;
-  const int row0 = blockIdx.x * 16;
-
-  for (int task = wave; task < active * slices; task += kDownWaves) {
+  const int row0 = blockIdx.x * 16, tasks = active * slices;
+  auto row = [&](int task) {
+    return a.down + (static_cast<int64_t>(table.expert[task / slices]) * a.hidden + row0 + r) * a.down_row_bytes;
+  };
+  int task = wave;
+  Step<FMT> s;
+  const uint8_t* w = nullptr;
+  if (task < tasks) {
+    w = row(task);
+    s.load(w, task % slices * per, q, units);
+  }
+  for (; task < tasks; task += kDownWaves) {
     const int slot = task / slices, slice = task - slot * slices;
-    const int first = table->off[slot], count = table->off[slot + 1] - first;
-    const uint8_t* w = a.down + (static_cast<int64_t>(table->expert[slot]) * a.hidden + row0 + r) * a.down_row_bytes;
-    const int sb1 = (slice + 1) * per < steps ? (slice + 1) * per : steps;
+    const int first = table.off[slot], count = table.off[slot + 1] - first;
+    const int sb0 = slice * per, sb1 = sb0 + per < steps ? sb0 + per : steps;
+    const int next = task + kDownWaves < tasks ? task + kDownWaves : task;
+    const uint8_t* next_w = row(next);
     for (int c0 = 0; c0 < count; c0 += 16) {
       const bool live = c0 + r < count;
-      const int pair = table->list[first + (live ? c0 + r : 0)];
+      const int pair = table.list[first + (live ? c0 + r : 0)];
       const uint8_t* h = reinterpret_cast<const uint8_t*>(a.h) + static_cast<int64_t>(pair) * a.inter * 4 + 16 * q;
       float4_t acc = {0, 0, 0, 0};
-      for (int sb = slice * per; sb < sb1; sb++) {
-        Step<FMT> s;
-        s.load(w, sb, q, units);
+      for (int sb = sb0; sb < sb1; sb++) {
+        u32x4 ha[8][2];
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+          ha[u][0] = ha[u][1] = u32x4{0, 0, 0, 0};
+          const int at = 8 * sb + u;
+          if (live && at < units) {
+            ha[u][0] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128);
+            ha[u][1] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128 + 64);
+          }
+        }
+        // the next step's weights, of this task or the next, while this one is multiplied
+        const bool more = sb + 1 < sb1, again = c0 + 16 < count;
+        Step<FMT> s2;
+        s2.load(more || again ? w : next_w, more ? sb + 1 : again ? sb0 : next % slices * per, q, units);
         s.finish(sb, q, units);
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-          u32x4 ha[4][2];
-#pragma unroll
-          for (int u = 0; u < 4; u++) {
-            ha[u][0] = ha[u][1] = u32x4{0, 0, 0, 0};
-            const int at = 8 * sb + 4 * j + u;
-            if (live && at < units) {
-              ha[u][0] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128);
-              ha[u][1] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128 + 64);
-            }
-          }
           quarters4x4(s.raw[j]);
 #pragma unroll
           for (int u = 0; u < 4; u++) {
-            const u32x4 op[2] = {u32x4{ha[u][0].x, ha[u][0].y, ha[u][1].x, ha[u][1].y},
-                                 u32x4{ha[u][0].z, ha[u][0].w, ha[u][1].z, ha[u][1].w}};
+            const u32x4 a0 = ha[4 * j + u][0], a1 = ha[4 * j + u][1];
+            const u32x4 op[2] = {u32x4{a0.x, a0.y, a1.x, a1.y}, u32x4{a0.z, a0.w, a1.z, a1.w}};
             const float4_t xs = unit_sum<FMT, false, 2>(op);
             mul_unit<FMT, false, 2>(s, 4 * j + u, s.raw[j][u], op, xs, acc);
           }
         }
+        s = s2;
       }
 #pragma unroll
       for (int i = 0; i < 4; i++)
         if (c0 + 4 * q + i < count)
-          slots[(slice * pairs + table->list[first + c0 + 4 * q + i]) * 16 + r] = acc[i];
+          slots[(slice * pairs + table.list[first + c0 + 4 * q + i]) * 16 + r] = acc[i];
     }
+    w = next_w;
   }
   __syncthreads();
   for (int o = threadIdx.x; o < a.n * 16; o += kDownWaves * kWave) {
