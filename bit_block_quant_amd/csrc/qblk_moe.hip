@@ -45,8 +45,7 @@ constexpr int kDownWaves = 16;  // waves that share the experts of one tile
 constexpr uint32_t kLo4 = 0x0F0F0F0Fu;
 
 // The routing of one piece, in LDS or in the workspace: experts with at least
-// one pair are slots 0 .. active-1 in order of their index; slot s owns
-// list[off[s] .. off[s+1]).
+// one pair are slots 0 .. active-1; slot s owns list[off[s] .. off[s+1]).
 struct Table {
   int active;
   int expert[kMoeMaxExperts];
@@ -247,67 +246,114 @@ __device__ __forceinline__ float4_t unit_sum(const u32x4 (&a)[PARTS]) {
 }
 
 // ---------------------------------------------------------------- routing
-// One token's experts by one wave: lane l looks at experts l, l + 64, ...
-__device__ void route_token(const float* __restrict__ logits, int experts, int top_k, int renorm, float wscale,
-                            int lane, int* ids, int32_t* __restrict__ out_ids, float* __restrict__ out_w) {
-  constexpr int PER = kMoeMaxExperts / 64;
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+// Over the 16 lanes of a DPP row, in every lane: exchanges with lanes ^1, ^2,
+// then mirrored in 8 and in 16.
+template <class Op>
+__device__ __forceinline__ float row16(float v, Op op) {
+  v = op(v, __builtin_bit_cast(float, dpp<0xB1>(__builtin_bit_cast(int, v))));
+  v = op(v, __builtin_bit_cast(float, dpp<0x4E>(__builtin_bit_cast(int, v))));
+  v = op(v, __builtin_bit_cast(float, dpp<0x141>(__builtin_bit_cast(int, v))));
+  return op(v, __builtin_bit_cast(float, dpp<0x140>(__builtin_bit_cast(int, v))));
+}
+__device__ __forceinline__ int row16_min(int v) {
+  int o = dpp<0xB1>(v);
+  v = v < o ? v : o;
+  o = dpp<0x4E>(v);
+  v = v < o ? v : o;
+  o = dpp<0x141>(v);
+  v = v < o ? v : o;
+  o = dpp<0x140>(v);
+  return v < o ? v : o;
+}
+
+// Four tokens by one wave, 16 lanes to each: lane l of a row looks at experts
+// l, l + 16, ...  A round takes the largest logit that is left and, of equal
+// ones, the lowest expert.  `token` may be past the end (its row idles).
+template <int PER>
+__device__ void route_tokens(const MoeArgs& a, int token, int* ids, bool write) {
   const float none = -__builtin_huge_valf();
+  const int l = threadIdx.x & 15;
+  const bool on = token < a.n;
+  const float* logits = a.logits + static_cast<int64_t>(on ? token : 0) * a.experts;
   float v[PER];
 #pragma unroll
   for (int i = 0; i < PER; i++) {
-    v[i] = none;
-    if (64 * i < experts) {
-      const int e = 64 * i + lane;
-      const float l = e < experts ? logits[e] : none;
-      v[i] = l > none ? __builtin_fminf(l, 3.402823466e38f) : none;  // NaN is never taken
-    }
+    const int e = 16 * i + l;
+    const float x = on && e < a.experts ? logits[e] : none;
+    v[i] = x > none ? __builtin_fminf(x, 3.402823466e38f) : none;  // NaN is never taken
   }
-  float top = none, sum = 0.0f, mine = 0.0f;
-  int id = -1;
-  for (int j = 0; j < top_k; j++) {
+  const auto max2 = [](float x, float y) { return __builtin_fmaxf(x, y); };
+  const auto sum2 = [](float x, float y) { return x + y; };
+  float top = none, sum = 0.0f, mine[2] = {0.0f, 0.0f};
+  int id[2] = {-1, -1};  // choices l and l + 16
+  for (int j = 0; j < a.top_k; j++) {
     float m = v[0];
+    int at = l;
 #pragma unroll
-    for (int i = 1; i < PER; i++)
-      if (64 * i < experts) m = __builtin_fmaxf(m, v[i]);
-    m = group_max<kWave>(m);
+    for (int i = 1; i < PER; i++) {
+      at = v[i] > m ? 16 * i + l : at;
+      m = __builtin_fmaxf(m, v[i]);
+    }
+    const float best = row16(m, max2);
+    const int e = row16_min(m == best ? at : 1 << 30);
     if (j == 0) {
-      top = m;
-      if (!renorm && m > none) {
+      top = best;
+      if (!a.renorm) {
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < PER; i++)
-          if (64 * i < experts) s += v[i] > none ? __builtin_expf(v[i] - top) : 0.0f;
-#pragma unroll
-        for (int x = 1; x < kWave; x <<= 1) s += __shfl_xor(s, x, kWave);
-        sum = s;
+        for (int i = 0; i < PER; i++) s += v[i] > none ? __builtin_expf(v[i] - top) : 0.0f;
+        sum = row16(s, sum2);
       }
     }
-    int e = -1;
-    if (m > none) {
-#pragma unroll
-      for (int i = 0; i < PER; i++)
-        if (64 * i < experts && e < 0) {
-          const uint64_t hit = __builtin_amdgcn_ballot_w64(v[i] == m);
-          if (hit != 0) {
-            const int at = __builtin_ctzll(hit);
-            e = 64 * i + at;
-            if (lane == at) v[i] = none;
-          }
-        }
-      const float p = __builtin_expf(m - top);
-      if (renorm) sum += p;
-      if (lane == j) {
-        id = e;
-        mine = p;
+    if (best > none) {
+      const float p = __builtin_expf(best - top);
+      if (a.renorm) sum += p;
+      if ((j & 15) == l) {
+        id[j >> 4] = e;
+        mine[j >> 4] = p;
       }
+#pragma unroll
+      for (int i = 0; i < PER; i++) v[i] = 16 * i + l == e ? none : v[i];
     }
   }
-  if (lane < top_k) {
-    ids[lane] = id;
-    if (out_ids != nullptr) {
-      out_ids[lane] = id;
-      out_w[lane] = id >= 0 ? mine / sum * wscale : 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; h++)
+    if (on && 16 * h + l < a.top_k) {
+      const int p = token * a.top_k + 16 * h + l;
+      ids[p] = id[h];
+      if (write) {
+        a.ids[p] = id[h];
+        a.weights[p] = id[h] >= 0 ? mine[h] / sum * a.wscale : 0.0f;
+      }
     }
+}
+
+// The table of up to 64 pairs, by one wave: the pairs of the first expert that
+// is left, found by comparing with it, until none is.
+__device__ void few_pairs_table(const int* ids, int pairs, Table& t) {
+  const int lane = threadIdx.x & 63;
+  const int id = lane < pairs ? ids[lane] : -1;
+  uint64_t left = __builtin_amdgcn_ballot_w64(id >= 0);
+  int slot = 0, off = 0;
+  while (left != 0) {
+    const int e = __shfl(id, __builtin_ctzll(left), kWave);
+    const uint64_t same = __builtin_amdgcn_ballot_w64(id == e);
+    if (lane == 0) {
+      t.expert[slot] = e;
+      t.off[slot] = off;
+    }
+    if (id == e) t.list[off + __popcll(same & ((uint64_t(1) << lane) - 1))] = lane;
+    off += __popcll(same);
+    slot++;
+    left &= ~same;
+  }
+  if (lane == 0) {
+    t.active = slot;
+    t.off[slot] = off;
   }
 }
 
@@ -368,9 +414,15 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   const int pairs = a.n * a.top_k;
 
   if (a.logits != nullptr) {
-    for (int t = wave; t < a.n; t += kUpWaves)
-      route_token(a.logits + static_cast<int64_t>(t) * a.experts, a.experts, a.top_k, a.renorm, a.wscale, lane,
-                  ids + t * a.top_k, blockIdx.x == 0 ? a.ids + t * a.top_k : nullptr, a.weights + t * a.top_k);
+    for (int t = 4 * wave; t < a.n; t += 4 * kUpWaves) {
+      const bool write = blockIdx.x == 0;
+      if (a.experts <= 64)
+        route_tokens<4>(a, t + q, ids, write);
+      else if (a.experts <= 128)
+        route_tokens<8>(a, t + q, ids, write);
+      else
+        route_tokens<kMoeMaxExperts / 16>(a, t + q, ids, write);
+    }
   } else {
     for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
       const int e = a.ids[p];
@@ -378,7 +430,12 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
     }
   }
   __syncthreads();
-  build_table(ids, pairs, a.experts, table, cursor);
+  if (pairs <= 64) {
+    if (wave == 0) few_pairs_table(ids, pairs, table);
+    __syncthreads();
+  } else {
+    build_table(ids, pairs, a.experts, table, cursor);
+  }
   if (blockIdx.x == 0) {
     Table* t = static_cast<Table*>(a.table);
     for (int s = threadIdx.x; s <= table.active; s += blockDim.x) {
@@ -413,25 +470,29 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
     const int first = table.off[slot], count = table.off[slot + 1] - first;
     const uint8_t* next_gate = task + gridDim.x < tasks ? gate_row(task + gridDim.x) : gate;
     for (int c0 = 0; c0 < count; c0 += 16, buf ^= 1) {
-      const bool live = c0 + r < count;  // the other lanes' rows of the tile are zero
-      const int pair = table.list[first + (live ? c0 + r : 0)];
+      // lanes past the expert's last pair repeat it: their rows of the tile are not used
+      const int pair = table.list[first + (c0 + r < count ? c0 + r : count - 1)];
       const uint8_t* x = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(pair / a.top_k) * a.hidden * 2 + 8 * q;
       float4_t ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
-      for (int sb = wave; sb < steps; sb += kUpWaves) {
-        u32x4 xa[8];
+      // x a half step (4 units) ahead.  Units past the row's end repeat its
+      // last one: their weights scale by zero.
+      u32x4 xa[2][4];
+      auto x_load = [&](int half, int j) {  // half steps 2 * sb + {0, 1}
 #pragma unroll
-        for (int u = 0; u < 8; u++) {
-          xa[u] = u32x4{0, 0, 0, 0};
-          if (live && 8 * sb + u < units) {
-            const u32x2 l0 = *reinterpret_cast<const u32x2*>(x + (8 * sb + u) * 64);
-            const u32x2 l1 = *reinterpret_cast<const u32x2*>(x + (8 * sb + u) * 64 + 32);
-            xa[u] = u32x4{l0.x, l0.y, l1.x, l1.y};
-          }
+        for (int u = 0; u < 4; u++) {
+          const int at = 4 * half + u < units ? 4 * half + u : units - 1;
+          const u32x2 l0 = *reinterpret_cast<const u32x2*>(x + at * 64);
+          const u32x2 l1 = *reinterpret_cast<const u32x2*>(x + at * 64 + 32);
+          xa[j][u] = u32x4{l0.x, l0.y, l1.x, l1.y};
         }
+      };
+      if (busy) x_load(2 * wave, 0);
+      for (int sb = wave; sb < steps; sb += kUpWaves) {
         const bool more = sb + kUpWaves < steps;
         const uint8_t* ng = more || c0 + 16 < count ? gate : next_gate;
         const int nsb = more ? sb + kUpWaves : wave;
         Step<FMT> g2, v2;
+        x_load(2 * sb + 1, 1);
         g2.load(ng, nsb, q, units);
         v2.load(ng + up_off, nsb, q, units);
         g.finish(sb, q, units);
@@ -442,11 +503,12 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
           quarters4x4(v.raw[j]);
 #pragma unroll
           for (int u = 0; u < 4; u++) {
-            const u32x4 op[1] = {xa[4 * j + u]};
+            const u32x4 op[1] = {xa[j][u]};
             const float4_t xs = unit_sum<FMT, F16, 1>(op);
             mul_unit<FMT, F16, 1>(g, 4 * j + u, g.raw[j][u], op, xs, ga);
             mul_unit<FMT, F16, 1>(v, 4 * j + u, v.raw[j][u], op, xs, ua);
           }
+          if (j == 0) x_load(more ? 2 * nsb : 2 * sb, 0);
         }
         g = g2;
         v = v2;
@@ -530,24 +592,24 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
     const int next = task + kDownWaves < tasks ? task + kDownWaves : task;
     const uint8_t* next_w = row(next);
     for (int c0 = 0; c0 < count; c0 += 16) {
-      const bool live = c0 + r < count;
-      const int pair = table.list[first + (live ? c0 + r : 0)];
+      const int pair = table.list[first + (c0 + r < count ? c0 + r : count - 1)];
       const uint8_t* h = reinterpret_cast<const uint8_t*>(a.h) + static_cast<int64_t>(pair) * a.inter * 4 + 16 * q;
       float4_t acc = {0, 0, 0, 0};
-      for (int sb = sb0; sb < sb1; sb++) {
-        u32x4 ha[8][2];
+      u32x4 ha[2][4][2];
+      auto h_load = [&](int half, int j) {
 #pragma unroll
-        for (int u = 0; u < 8; u++) {
-          ha[u][0] = ha[u][1] = u32x4{0, 0, 0, 0};
-          const int at = 8 * sb + u;
-          if (live && at < units) {
-            ha[u][0] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128);
-            ha[u][1] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128 + 64);
-          }
+        for (int u = 0; u < 4; u++) {
+          const int at = 4 * half + u < units ? 4 * half + u : units - 1;
+          ha[j][u][0] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128);
+          ha[j][u][1] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128 + 64);
         }
+      };
+      h_load(2 * sb0, 0);
+      for (int sb = sb0; sb < sb1; sb++) {
         // the next step's weights, of this task or the next, while this one is multiplied
         const bool more = sb + 1 < sb1, again = c0 + 16 < count;
         Step<FMT> s2;
+        h_load(2 * sb + 1, 1);
         s2.load(more || again ? w : next_w, more ? sb + 1 : again ? sb0 : next % slices * per, q, units);
         s.finish(sb, q, units);
 #pragma unroll
@@ -555,11 +617,12 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
           quarters4x4(s.raw[j]);
 #pragma unroll
           for (int u = 0; u < 4; u++) {
-            const u32x4 a0 = ha[4 * j + u][0], a1 = ha[4 * j + u][1];
+            const u32x4 a0 = ha[j][u][0], a1 = ha[j][u][1];
             const u32x4 op[2] = {u32x4{a0.x, a0.y, a1.x, a1.y}, u32x4{a0.z, a0.w, a1.z, a1.w}};
             const float4_t xs = unit_sum<FMT, false, 2>(op);
             mul_unit<FMT, false, 2>(s, 4 * j + u, s.raw[j][u], op, xs, acc);
           }
+          if (j == 0) h_load(more ? 2 * sb + 2 : 2 * sb, 0);
         }
         s = s2;
       }
@@ -594,7 +657,7 @@ template <int FMT>
 hipError_t run(const MoeArgs& a, hipStream_t s) {
   const int64_t reach = static_cast<int64_t>(a.n) * a.top_k < a.experts ? static_cast<int64_t>(a.n) * a.top_k : a.experts;
   const int64_t tasks = reach * (a.inter / 16);
-  const int64_t most = static_cast<int64_t>(cu_count()) * 3;
+  const int64_t most = static_cast<int64_t>(cu_count()) * 2;  // what fits at once, by registers
   const unsigned grid = static_cast<unsigned>(tasks < most ? tasks : most);
   if (a.xt == QBLK_F16)
     k_moe_up<FMT, true><<<grid, kUpWaves * kWave, 0, s>>>(a);
