@@ -44,6 +44,12 @@ constexpr int kUpWaves = 8;     // waves that share the columns of one tile
 constexpr int kDownWaves = 16;  // waves that share the experts of one tile
 constexpr uint32_t kLo4 = 0x0F0F0F0Fu;
 
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void glob_void;
+// s_waitcnt immediates (gfx9: vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt
+// 11:8): no vector memory, or no LDS access, in flight
+constexpr int kWaitLoads = 0x0F70, kWaitLds = 0xC07F;
+
 // The routing of one piece, in LDS or in the workspace: experts with at least
 // one pair are slots 0 .. active-1; slot s owns list[off[s] .. off[s+1]).
 struct Table {
@@ -109,20 +115,21 @@ __device__ __forceinline__ void quarters4x4(uint32_t v[4]) {
 }
 
 // ------------------------------------------------------------- the formats
-// 256 weights (8 units) of one row per lane row: what is loaded, and unit u's
-// scale and offset.  `units` is the number of units of a row (Q4_0 rows may
-// end inside a step; every other format has whole super-blocks).
+// 128 weights (4 units) of one row per lane row, the codes of unit q in lane
+// quarter q: what is loaded (`load`, half super-block `hf` of the row), and
+// after `finish` unit u's scale and offset.  `units` is the number of units
+// of a row: Q4_0 rows may end inside a half; units past the end repeat the
+// last one's codes and scale by zero.
 template <int FMT>
-struct Step;
+struct Half;
 
 template <>
-struct Step<QBLK_SB4> {
+struct Half<QBLK_SB4> {
   static constexpr bool affine = false;
-  uint32_t raw[2][4], h[3];
-  __device__ __forceinline__ void load(const uint8_t* row, int sb, int q, int) {
-    const uint8_t* p = row + static_cast<int64_t>(sb) * 138;
-    load16_a2(p + 10 + 16 * q, raw[0]);
-    load16_a2(p + 74 + 16 * q, raw[1]);
+  uint32_t raw[4], h[3];
+  __device__ __forceinline__ void load(const uint8_t* row, int hf, int q, int) {
+    const uint8_t* p = row + static_cast<int64_t>(hf >> 1) * 138;
+    load16_a2(p + 10 + 64 * (hf & 1) + 16 * q, raw);
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
     const u32x3_a4 v = *reinterpret_cast<const u32x3_a4*>(a & ~uintptr_t(3));
     const uint32_t sh = static_cast<uint32_t>(a & 3u);
@@ -130,102 +137,96 @@ struct Step<QBLK_SB4> {
     h[1] = __builtin_amdgcn_alignbyte(v.z, v.y, sh);
     h[2] = v.z >> (8 * sh);
   }
+  __device__ __forceinline__ void finish(int hf, int, int) {  // h[1]: the half's four sub-scales
+    h[1] = (hf & 1) ? __builtin_amdgcn_alignbyte(h[2], h[1], 2) : __builtin_amdgcn_alignbyte(h[1], h[0], 2);
+  }
   __device__ __forceinline__ float scale(int u) const {
-    const uint32_t w = h[(u + 2) >> 2];
-    const int c = static_cast<int8_t>(w >> (8 * ((u + 2) & 3)));
-    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(c);
+    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(static_cast<int8_t>(h[1] >> (8 * u)));
   }
   __device__ __forceinline__ float offset(int) const { return 0.0f; }
-  __device__ __forceinline__ void finish(int, int, int) {}
 };
 
 template <>
-struct Step<QBLK_SB4_AFFINE> {
+struct Half<QBLK_SB4_AFFINE> {
   static constexpr bool affine = true;
-  uint32_t raw[2][4], h[5];
-  __device__ __forceinline__ void load(const uint8_t* row, int sb, int q, int) {
-    const uint8_t* p = row + static_cast<int64_t>(sb) * 148;  // a multiple of 4: every field is dword aligned
-    const u32x4_a4 a = *reinterpret_cast<const u32x4_a4*>(p + 20 + 16 * q);
-    const u32x4_a4 b = *reinterpret_cast<const u32x4_a4*>(p + 84 + 16 * q);
-    const u32x4_a4 c = *reinterpret_cast<const u32x4_a4*>(p);
+  uint32_t raw[4], h[3];
+  __device__ __forceinline__ void load(const uint8_t* row, int hf, int q, int) {
+    const uint8_t* p = row + static_cast<int64_t>(hf >> 1) * 148;  // a multiple of 4: every field is dword aligned
+    const u32x4_a4 a = *reinterpret_cast<const u32x4_a4*>(p + 20 + 64 * (hf & 1) + 16 * q);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      raw[0][i] = a[i];
-      raw[1][i] = b[i];
-      h[i] = c[i];
-    }
-    h[4] = *reinterpret_cast<const uint32_t*>(p + 16);
+    for (int i = 0; i < 4; i++) raw[i] = a[i];
+    h[0] = *reinterpret_cast<const uint32_t*>(p);
+    h[1] = *reinterpret_cast<const uint32_t*>(p + 4 + 4 * (hf & 1));
+    h[2] = *reinterpret_cast<const uint32_t*>(p + 12 + 4 * (hf & 1));
   }
+  __device__ __forceinline__ void finish(int, int, int) {}
   __device__ __forceinline__ float scale(int u) const {
-    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(static_cast<int8_t>(h[1 + (u >> 2)] >> (8 * (u & 3))));
+    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(static_cast<int8_t>(h[1] >> (8 * u)));
   }
   __device__ __forceinline__ float offset(int u) const {
-    return f16_bits_to_f32(h[0] >> 16) * static_cast<float>(static_cast<int8_t>(h[3 + (u >> 2)] >> (8 * (u & 3))));
+    return f16_bits_to_f32(h[0] >> 16) * static_cast<float>(static_cast<int8_t>(h[2] >> (8 * u)));
   }
-  __device__ __forceinline__ void finish(int, int, int) {}
 };
 
 template <>
-struct Step<QBLK_Q4_K> {
+struct Half<QBLK_Q4_K> {
   static constexpr bool affine = true;
-  uint32_t raw[2][4], h[4];
-  __device__ __forceinline__ void load(const uint8_t* row, int sb, int q, int) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(sb) * 144);  // 16-byte aligned
-    const u32x4 a = p[1 + q], b = p[5 + q], c = p[0];
+  uint32_t raw[4], h[4];
+  __device__ __forceinline__ void load(const uint8_t* row, int hf, int q, int) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(hf >> 1) * 144);  // 16-byte aligned
+    const u32x4 a = p[1 + 4 * (hf & 1) + q], c = p[0];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      raw[0][i] = a[i];
-      raw[1][i] = b[i];
+      raw[i] = a[i];
       h[i] = c[i];
     }
   }
+  // the half's 6-bit scales to h[1], mins to h[2]: fields 4j .. 4j+3 are bits
+  // 24j .. 24j+23 of h1:h2:h3, the mins 48 bits further on
+  __device__ __forceinline__ void finish(int hf, int, int) {
+    const uint32_t s = (hf & 1) ? (h[1] >> 24) | (h[2] << 8) : h[1];
+    const uint32_t m = (hf & 1) ? h[3] >> 8 : (h[2] >> 16) | (h[3] << 16);
+    h[1] = s;
+    h[2] = m;
+  }
   __device__ __forceinline__ float scale(int u) const {
-    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(q4k_scale6(h[1], h[2], u));
+    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>((h[1] >> (6 * u)) & 63u);
   }
   __device__ __forceinline__ float offset(int u) const {
-    return -(f16_bits_to_f32(h[0] >> 16) * static_cast<float>(q4k_min6(h[2], h[3], u)));
+    return -(f16_bits_to_f32(h[0] >> 16) * static_cast<float>((h[2] >> (6 * u)) & 63u));
   }
-  __device__ __forceinline__ void finish(int, int, int) {}
 };
 
 template <>
-struct Step<QBLK_Q4_0> {
+struct Half<QBLK_Q4_0> {
   static constexpr bool affine = false;
-  uint32_t raw[2][4], d[4];
-  __device__ __forceinline__ void load(const uint8_t* row, int sb, int q, int units) {
-    uint32_t s[2];
-#pragma unroll
-    for (int j = 0; j < 2; j++) {
-      const int u = 8 * sb + 4 * j + q;
-      const uint8_t* p = row + static_cast<int64_t>(u < units ? u : units - 1) * 18;
-      load16_a2(p + 2, raw[j]);
-      s[j] = load_u16(p);
-    }
-    d[0] = s[0];
-    d[1] = s[1];
+  uint32_t raw[4], d[4];
+  __device__ __forceinline__ void load(const uint8_t* row, int hf, int q, int units) {
+    const int u = 4 * hf + q;
+    const uint8_t* p = row + static_cast<int64_t>(u < units ? u : units - 1) * 18;
+    load16_a2(p + 2, raw);
+    d[0] = load_u16(p);
   }
-  // the scales of all eight units to every quarter; a unit past the row's end scales by zero
-  __device__ __forceinline__ void finish(int sb, int q, int units) {
-    const uint32_t a = 8 * sb + q < units ? d[0] : 0u, b = 8 * sb + 4 + q < units ? d[1] : 0u;
-    d[0] = d[1] = d[2] = d[3] = a | (b << 16);
+  // the scales of all four units to every quarter
+  __device__ __forceinline__ void finish(int hf, int q, int units) {
+    d[0] = 4 * hf + q < units ? d[0] : 0u;
+    d[1] = d[2] = d[3] = d[0];
     quarters4x4(d);
   }
-  __device__ __forceinline__ float scale(int u) const {
-    return f16_bits_to_f32(u < 4 ? d[u & 3] & 0xffffu : d[u & 3] >> 16);
-  }
+  __device__ __forceinline__ float scale(int u) const { return f16_bits_to_f32(d[u]); }
   __device__ __forceinline__ float offset(int) const { return 0.0f; }
 };
 
-// acc += (the step's 16 rows) x (16 gathered token rows): PARTS operands a[part][unit]
+// acc += (unit u of 16 rows) x (16 gathered token rows), the operand in PARTS summands
 template <int FMT, bool F16, int PARTS>
-__device__ __forceinline__ void mul_unit(const Step<FMT>& w, int u, uint32_t codes, const u32x4 (&a)[PARTS],
+__device__ __forceinline__ void mul_unit(const Half<FMT>& w, int u, uint32_t codes, const u32x4 (&a)[PARTS],
                                          const float4_t& xs, float4_t& acc) {
   const u32x4 b = codes8_op<F16>(codes);
-  float4_t p = Step<FMT>::affine ? float4_t{0, 0, 0, 0} : xs;
+  float4_t p = Half<FMT>::affine ? float4_t{0, 0, 0, 0} : xs;
 #pragma unroll
   for (int i = 0; i < PARTS; i++) p = Op<F16>::mma(a[i], b, p);
   const float s = w.scale(u);
-  if constexpr (Step<FMT>::affine) {
+  if constexpr (Half<FMT>::affine) {
     const float o = w.offset(u);
 #pragma unroll
     for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(o, xs[i], __builtin_fmaf(s, p[i], acc[i]));
@@ -238,7 +239,7 @@ __device__ __forceinline__ void mul_unit(const Step<FMT>& w, int u, uint32_t cod
 // sum(x) of the unit per token (times -8 for the formats whose offset that is)
 template <int FMT, bool F16, int PARTS>
 __device__ __forceinline__ float4_t unit_sum(const u32x4 (&a)[PARTS]) {
-  const uint32_t c = Step<FMT>::affine ? Op<F16>::one2 : Op<F16>::minus8;
+  const uint32_t c = Half<FMT>::affine ? Op<F16>::one2 : Op<F16>::minus8;
   float4_t p = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < PARTS; i++) p = Op<F16>::mma(a[i], u32x4{c, c, c, c}, p);
@@ -357,19 +358,51 @@ __device__ void few_pairs_table(const int* ids, int pairs, Table& t) {
   }
 }
 
-// The table from ids (pairs of them, in LDS); all threads of the workgroup.
-__device__ void build_table(const int* ids, int pairs, int experts, Table& t, int* cursor) {
-  for (int e = threadIdx.x; e < experts; e += blockDim.x) cursor[e] = 0;
+// The table of any number of pairs, by all threads of the workgroup.  A pair's
+// place must not depend on timing (every workgroup makes the table for itself
+// and h is stored by place), so it is counted: the pairs of its expert in the
+// blocks of 64 before its own, then those before it in the block.
+struct TableScratch {
+  int ids[kMoeMaxPairs];
+  int base[kMoeMaxExperts];
+  uint16_t count[kMoeMaxPairs / 64][kMoeMaxExperts];
+};
+
+__device__ void build_table(int pairs, int experts, Table& t, TableScratch& z) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, blocks = (pairs + 63) / 64;
+  constexpr int kRounds = (kMoeMaxPairs / 64 + kUpWaves - 1) / kUpWaves;
+  for (int i = threadIdx.x; i < blocks * kMoeMaxExperts; i += blockDim.x) (&z.count[0][0])[i] = 0;
   __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += blockDim.x)
-    if (ids[p] >= 0) atomicAdd(&cursor[ids[p]], 1);
+  int id[kRounds], rank[kRounds];
+#pragma unroll
+  for (int k = 0; k < kRounds; k++) {
+    const int b = wave + k * kUpWaves, p = 64 * b + lane;
+    id[k] = b < blocks && p < pairs ? z.ids[p] : -1;
+    uint64_t same = __builtin_amdgcn_ballot_w64(id[k] >= 0);  // the lanes with this lane's expert, a bit at a time
+#pragma unroll
+    for (int bit = 1; bit < kMoeMaxExperts; bit <<= 1) {
+      const uint64_t set = __builtin_amdgcn_ballot_w64((id[k] & bit) != 0);
+      same &= (id[k] & bit) ? set : ~set;
+    }
+    rank[k] = __popcll(same & ((uint64_t(1) << lane) - 1));
+    if (id[k] >= 0 && rank[k] == 0) z.count[b][id[k]] = static_cast<uint16_t>(__popcll(same));
+  }
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
+  for (int e = threadIdx.x; e < experts; e += blockDim.x) {
+    int before = 0;
+    for (int b = 0; b < blocks; b++) {
+      const int c = z.count[b][e];
+      z.count[b][e] = static_cast<uint16_t>(before);
+      before += c;
+    }
+    z.base[e] = before;
+  }
+  __syncthreads();
+  if (wave == 0) {
     int slots = 0, total = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
       const int e = e0 + lane;
-      const int c = e < experts ? cursor[e] : 0;
+      const int c = e < experts ? z.base[e] : 0;
       int run = c;  // inclusive sum over the lanes
 #pragma unroll
       for (int x = 1; x < kWave; x <<= 1) {
@@ -381,7 +414,7 @@ __device__ void build_table(const int* ids, int pairs, int experts, Table& t, in
         const int s = slots + __popcll(some & ((uint64_t(1) << lane) - 1));
         t.expert[s] = e;
         t.off[s] = total + run - c;
-        cursor[e] = total + run - c;
+        z.base[e] = total + run - c;
       }
       slots += __popcll(some);
       total += __shfl(run, 63, kWave);
@@ -392,23 +425,29 @@ __device__ void build_table(const int* ids, int pairs, int experts, Table& t, in
     }
   }
   __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += blockDim.x)
-    if (ids[p] >= 0) t.list[atomicAdd(&cursor[ids[p]], 1)] = p;
+#pragma unroll
+  for (int k = 0; k < kRounds; k++)
+    if (id[k] >= 0) {
+      const int b = wave + k * kUpWaves;
+      t.list[z.base[id[k]] + z.count[b][id[k]] + rank[k]] = 64 * b + lane;
+    }
   __syncthreads();
 }
 
 // --------------------------------------------------------------- gate, up
 // A workgroup takes tiles of 16 gate rows and the 16 up rows that go with
 // them, for all tokens of one expert; its waves split the columns (wave w
-// takes 256-column steps w, w + 8, ...) and their sums meet in LDS.
+// takes 256-column super-blocks w, w + 8, ...) and their sums meet in LDS.
 // Workgroups are persistent, so the routing is worked out once in each rather
 // than by a launch of its own.
 template <int FMT, bool F16>
 __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   __shared__ Table table;
-  __shared__ int ids[kMoeMaxPairs];
-  __shared__ int cursor[kMoeMaxExperts];
   __shared__ float4_t red[2][kUpWaves][2][64];
+  __shared__ u32x4 xbuf[kUpWaves][256];
+  TableScratch& scratch = *reinterpret_cast<TableScratch*>(red);  // before the first tile
+  static_assert(sizeof red >= sizeof(TableScratch));
+  int* const ids = scratch.ids;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int pairs = a.n * a.top_k;
@@ -434,7 +473,7 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
     if (wave == 0) few_pairs_table(ids, pairs, table);
     __syncthreads();
   } else {
-    build_table(ids, pairs, a.experts, table, cursor);
+    build_table(pairs, a.experts, table, scratch);
   }
   if (blockIdx.x == 0) {
     Table* t = static_cast<Table*>(a.table);
@@ -446,9 +485,12 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
     if (threadIdx.x == 0) t->active = table.active;
   }
 
-  const int tiles = a.inter / 16, steps = (a.hidden + 255) / 256, units = a.hidden / 32;
+  const int tiles = a.inter / 16, units = a.hidden / 32, halves = (units + 3) / 4;
   const int64_t tasks = static_cast<int64_t>(table.active) * tiles;
-  const bool busy = wave < steps;
+  // The waves split a row's halves, two (a super-block) in turn.
+  const int step0 = 2 * wave;
+  const bool busy = step0 < halves;
+  const auto after = [](int hf) { return (hf & 1) ? hf + 2 * kUpWaves - 1 : hf + 1; };
   const int64_t up_off = static_cast<int64_t>(a.inter) * a.up_row_bytes;
   auto gate_row = [&](int64_t task) {
     const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
@@ -456,62 +498,93 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   };
   int64_t task = blockIdx.x;
   if (task >= tasks) return;
-  // Every step's weights are loaded while the step before it is multiplied,
-  // across tiles too.
+  // Weights and activations are loaded one half ahead, across tiles too.
   const uint8_t* gate = gate_row(task);
-  Step<FMT> g, v;
+  Half<FMT> g, v;
   if (busy) {
-    g.load(gate, wave, q, units);
-    v.load(gate + up_off, wave, q, units);
+    g.load(gate, step0, q, units);
+    v.load(gate + up_off, step0, q, units);
+  }
+  // x by halves (128 columns), whole rows at a time: 16 lanes copy 256 bytes of
+  // a token's row, four rows an instruction and only as many as the expert
+  // has, straight to LDS, where they are read as operands.  (Loaded as
+  // operands from memory, 16 rows lie 2 * hidden bytes apart and every load
+  // asks for 16 lines.)
+  u32x4* const xw = xbuf[wave];
+  const uint8_t* xrow[4];
+  int xrows = 0;
+  auto x_rows = [&](int slot, int c0) {  // pairs c0 .. c0+15 of the expert; past its last one that again
+    const int first = table.off[slot] + c0;
+    xrows = table.off[slot + 1] - first;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int at = 4 * i + q < xrows ? 4 * i + q : xrows - 1;
+      xrow[i] = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(table.list[first + at] / a.top_k) * a.hidden * 2;
+    }
+  };
+  auto x_copy = [&](int hf) {
+    // 16-byte chunk r ^ row of the row, to LDS chunk r: 16 rows of one chunk
+    // column then lie in 16 different columns of banks.  Past the row's end
+    // (only Q4_0) the last chunk again: those weights scale by zero.
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (4 * i < xrows) {
+        int at = 16 * hf + (r ^ (4 * i + q));
+        at = at < 4 * units ? at : 4 * units - 1;
+        __builtin_amdgcn_global_load_lds((glob_void*)(xrow[i] + 16 * at), (lds_void*)(xw + 64 * i), 16, 0, 0);
+      }
+  };
+  if (busy) {
+    x_rows(static_cast<int>(task / tiles), 0);
+    x_copy(step0);
   }
   int buf = 0;
   for (; task < tasks; task += gridDim.x) {
     const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
     const int first = table.off[slot], count = table.off[slot + 1] - first;
-    const uint8_t* next_gate = task + gridDim.x < tasks ? gate_row(task + gridDim.x) : gate;
+    const int64_t next = task + gridDim.x < tasks ? task + gridDim.x : task;
+    const int next_slot = static_cast<int>(next / tiles);
+    const uint8_t* next_gate = gate_row(next);
     for (int c0 = 0; c0 < count; c0 += 16, buf ^= 1) {
-      // lanes past the expert's last pair repeat it: their rows of the tile are not used
-      const int pair = table.list[first + (c0 + r < count ? c0 + r : count - 1)];
-      const uint8_t* x = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(pair / a.top_k) * a.hidden * 2 + 8 * q;
       float4_t ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
-      // x a half step (4 units) ahead.  Units past the row's end repeat its
-      // last one: their weights scale by zero.
-      u32x4 xa[2][4];
-      auto x_load = [&](int half, int j) {  // half steps 2 * sb + {0, 1}
+      for (int hf = step0; hf < halves;) {
+        const int nh = after(hf);
+        const bool more = nh < halves;
+        // all that is in flight belongs to this half
+        __builtin_amdgcn_s_waitcnt(kWaitLoads);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        u32x4 xa[4];
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(xw) + 256 * r + 8 * (q & 1);
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-          const int at = 4 * half + u < units ? 4 * half + u : units - 1;
-          const u32x2 l0 = *reinterpret_cast<const u32x2*>(x + at * 64);
-          const u32x2 l1 = *reinterpret_cast<const u32x2*>(x + at * 64 + 32);
-          xa[j][u] = u32x4{l0.x, l0.y, l1.x, l1.y};
+          const u32x2 l0 = *reinterpret_cast<const u32x2*>(from + 16 * ((4 * u + (q >> 1)) ^ r));
+          const u32x2 l1 = *reinterpret_cast<const u32x2*>(from + 16 * ((4 * u + 2 + (q >> 1)) ^ r));
+          xa[u] = u32x4{l0.x, l0.y, l1.x, l1.y};
         }
-      };
-      if (busy) x_load(2 * wave, 0);
-      for (int sb = wave; sb < steps; sb += kUpWaves) {
-        const bool more = sb + kUpWaves < steps;
-        const uint8_t* ng = more || c0 + 16 < count ? gate : next_gate;
-        const int nsb = more ? sb + kUpWaves : wave;
-        Step<FMT> g2, v2;
-        x_load(2 * sb + 1, 1);
-        g2.load(ng, nsb, q, units);
-        v2.load(ng + up_off, nsb, q, units);
-        g.finish(sb, q, units);
-        v.finish(sb, q, units);
+        __builtin_amdgcn_s_waitcnt(kWaitLds);  // read before the next half is copied over it
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_sched_barrier(0);
+        const bool again = c0 + 16 < count;
+        if (!more) x_rows(again ? slot : next_slot, again ? c0 + 16 : 0);
+        x_copy(more ? nh : step0);
+        const uint8_t* ng = more || again ? gate : next_gate;
+        Half<FMT> g2, v2;
+        g2.load(ng, more ? nh : step0, q, units);
+        v2.load(ng + up_off, more ? nh : step0, q, units);
+        g.finish(hf, q, units);
+        v.finish(hf, q, units);
+        quarters4x4(g.raw);
+        quarters4x4(v.raw);
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-          quarters4x4(g.raw[j]);
-          quarters4x4(v.raw[j]);
-#pragma unroll
-          for (int u = 0; u < 4; u++) {
-            const u32x4 op[1] = {xa[j][u]};
-            const float4_t xs = unit_sum<FMT, F16, 1>(op);
-            mul_unit<FMT, F16, 1>(g, 4 * j + u, g.raw[j][u], op, xs, ga);
-            mul_unit<FMT, F16, 1>(v, 4 * j + u, v.raw[j][u], op, xs, ua);
-          }
-          if (j == 0) x_load(more ? 2 * nsb : 2 * sb, 0);
+        for (int u = 0; u < 4; u++) {
+          const u32x4 op[1] = {xa[u]};
+          const float4_t xs = unit_sum<FMT, F16, 1>(op);
+          mul_unit<FMT, F16, 1>(g, u, g.raw[u], op, xs, ga);
+          mul_unit<FMT, F16, 1>(v, u, v.raw[u], op, xs, ua);
         }
         g = g2;
         v = v2;
+        hf = nh;
       }
       red[buf][wave][0][lane] = ga;
       red[buf][wave][1][lane] = ua;
@@ -529,17 +602,17 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
           const float h = silu_mul(gs, us);
           const uint16_t hi = f32_to_bf16_bits(h);
           const float rest = h - bf16_bits_to_f32(hi);
-          const int col = 16 * tile + rr;
-          // four hi, four lo, ... : one 16-byte load per lane in k_moe_down
-          uint16_t* out = reinterpret_cast<uint16_t*>(a.h) +
-                          (static_cast<int64_t>(table.list[first + c0 + tok]) * a.inter + (col & ~3)) * 2 + (col & 3);
+          // operand order, see h_load: unit tile/2 of this expert's pairs
+          uint16_t* out = reinterpret_cast<uint16_t*>(a.h) + static_cast<int64_t>(first) * a.inter * 2 +
+                          (static_cast<int64_t>(tile & ~1) * count + c0 + tok) * 32 + 8 * (rr >> 2) + 4 * (tile & 1) + (rr & 3);
           out[0] = hi;
-          out[4] = __builtin_isfinite(rest) ? f32_to_bf16_bits(rest) : 0;
+          out[static_cast<int64_t>(count) * 32] = __builtin_isfinite(rest) ? f32_to_bf16_bits(rest) : 0;
         }
       }
     }
     gate = next_gate;
   }
+  __builtin_amdgcn_s_waitcnt(kWaitLoads);  // no copy to LDS outlives the workgroup
 }
 
 // -------------------------------------------------------------------- down
@@ -567,64 +640,77 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
     __syncthreads();
   }
   const int active = table.active;
-  const int steps = (a.inter + 255) / 256, units = a.inter / 32;
-  // slices: as many as give every wave work, evenly
+  const int units = a.inter / 32, halves = (units + 3) / 4, steps = (halves + 1) / 2;
+  // slices of whole super-blocks: as many as give every wave work, evenly
   int slices = active > 0 ? (2 * kDownWaves + active - 1) / active : 1;
   slices = slices < max_slices ? slices : max_slices;
   slices = slices < steps ? slices : steps;
-  const int per = (steps + slices - 1) / slices;
+  int per = (steps + slices - 1) / slices;
   slices = (steps + per - 1) / per;
+  per *= 2;  // in halves
   const int row0 = blockIdx.x * 16, tasks = active * slices;
   auto row = [&](int task) {
     return a.down + (static_cast<int64_t>(table.expert[task / slices]) * a.hidden + row0 + r) * a.down_row_bytes;
   };
+  // h of an expert's pairs is stored as operands: per unit of 32 columns the hi
+  // parts of all pairs, then the lo parts, 64 bytes a pair (16 per lane
+  // quarter).  Lanes past the last pair repeat it: not used.
+  const uint8_t* h = nullptr;
+  int64_t hstep = 0;
+  auto h_rows = [&](int slot, int c0) {
+    const int first = table.off[slot], count = table.off[slot + 1] - first;
+    h = static_cast<const uint8_t*>(a.h) + static_cast<int64_t>(first) * a.inter * 4 +
+        (c0 + r < count ? c0 + r : count - 1) * 64 + 16 * q;
+    hstep = static_cast<int64_t>(count) * 64;
+  };
+  auto h_load = [&](int hf, u32x4(&to)[4][2]) {
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const int at = 4 * hf + u < units ? 4 * hf + u : units - 1;
+      to[u][0] = *reinterpret_cast<const u32x4*>(h + 2 * at * hstep);
+      to[u][1] = *reinterpret_cast<const u32x4*>(h + (2 * at + 1) * hstep);
+    }
+  };
   int task = wave;
-  Step<FMT> s;
+  Half<FMT> s;
+  u32x4 ha[4][2];
   const uint8_t* w = nullptr;
   if (task < tasks) {
     w = row(task);
     s.load(w, task % slices * per, q, units);
+    h_rows(task / slices, 0);
+    h_load(task % slices * per, ha);
   }
   for (; task < tasks; task += kDownWaves) {
     const int slot = task / slices, slice = task - slot * slices;
     const int first = table.off[slot], count = table.off[slot + 1] - first;
-    const int sb0 = slice * per, sb1 = sb0 + per < steps ? sb0 + per : steps;
+    const int h0 = slice * per, h1 = h0 + per < halves ? h0 + per : halves;
     const int next = task + kDownWaves < tasks ? task + kDownWaves : task;
     const uint8_t* next_w = row(next);
     for (int c0 = 0; c0 < count; c0 += 16) {
-      const int pair = table.list[first + (c0 + r < count ? c0 + r : count - 1)];
-      const uint8_t* h = reinterpret_cast<const uint8_t*>(a.h) + static_cast<int64_t>(pair) * a.inter * 4 + 16 * q;
       float4_t acc = {0, 0, 0, 0};
-      u32x4 ha[2][4][2];
-      auto h_load = [&](int half, int j) {
+      for (int hf = h0; hf < h1; hf++) {
+        // the next half, of this task or the next, while this one is multiplied
+        const bool more = hf + 1 < h1, again = c0 + 16 < count;
+        const int to = more ? hf + 1 : again ? h0 : next % slices * per;
+        if (!more) h_rows(again ? slot : next / slices, again ? c0 + 16 : 0);
+        u32x4 hn[4][2];
+        h_load(to, hn);
+        Half<FMT> s2;
+        s2.load(more || again ? w : next_w, to, q, units);
+        s.finish(hf, q, units);
+        quarters4x4(s.raw);
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-          const int at = 4 * half + u < units ? 4 * half + u : units - 1;
-          ha[j][u][0] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128);
-          ha[j][u][1] = *reinterpret_cast<const u32x4*>(h + static_cast<int64_t>(at) * 128 + 64);
-        }
-      };
-      h_load(2 * sb0, 0);
-      for (int sb = sb0; sb < sb1; sb++) {
-        // the next step's weights, of this task or the next, while this one is multiplied
-        const bool more = sb + 1 < sb1, again = c0 + 16 < count;
-        Step<FMT> s2;
-        h_load(2 * sb + 1, 1);
-        s2.load(more || again ? w : next_w, more ? sb + 1 : again ? sb0 : next % slices * per, q, units);
-        s.finish(sb, q, units);
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-          quarters4x4(s.raw[j]);
-#pragma unroll
-          for (int u = 0; u < 4; u++) {
-            const u32x4 a0 = ha[j][u][0], a1 = ha[j][u][1];
-            const u32x4 op[2] = {u32x4{a0.x, a0.y, a1.x, a1.y}, u32x4{a0.z, a0.w, a1.z, a1.w}};
-            const float4_t xs = unit_sum<FMT, false, 2>(op);
-            mul_unit<FMT, false, 2>(s, 4 * j + u, s.raw[j][u], op, xs, acc);
-          }
-          if (j == 0) h_load(more ? 2 * sb + 2 : 2 * sb, 0);
+          const float4_t xs = unit_sum<FMT, false, 2>(ha[u]);
+          mul_unit<FMT, false, 2>(s, u, s.raw[u], ha[u], xs, acc);
         }
         s = s2;
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          ha[u][0] = hn[u][0];
+          ha[u][1] = hn[u][1];
+        }
       }
 #pragma unroll
       for (int i = 0; i < 4; i++)
