@@ -487,10 +487,9 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
 
   const int tiles = a.inter / 16, units = a.hidden / 32, halves = (units + 3) / 4;
   const int64_t tasks = static_cast<int64_t>(table.active) * tiles;
-  // The waves split a row's halves, two (a super-block) in turn.
-  const int step0 = 2 * wave;
-  const bool busy = step0 < halves;
-  const auto after = [](int hf) { return (hf & 1) ? hf + 2 * kUpWaves - 1 : hf + 1; };
+  // The waves take a row's halves in turn: the two halves of a super-block,
+  // which share its lines, are loaded by neighbours at the same time.
+  const bool busy = wave < halves;
   const int64_t up_off = static_cast<int64_t>(a.inter) * a.up_row_bytes;
   auto gate_row = [&](int64_t task) {
     const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
@@ -502,8 +501,8 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   const uint8_t* gate = gate_row(task);
   Half<FMT> g, v;
   if (busy) {
-    g.load(gate, step0, q, units);
-    v.load(gate + up_off, step0, q, units);
+    g.load(gate, wave, q, units);
+    v.load(gate + up_off, wave, q, units);
   }
   // x by halves (128 columns), whole rows at a time: 16 lanes copy 256 bytes of
   // a token's row, four rows an instruction and only as many as the expert
@@ -536,7 +535,7 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   };
   if (busy) {
     x_rows(static_cast<int>(task / tiles), 0);
-    x_copy(step0);
+    x_copy(wave);
   }
   int buf = 0;
   for (; task < tasks; task += gridDim.x) {
@@ -547,8 +546,8 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
     const uint8_t* next_gate = gate_row(next);
     for (int c0 = 0; c0 < count; c0 += 16, buf ^= 1) {
       float4_t ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
-      for (int hf = step0; hf < halves;) {
-        const int nh = after(hf);
+      for (int hf = wave; hf < halves;) {
+        const int nh = hf + kUpWaves;
         const bool more = nh < halves;
         // all that is in flight belongs to this half
         __builtin_amdgcn_s_waitcnt(kWaitLoads);
@@ -566,11 +565,11 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
         __builtin_amdgcn_sched_barrier(0);
         const bool again = c0 + 16 < count;
         if (!more) x_rows(again ? slot : next_slot, again ? c0 + 16 : 0);
-        x_copy(more ? nh : step0);
+        x_copy(more ? nh : wave);
         const uint8_t* ng = more || again ? gate : next_gate;
         Half<FMT> g2, v2;
-        g2.load(ng, more ? nh : step0, q, units);
-        v2.load(ng + up_off, more ? nh : step0, q, units);
+        g2.load(ng, more ? nh : wave, q, units);
+        v2.load(ng + up_off, more ? nh : wave, q, units);
         g.finish(hf, q, units);
         v.finish(hf, q, units);
         quarters4x4(g.raw);
@@ -640,14 +639,14 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
     __syncthreads();
   }
   const int active = table.active;
-  const int units = a.inter / 32, halves = (units + 3) / 4, steps = (halves + 1) / 2;
-  // slices of whole super-blocks: as many as give every wave work, evenly
+  const int units = a.inter / 32, halves = (units + 3) / 4;
+  // Slice i of a row is its halves i, i + slices, ...: neighbouring waves load
+  // the two halves of a super-block, which share its lines, at the same time.
+  // As many slices as give every wave work, evenly, and two at least.
   int slices = active > 0 ? (2 * kDownWaves + active - 1) / active : 1;
+  slices = slices < 2 ? 2 : slices;
   slices = slices < max_slices ? slices : max_slices;
-  slices = slices < steps ? slices : steps;
-  int per = (steps + slices - 1) / slices;
-  slices = (steps + per - 1) / per;
-  per *= 2;  // in halves
+  slices = slices < halves ? slices : halves;
   const int row0 = blockIdx.x * 16, tasks = active * slices;
   auto row = [&](int task) {
     return a.down + (static_cast<int64_t>(table.expert[task / slices]) * a.hidden + row0 + r) * a.down_row_bytes;
@@ -677,22 +676,21 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
   const uint8_t* w = nullptr;
   if (task < tasks) {
     w = row(task);
-    s.load(w, task % slices * per, q, units);
+    s.load(w, task % slices, q, units);
     h_rows(task / slices, 0);
-    h_load(task % slices * per, ha);
+    h_load(task % slices, ha);
   }
   for (; task < tasks; task += kDownWaves) {
     const int slot = task / slices, slice = task - slot * slices;
     const int first = table.off[slot], count = table.off[slot + 1] - first;
-    const int h0 = slice * per, h1 = h0 + per < halves ? h0 + per : halves;
     const int next = task + kDownWaves < tasks ? task + kDownWaves : task;
     const uint8_t* next_w = row(next);
     for (int c0 = 0; c0 < count; c0 += 16) {
       float4_t acc = {0, 0, 0, 0};
-      for (int hf = h0; hf < h1; hf++) {
+      for (int hf = slice; hf < halves; hf += slices) {
         // the next half, of this task or the next, while this one is multiplied
-        const bool more = hf + 1 < h1, again = c0 + 16 < count;
-        const int to = more ? hf + 1 : again ? h0 : next % slices * per;
+        const bool more = hf + slices < halves, again = c0 + 16 < count;
+        const int to = more ? hf + slices : again ? slice : next % slices;
         if (!more) h_rows(again ? slot : next / slices, again ? c0 + 16 : 0);
         u32x4 hn[4][2];
         h_load(to, hn);
