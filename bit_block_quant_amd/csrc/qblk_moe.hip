@@ -12,14 +12,17 @@
 // expert's weights are read once for all of them; the codes are decoded into
 // registers in the operand layout of the 16x16x32 matrix instructions.
 //
-// Layout.  Four units of 32 weights of a row are one 16-byte load each in the
-// four lane quarters; a 4 x 4 exchange between the quarters (v_permlane swaps)
-// turns them into one unit per register with its four dwords over the
-// quarters, which is a matrix operand: quarter q holds weights 4q..4q+3 (low
-// nibbles) and 16+4q..16+4q+3 (high).  The other operand is read from memory
-// in that order.  A code byte 0..15 is the e4m3 number code * 2^-9 as it
-// stands (subnormals below 8, the first binade from 8 on), so one conversion
-// with scale 2^9 gives two exact codes as f16 or bf16.
+// Layout.  Weights are loaded by halves of a super-block (128 columns) of 16
+// rows: four neighbouring lanes load the four units of 32 of one row, 64
+// consecutive bytes, and the scale of their unit.  (In operand order, with
+// neighbouring lanes in different rows, every lane is an access of its own to
+// the vector cache, which then bounds the kernel: 581 accesses instead of
+// about 150 per half of a gate and an up tile.)  Through 1.5 KB of LDS per
+// wave they become matrix operands: quarter q of the lanes holds weights
+// 4q..4q+3 (low nibbles) and 16+4q..16+4q+3 (high) of a unit.  The other
+// operand is brought into that order too.  A code byte 0..15 is the e4m3
+// number code * 2^-9 as it stands (subnormals below 8, the first binade from 8
+// on), so one conversion with scale 2^9 gives two exact codes as f16 or bf16.
 //
 // Sums.  Codes and activations are exact in the operands, products and sums
 // fp32.  The offset of the format (-8, or the affine formats' own) multiplies
@@ -98,148 +101,144 @@ __device__ __forceinline__ u32x4 codes8_op(uint32_t t) {
   return u32x4{Op<F16>::two(lo, false), Op<F16>::two(lo, true), Op<F16>::two(hi, false), Op<F16>::two(hi, true)};
 }
 
-// reg d of quarter q -> reg q of quarter d
-__device__ __forceinline__ void quarters4x4(uint32_t v[4]) {
-#pragma unroll
-  for (int d = 0; d < 2; d++) {
-    const auto r = __builtin_amdgcn_permlane32_swap(v[d], v[d + 2], false, false);
-    v[d] = r[0];
-    v[d + 2] = r[1];
-  }
-#pragma unroll
-  for (int d = 0; d < 4; d += 2) {
-    const auto r = __builtin_amdgcn_permlane16_swap(v[d], v[d + 1], false, false);
-    v[d] = r[0];
-    v[d + 1] = r[1];
-  }
-}
-
 // ------------------------------------------------------------- the formats
-// 128 weights (4 units) of one row per lane row, the codes of unit q in lane
-// quarter q: what is loaded (`load`, half super-block `hf` of the row), and
-// after `finish` unit u's scale and offset.  `units` is the number of units
-// of a row: Q4_0 rows may end inside a half; units past the end repeat the
-// last one's codes and scale by zero.
+// One unit of 32 weights per lane: unit u = lane & 3 of half super-block hf
+// of row lane >> 2.  `load` fetches it, scale() and offset() decode its scale
+// (weight = scale * code + offset, for the formats with affine = false offset
+// is -8 * scale and not formed).  `units` is the number of units of a row:
+// only Q4_0 rows may end inside a half; units past the end repeat the last
+// one's codes and scale by zero.
 template <int FMT>
-struct Half;
+struct Unit;
 
 template <>
-struct Half<QBLK_SB4> {
+struct Unit<QBLK_SB4> {
   static constexpr bool affine = false;
-  uint32_t raw[4], h[3];
-  __device__ __forceinline__ void load(const uint8_t* row, int hf, int q, int) {
+  uint32_t raw[4], s, c;
+  __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int) {
     const uint8_t* p = row + static_cast<int64_t>(hf >> 1) * 138;
-    load16_a2(p + 10 + 64 * (hf & 1) + 16 * q, raw);
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    const u32x3_a4 v = *reinterpret_cast<const u32x3_a4*>(a & ~uintptr_t(3));
-    const uint32_t sh = static_cast<uint32_t>(a & 3u);
-    h[0] = __builtin_amdgcn_alignbyte(v.y, v.x, sh);
-    h[1] = __builtin_amdgcn_alignbyte(v.z, v.y, sh);
-    h[2] = v.z >> (8 * sh);
+    const int j = 4 * (hf & 1) + u;
+    load16_a2(p + 10 + 16 * j, raw);
+    s = load_u16(p);
+    c = p[2 + j];
   }
-  __device__ __forceinline__ void finish(int hf, int, int) {  // h[1]: the half's four sub-scales
-    h[1] = (hf & 1) ? __builtin_amdgcn_alignbyte(h[2], h[1], 2) : __builtin_amdgcn_alignbyte(h[1], h[0], 2);
+  __device__ __forceinline__ float scale(int, int, int) const {
+    return f16_bits_to_f32(s) * static_cast<float>(static_cast<int8_t>(c));
   }
-  __device__ __forceinline__ float scale(int u) const {
-    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(static_cast<int8_t>(h[1] >> (8 * u)));
-  }
-  __device__ __forceinline__ float offset(int) const { return 0.0f; }
+  __device__ __forceinline__ float offset(int, int) const { return 0.0f; }
 };
 
 template <>
-struct Half<QBLK_SB4_AFFINE> {
+struct Unit<QBLK_SB4_AFFINE> {
   static constexpr bool affine = true;
-  uint32_t raw[4], h[3];
-  __device__ __forceinline__ void load(const uint8_t* row, int hf, int q, int) {
-    const uint8_t* p = row + static_cast<int64_t>(hf >> 1) * 148;  // a multiple of 4: every field is dword aligned
-    const u32x4_a4 a = *reinterpret_cast<const u32x4_a4*>(p + 20 + 64 * (hf & 1) + 16 * q);
+  uint32_t raw[4], s, c, o;
+  __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int) {
+    const uint8_t* p = row + static_cast<int64_t>(hf >> 1) * 148;  // a multiple of 4: codes are dword aligned
+    const int j = 4 * (hf & 1) + u;
+    const u32x4_a4 a = *reinterpret_cast<const u32x4_a4*>(p + 20 + 16 * j);
 #pragma unroll
     for (int i = 0; i < 4; i++) raw[i] = a[i];
-    h[0] = *reinterpret_cast<const uint32_t*>(p);
-    h[1] = *reinterpret_cast<const uint32_t*>(p + 4 + 4 * (hf & 1));
-    h[2] = *reinterpret_cast<const uint32_t*>(p + 12 + 4 * (hf & 1));
+    s = *reinterpret_cast<const uint32_t*>(p);
+    c = p[4 + j];
+    o = p[12 + j];
   }
-  __device__ __forceinline__ void finish(int, int, int) {}
-  __device__ __forceinline__ float scale(int u) const {
-    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>(static_cast<int8_t>(h[1] >> (8 * u)));
+  __device__ __forceinline__ float scale(int, int, int) const {
+    return f16_bits_to_f32(s & 0xffffu) * static_cast<float>(static_cast<int8_t>(c));
   }
-  __device__ __forceinline__ float offset(int u) const {
-    return f16_bits_to_f32(h[0] >> 16) * static_cast<float>(static_cast<int8_t>(h[2] >> (8 * u)));
+  __device__ __forceinline__ float offset(int, int) const {
+    return f16_bits_to_f32(s >> 16) * static_cast<float>(static_cast<int8_t>(o));
   }
 };
 
 template <>
-struct Half<QBLK_Q4_K> {
+struct Unit<QBLK_Q4_K> {
   static constexpr bool affine = true;
-  uint32_t raw[4], h[4];
-  __device__ __forceinline__ void load(const uint8_t* row, int hf, int q, int) {
+  uint32_t raw[4], h;
+  __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int) {
     const u32x4* p = reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(hf >> 1) * 144);  // 16-byte aligned
-    const u32x4 a = p[1 + 4 * (hf & 1) + q], c = p[0];
+    const u32x4 a = p[1 + 4 * (hf & 1) + u];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      raw[i] = a[i];
-      h[i] = c[i];
-    }
+    for (int i = 0; i < 4; i++) raw[i] = a[i];
+    h = reinterpret_cast<const uint32_t*>(p)[u];  // a dword of the header each
   }
-  // the half's 6-bit scales to h[1], mins to h[2]: fields 4j .. 4j+3 are bits
-  // 24j .. 24j+23 of h1:h2:h3, the mins 48 bits further on
-  __device__ __forceinline__ void finish(int hf, int, int) {
-    const uint32_t s = (hf & 1) ? (h[1] >> 24) | (h[2] << 8) : h[1];
-    const uint32_t m = (hf & 1) ? h[3] >> 8 : (h[2] >> 16) | (h[3] << 16);
-    h[1] = s;
-    h[2] = m;
+  template <int I>
+  __device__ __forceinline__ uint32_t head() const {  // dword I of it, from lane I of the four
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(h), I * 0x55, 0xF, 0xF, true));
   }
-  __device__ __forceinline__ float scale(int u) const {
-    return f16_bits_to_f32(h[0] & 0xffffu) * static_cast<float>((h[1] >> (6 * u)) & 63u);
+  __device__ __forceinline__ float scale(int hf, int u, int) const {
+    return f16_bits_to_f32(head<0>() & 0xffffu) * static_cast<float>(q4k_scale6(head<1>(), head<2>(), 4 * (hf & 1) + u));
   }
-  __device__ __forceinline__ float offset(int u) const {
-    return -(f16_bits_to_f32(h[0] >> 16) * static_cast<float>((h[2] >> (6 * u)) & 63u));
+  __device__ __forceinline__ float offset(int hf, int u) const {
+    return -(f16_bits_to_f32(head<0>() >> 16) * static_cast<float>(q4k_min6(head<2>(), head<3>(), 4 * (hf & 1) + u)));
   }
 };
 
 template <>
-struct Half<QBLK_Q4_0> {
+struct Unit<QBLK_Q4_0> {
   static constexpr bool affine = false;
-  uint32_t raw[4], d[4];
-  __device__ __forceinline__ void load(const uint8_t* row, int hf, int q, int units) {
-    const int u = 4 * hf + q;
-    const uint8_t* p = row + static_cast<int64_t>(u < units ? u : units - 1) * 18;
+  uint32_t raw[4], d;
+  __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int units) {
+    const int at = 4 * hf + u;
+    const uint8_t* p = row + static_cast<int64_t>(at < units ? at : units - 1) * 18;
     load16_a2(p + 2, raw);
-    d[0] = load_u16(p);
+    d = load_u16(p);
   }
-  // the scales of all four units to every quarter
-  __device__ __forceinline__ void finish(int hf, int q, int units) {
-    d[0] = 4 * hf + q < units ? d[0] : 0u;
-    d[1] = d[2] = d[3] = d[0];
-    quarters4x4(d);
+  __device__ __forceinline__ float scale(int hf, int u, int units) const {
+    return 4 * hf + u < units ? f16_bits_to_f32(d) : 0.0f;
   }
-  __device__ __forceinline__ float scale(int u) const { return f16_bits_to_f32(d[u]); }
-  __device__ __forceinline__ float offset(int) const { return 0.0f; }
+  __device__ __forceinline__ float offset(int, int) const { return 0.0f; }
 };
+
+// The exchange of one half of 16 rows from units per lane to operands, in a
+// wave's own LDS (its accesses there are executed in order).
+struct Stage {
+  u32x4 codes[64];  // row, unit ^ (row >> 2 & 3): the 16 rows' dwords of one unit lie in different banks
+  float scale[64], offset[64];
+};
+// One row of 128 weights per lane row: unit u's dword of this quarter, scales, offsets.
+struct Operand {
+  uint32_t t[4];
+  float4_t s, o;
+};
+template <int FMT>
+__device__ __forceinline__ Operand to_operand(const Unit<FMT>& w, int hf, int units, Stage& st) {
+  const int lane = threadIdx.x & 63, row = lane >> 2, u = lane & 3, r = lane & 15, q = lane >> 4;
+  st.codes[4 * row + (u ^ ((row >> 2) & 3))] = u32x4{w.raw[0], w.raw[1], w.raw[2], w.raw[3]};
+  st.scale[lane] = w.scale(hf, u, units);
+  if constexpr (Unit<FMT>::affine) st.offset[lane] = w.offset(hf, u);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  Operand p;
+  const uint32_t* c = reinterpret_cast<const uint32_t*>(st.codes);
+#pragma unroll
+  for (int i = 0; i < 4; i++) p.t[i] = c[16 * r + 4 * (i ^ ((r >> 2) & 3)) + q];
+  p.s = *reinterpret_cast<const float4_t*>(st.scale + 4 * r);
+  if constexpr (Unit<FMT>::affine) p.o = *reinterpret_cast<const float4_t*>(st.offset + 4 * r);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  return p;
+}
 
 // acc += (unit u of 16 rows) x (16 gathered token rows), the operand in PARTS summands
 template <int FMT, bool F16, int PARTS>
-__device__ __forceinline__ void mul_unit(const Half<FMT>& w, int u, uint32_t codes, const u32x4 (&a)[PARTS],
-                                         const float4_t& xs, float4_t& acc) {
-  const u32x4 b = codes8_op<F16>(codes);
-  float4_t p = Half<FMT>::affine ? float4_t{0, 0, 0, 0} : xs;
+__device__ __forceinline__ void mul_unit(const Operand& w, int u, const u32x4 (&a)[PARTS], const float4_t& xs,
+                                         float4_t& acc) {
+  const u32x4 b = codes8_op<F16>(w.t[u]);
+  float4_t p = Unit<FMT>::affine ? float4_t{0, 0, 0, 0} : xs;
 #pragma unroll
   for (int i = 0; i < PARTS; i++) p = Op<F16>::mma(a[i], b, p);
-  const float s = w.scale(u);
-  if constexpr (Half<FMT>::affine) {
-    const float o = w.offset(u);
 #pragma unroll
-    for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(o, xs[i], __builtin_fmaf(s, p[i], acc[i]));
-  } else {
+  for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(w.s[u], p[i], acc[i]);
+  if constexpr (Unit<FMT>::affine) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(s, p[i], acc[i]);
+    for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(w.o[u], xs[i], acc[i]);
   }
 }
 
 // sum(x) of the unit per token (times -8 for the formats whose offset that is)
 template <int FMT, bool F16, int PARTS>
 __device__ __forceinline__ float4_t unit_sum(const u32x4 (&a)[PARTS]) {
-  const uint32_t c = Half<FMT>::affine ? Op<F16>::one2 : Op<F16>::minus8;
+  const uint32_t c = Unit<FMT>::affine ? Op<F16>::one2 : Op<F16>::minus8;
   float4_t p = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < PARTS; i++) p = Op<F16>::mma(a[i], u32x4{c, c, c, c}, p);
@@ -437,19 +436,27 @@ __device__ void build_table(int pairs, int experts, Table& t, TableScratch& z) {
 // --------------------------------------------------------------- gate, up
 // A workgroup takes tiles of 16 gate rows and the 16 up rows that go with
 // them, for all tokens of one expert; its waves split the columns (wave w
-// takes 256-column super-blocks w, w + 8, ...) and their sums meet in LDS.
+// takes halves w, w + 8, ...) and their sums meet in LDS.
 // Workgroups are persistent, so the routing is worked out once in each rather
 // than by a launch of its own.
 template <int FMT, bool F16>
 __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
+  // two workgroups to a CU: at most 80 KB each
   __shared__ Table table;
-  __shared__ float4_t red[2][kUpWaves][2][64];
-  __shared__ u32x4 xbuf[kUpWaves][256];
-  TableScratch& scratch = *reinterpret_cast<TableScratch*>(red);  // before the first tile
-  static_assert(sizeof red >= sizeof(TableScratch));
+  struct Tiles {
+    float4_t red[kUpWaves][2][64];
+    u32x4 x[kUpWaves][256];
+    Stage stage[kUpWaves];
+  };
+  __shared__ union {
+    Tiles tiles;
+    TableScratch scratch;  // before the first tile
+  } lds;
+  static_assert(sizeof lds + sizeof table <= 80 * 1024);
+  TableScratch& scratch = lds.scratch;
   int* const ids = scratch.ids;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4;
+  const int r = lane & 15, q = lane >> 4, wrow = lane >> 2, wu = lane & 3;
   const int pairs = a.n * a.top_k;
 
   if (a.logits != nullptr) {
@@ -493,23 +500,25 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   const int64_t up_off = static_cast<int64_t>(a.inter) * a.up_row_bytes;
   auto gate_row = [&](int64_t task) {
     const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
-    return a.gate_up + (static_cast<int64_t>(table.expert[slot]) * 2 * a.inter + 16 * tile + r) * a.up_row_bytes;
+    return a.gate_up + (static_cast<int64_t>(table.expert[slot]) * 2 * a.inter + 16 * tile + wrow) * a.up_row_bytes;
   };
   int64_t task = blockIdx.x;
   if (task >= tasks) return;
   // Weights and activations are loaded one half ahead, across tiles too.
   const uint8_t* gate = gate_row(task);
-  Half<FMT> g, v;
+  Unit<FMT> g, v;
   if (busy) {
-    g.load(gate, wave, q, units);
-    v.load(gate + up_off, wave, q, units);
+    g.load(gate, wave, wu, units);
+    v.load(gate + up_off, wave, wu, units);
   }
   // x by halves (128 columns), whole rows at a time: 16 lanes copy 256 bytes of
   // a token's row, four rows an instruction and only as many as the expert
   // has, straight to LDS, where they are read as operands.  (Loaded as
   // operands from memory, 16 rows lie 2 * hidden bytes apart and every load
   // asks for 16 lines.)
-  u32x4* const xw = xbuf[wave];
+  u32x4* const xw = lds.tiles.x[wave];
+  Stage& stage = lds.tiles.stage[wave];
+  auto& red = lds.tiles.red;
   const uint8_t* xrow[4];
   int xrows = 0;
   auto x_rows = [&](int slot, int c0) {  // pairs c0 .. c0+15 of the expert; past its last one that again
@@ -537,14 +546,13 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
     x_rows(static_cast<int>(task / tiles), 0);
     x_copy(wave);
   }
-  int buf = 0;
   for (; task < tasks; task += gridDim.x) {
     const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
     const int first = table.off[slot], count = table.off[slot + 1] - first;
     const int64_t next = task + gridDim.x < tasks ? task + gridDim.x : task;
     const int next_slot = static_cast<int>(next / tiles);
     const uint8_t* next_gate = gate_row(next);
-    for (int c0 = 0; c0 < count; c0 += 16, buf ^= 1) {
+    for (int c0 = 0; c0 < count; c0 += 16) {
       float4_t ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
       for (int hf = wave; hf < halves;) {
         const int nh = hf + kUpWaves;
@@ -567,27 +575,25 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
         if (!more) x_rows(again ? slot : next_slot, again ? c0 + 16 : 0);
         x_copy(more ? nh : wave);
         const uint8_t* ng = more || again ? gate : next_gate;
-        Half<FMT> g2, v2;
-        g2.load(ng, more ? nh : wave, q, units);
-        v2.load(ng + up_off, more ? nh : wave, q, units);
-        g.finish(hf, q, units);
-        v.finish(hf, q, units);
-        quarters4x4(g.raw);
-        quarters4x4(v.raw);
+        Unit<FMT> g2, v2;
+        g2.load(ng, more ? nh : wave, wu, units);
+        v2.load(ng + up_off, more ? nh : wave, wu, units);
+        const Operand go = to_operand(g, hf, units, stage);
+        const Operand vo = to_operand(v, hf, units, stage);
 #pragma unroll
         for (int u = 0; u < 4; u++) {
           const u32x4 op[1] = {xa[u]};
           const float4_t xs = unit_sum<FMT, F16, 1>(op);
-          mul_unit<FMT, F16, 1>(g, u, g.raw[u], op, xs, ga);
-          mul_unit<FMT, F16, 1>(v, u, v.raw[u], op, xs, ua);
+          mul_unit<FMT, F16, 1>(go, u, op, xs, ga);
+          mul_unit<FMT, F16, 1>(vo, u, op, xs, ua);
         }
         g = g2;
         v = v2;
         hf = nh;
       }
-      red[buf][wave][0][lane] = ga;
-      red[buf][wave][1][lane] = ua;
-      __syncthreads();  // the other buffer's readers are past it by the next one
+      red[wave][0][lane] = ga;
+      red[wave][1][lane] = ua;
+      __syncthreads();
       // lane (row r, quarter q) of the sums holds tokens 4q .. 4q+3
       if (threadIdx.x < 256) {
         const int tok = threadIdx.x >> 4, rr = threadIdx.x & 15;
@@ -595,19 +601,20 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
           float gs = 0.0f, us = 0.0f;
 #pragma unroll
           for (int w = 0; w < kUpWaves; w++) {
-            gs += red[buf][w][0][(tok >> 2) * 16 + rr][tok & 3];
-            us += red[buf][w][1][(tok >> 2) * 16 + rr][tok & 3];
+            gs += red[w][0][(tok >> 2) * 16 + rr][tok & 3];
+            us += red[w][1][(tok >> 2) * 16 + rr][tok & 3];
           }
           const float h = silu_mul(gs, us);
           const uint16_t hi = f32_to_bf16_bits(h);
           const float rest = h - bf16_bits_to_f32(hi);
-          // operand order, see h_load: unit tile/2 of this expert's pairs
-          uint16_t* out = reinterpret_cast<uint16_t*>(a.h) + static_cast<int64_t>(first) * a.inter * 2 +
-                          (static_cast<int64_t>(tile & ~1) * count + c0 + tok) * 32 + 8 * (rr >> 2) + 4 * (tile & 1) + (rr & 3);
+          // operand order, see h_rows in k_moe_down: unit tile/2 of this expert's pairs
+          uint16_t* out = static_cast<uint16_t*>(a.h) + static_cast<int64_t>(first) * a.inter * 2 +
+                          (static_cast<int64_t>((tile & ~1) * 4 + (rr >> 2)) * count + c0 + tok) * 8 + 4 * (tile & 1) + (rr & 3);
           out[0] = hi;
           out[static_cast<int64_t>(count) * 32] = __builtin_isfinite(rest) ? f32_to_bf16_bits(rest) : 0;
         }
       }
+      __syncthreads();
     }
     gate = next_gate;
   }
@@ -623,8 +630,10 @@ template <int FMT>
 __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int max_slices) {
   extern __shared__ __align__(16) float slots[];  // [slice][pair][16]
   __shared__ Table table;
+  __shared__ Stage stages[kDownWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4;
+  const int r = lane & 15, q = lane >> 4, wrow = lane >> 2, wu = lane & 3;
+  Stage& stage = stages[wave];
   const int pairs = a.n * a.top_k;
   {
     // all of the table at once: it is read by one round trip, not by three
@@ -649,17 +658,17 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
   slices = slices < halves ? slices : halves;
   const int row0 = blockIdx.x * 16, tasks = active * slices;
   auto row = [&](int task) {
-    return a.down + (static_cast<int64_t>(table.expert[task / slices]) * a.hidden + row0 + r) * a.down_row_bytes;
+    return a.down + (static_cast<int64_t>(table.expert[task / slices]) * a.hidden + row0 + wrow) * a.down_row_bytes;
   };
   // h of an expert's pairs is stored as operands: per unit of 32 columns the hi
-  // parts of all pairs, then the lo parts, 64 bytes a pair (16 per lane
-  // quarter).  Lanes past the last pair repeat it: not used.
+  // parts, then the lo parts, each per lane quarter 16 bytes of every pair.
+  // Lanes past the last pair repeat it: not used.
   const uint8_t* h = nullptr;
   int64_t hstep = 0;
   auto h_rows = [&](int slot, int c0) {
     const int first = table.off[slot], count = table.off[slot + 1] - first;
     h = static_cast<const uint8_t*>(a.h) + static_cast<int64_t>(first) * a.inter * 4 +
-        (c0 + r < count ? c0 + r : count - 1) * 64 + 16 * q;
+        (static_cast<int64_t>(q) * count + (c0 + r < count ? c0 + r : count - 1)) * 16;
     hstep = static_cast<int64_t>(count) * 64;
   };
   auto h_load = [&](int hf, u32x4(&to)[4][2]) {
@@ -671,12 +680,12 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
     }
   };
   int task = wave;
-  Half<FMT> s;
+  Unit<FMT> s;
   u32x4 ha[4][2];
   const uint8_t* w = nullptr;
   if (task < tasks) {
     w = row(task);
-    s.load(w, task % slices, q, units);
+    s.load(w, task % slices, wu, units);
     h_rows(task / slices, 0);
     h_load(task % slices, ha);
   }
@@ -694,14 +703,13 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
         if (!more) h_rows(again ? slot : next / slices, again ? c0 + 16 : 0);
         u32x4 hn[4][2];
         h_load(to, hn);
-        Half<FMT> s2;
-        s2.load(more || again ? w : next_w, to, q, units);
-        s.finish(hf, q, units);
-        quarters4x4(s.raw);
+        Unit<FMT> s2;
+        s2.load(more || again ? w : next_w, to, wu, units);
+        const Operand so = to_operand(s, hf, units, stage);
 #pragma unroll
         for (int u = 0; u < 4; u++) {
           const float4_t xs = unit_sum<FMT, false, 2>(ha[u]);
-          mul_unit<FMT, false, 2>(s, u, s.raw[u], ha[u], xs, acc);
+          mul_unit<FMT, false, 2>(so, u, ha[u], xs, acc);
         }
         s = s2;
 #pragma unroll
