@@ -43,15 +43,10 @@ typedef half_t half8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kUpWaves = 8;     // waves that share the columns of one tile
+constexpr int kSplit = 4;       // waves that share the columns of one tile of gate or up rows
+constexpr int kUpWaves = 2 * kSplit;
 constexpr int kDownWaves = 16;  // waves that share the experts of one tile
 constexpr uint32_t kLo4 = 0x0F0F0F0Fu;
-
-typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void glob_void;
-// s_waitcnt immediates (gfx9: vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt
-// 11:8): no vector memory, or no LDS access, in flight
-constexpr int kWaitLoads = 0x0F70, kWaitLds = 0xC07F;
 
 // The routing of one piece, in LDS or in the workspace: experts with at least
 // one pair are slots 0 .. active-1; slot s owns list[off[s] .. off[s+1]).
@@ -111,17 +106,36 @@ __device__ __forceinline__ u32x4 codes8_op(uint32_t t) {
 template <int FMT>
 struct Unit;
 
+// 16 bytes at a 2-byte aligned address, put in order only when they are used
+// (load16_a2 in two steps: the first does not wait for its loads)
+struct Raw16 {
+  u32x4_a4 v;
+  uint32_t tail, shift;
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    v = *reinterpret_cast<const u32x4_a4*>(a & ~uintptr_t(3));
+    tail = *reinterpret_cast<const uint16_t*>(p + 14);
+    shift = static_cast<uint32_t>(a & 3u);  // 0 or 2
+  }
+  __device__ __forceinline__ u32x4 get() const {
+    return u32x4{__builtin_amdgcn_alignbyte(v.y, v.x, shift), __builtin_amdgcn_alignbyte(v.z, v.y, shift),
+                 __builtin_amdgcn_alignbyte(v.w, v.z, shift), __builtin_amdgcn_alignbyte(tail, v.w, shift)};
+  }
+};
+
 template <>
 struct Unit<QBLK_SB4> {
   static constexpr bool affine = false;
-  uint32_t raw[4], s, c;
+  Raw16 raw;
+  uint32_t s, c;
   __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int) {
     const uint8_t* p = row + static_cast<int64_t>(hf >> 1) * 138;
     const int j = 4 * (hf & 1) + u;
-    load16_a2(p + 10 + 16 * j, raw);
+    raw.load(p + 10 + 16 * j);
     s = load_u16(p);
     c = p[2 + j];
   }
+  __device__ __forceinline__ u32x4 codes() const { return raw.get(); }
   __device__ __forceinline__ float scale(int, int, int) const {
     return f16_bits_to_f32(s) * static_cast<float>(static_cast<int8_t>(c));
   }
@@ -131,13 +145,13 @@ struct Unit<QBLK_SB4> {
 template <>
 struct Unit<QBLK_SB4_AFFINE> {
   static constexpr bool affine = true;
-  uint32_t raw[4], s, c, o;
+  u32x4_a4 raw;
+  uint32_t s, c, o;
+  __device__ __forceinline__ u32x4 codes() const { return raw; }
   __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int) {
     const uint8_t* p = row + static_cast<int64_t>(hf >> 1) * 148;  // a multiple of 4: codes are dword aligned
     const int j = 4 * (hf & 1) + u;
-    const u32x4_a4 a = *reinterpret_cast<const u32x4_a4*>(p + 20 + 16 * j);
-#pragma unroll
-    for (int i = 0; i < 4; i++) raw[i] = a[i];
+    raw = *reinterpret_cast<const u32x4_a4*>(p + 20 + 16 * j);
     s = *reinterpret_cast<const uint32_t*>(p);
     c = p[4 + j];
     o = p[12 + j];
@@ -153,12 +167,12 @@ struct Unit<QBLK_SB4_AFFINE> {
 template <>
 struct Unit<QBLK_Q4_K> {
   static constexpr bool affine = true;
-  uint32_t raw[4], h;
+  u32x4 raw;
+  uint32_t h;
+  __device__ __forceinline__ u32x4 codes() const { return raw; }
   __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int) {
     const u32x4* p = reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(hf >> 1) * 144);  // 16-byte aligned
-    const u32x4 a = p[1 + 4 * (hf & 1) + u];
-#pragma unroll
-    for (int i = 0; i < 4; i++) raw[i] = a[i];
+    raw = p[1 + 4 * (hf & 1) + u];
     h = reinterpret_cast<const uint32_t*>(p)[u];  // a dword of the header each
   }
   template <int I>
@@ -176,11 +190,13 @@ struct Unit<QBLK_Q4_K> {
 template <>
 struct Unit<QBLK_Q4_0> {
   static constexpr bool affine = false;
-  uint32_t raw[4], d;
+  Raw16 raw;
+  uint32_t d;
+  __device__ __forceinline__ u32x4 codes() const { return raw.get(); }
   __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int units) {
     const int at = 4 * hf + u;
     const uint8_t* p = row + static_cast<int64_t>(at < units ? at : units - 1) * 18;
-    load16_a2(p + 2, raw);
+    raw.load(p + 2);
     d = load_u16(p);
   }
   __device__ __forceinline__ float scale(int hf, int u, int units) const {
@@ -203,7 +219,7 @@ struct Operand {
 template <int FMT>
 __device__ __forceinline__ Operand to_operand(const Unit<FMT>& w, int hf, int units, Stage& st) {
   const int lane = threadIdx.x & 63, row = lane >> 2, u = lane & 3, r = lane & 15, q = lane >> 4;
-  st.codes[4 * row + (u ^ ((row >> 2) & 3))] = u32x4{w.raw[0], w.raw[1], w.raw[2], w.raw[3]};
+  st.codes[4 * row + (u ^ ((row >> 2) & 3))] = w.codes();
   st.scale[lane] = w.scale(hf, u, units);
   if constexpr (Unit<FMT>::affine) st.offset[lane] = w.offset(hf, u);
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -435,16 +451,18 @@ __device__ void build_table(int pairs, int experts, Table& t, TableScratch& z) {
 
 // --------------------------------------------------------------- gate, up
 // A workgroup takes tiles of 16 gate rows and the 16 up rows that go with
-// them, for all tokens of one expert; its waves split the columns (wave w
-// takes halves w, w + 8, ...) and their sums meet in LDS.
-// Workgroups are persistent, so the routing is worked out once in each rather
-// than by a launch of its own.
+// them, for all tokens of one expert.  Four waves work on the gate rows, four
+// on the up rows; the four split the columns (wave k takes halves k, k + 4,
+// ...) and their sums meet in LDS.  One tile per wave leaves the registers for
+// weights two halves ahead of the multiply: what bounds the kernel is how many
+// bytes are on their way.  Workgroups are persistent, so the routing is worked
+// out once in each rather than by a launch of its own.
 template <int FMT, bool F16>
 __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   // two workgroups to a CU: at most 80 KB each
   __shared__ Table table;
   struct Tiles {
-    float4_t red[kUpWaves][2][64];
+    float4_t red[kUpWaves][64];
     u32x4 x[kUpWaves][256];
     Stage stage[kUpWaves];
   };
@@ -494,43 +512,57 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
 
   const int tiles = a.inter / 16, units = a.hidden / 32, halves = (units + 3) / 4;
   const int64_t tasks = static_cast<int64_t>(table.active) * tiles;
-  // The waves take a row's halves in turn: the two halves of a super-block,
-  // which share its lines, are loaded by neighbours at the same time.
-  const bool busy = wave < halves;
-  const int64_t up_off = static_cast<int64_t>(a.inter) * a.up_row_bytes;
-  auto gate_row = [&](int64_t task) {
-    const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
-    return a.gate_up + (static_cast<int64_t>(table.expert[slot]) * 2 * a.inter + 16 * tile + wrow) * a.up_row_bytes;
-  };
-  int64_t task = blockIdx.x;
-  if (task >= tasks) return;
-  // Weights and activations are loaded one half ahead, across tiles too.
-  const uint8_t* gate = gate_row(task);
-  Unit<FMT> g, v;
-  if (busy) {
-    g.load(gate, wave, wu, units);
-    v.load(gate + up_off, wave, wu, units);
-  }
-  // x by halves (128 columns), whole rows at a time: 16 lanes copy 256 bytes of
-  // a token's row, four rows an instruction and only as many as the expert
-  // has, straight to LDS, where they are read as operands.  (Loaded as
-  // operands from memory, 16 rows lie 2 * hidden bytes apart and every load
-  // asks for 16 lines.)
+  if (blockIdx.x >= tasks) return;
+  const int side = wave / kSplit, part = wave % kSplit;  // gate or up; share of the columns
+  const bool busy = part < halves;
   u32x4* const xw = lds.tiles.x[wave];
   Stage& stage = lds.tiles.stage[wave];
   auto& red = lds.tiles.red;
-  const uint8_t* xrow[4];
+
+  // A place in the sequence of halves that this wave multiplies: for its
+  // workgroup's tiles, each expert's pairs 16 at a time, halves part, part +
+  // kSplit, ...  At the end it stays at the last tile (loaded, not used).
+  struct Place {
+    int64_t task;
+    int slot, first, count, c0, hf;
+  };
+  auto at_task = [&](Place& p, int64_t task) {
+    p.task = task;
+    p.slot = __builtin_amdgcn_readfirstlane(static_cast<int>(task / tiles));
+    p.first = __builtin_amdgcn_readfirstlane(table.off[p.slot]);
+    p.count = __builtin_amdgcn_readfirstlane(table.off[p.slot + 1]) - p.first;
+    p.c0 = 0;
+  };
+  auto advance = [&](Place& p) {  // whether the tile or the 16 pairs changed
+    p.hf += kSplit;
+    if (p.hf < halves) return false;
+    p.hf = part;
+    p.c0 += 16;
+    if (p.c0 >= p.count) at_task(p, p.task + gridDim.x < tasks ? p.task + gridDim.x : p.task);
+    return true;
+  };
+  auto row_of = [&](const Place& p) {
+    const int tile = static_cast<int>(p.task - static_cast<int64_t>(p.slot) * tiles);
+    const int64_t e = __builtin_amdgcn_readfirstlane(table.expert[p.slot]);
+    return a.gate_up + (e * 2 * a.inter + static_cast<int64_t>(side) * a.inter + 16 * tile + wrow) * a.up_row_bytes;
+  };
+
+  // x by halves (128 columns), whole rows at a time: 16 lanes load 256 bytes of
+  // a token's row, four rows an instruction and only as many as the expert
+  // has; through LDS they become operands.  (Loaded as operands from memory,
+  // 16 rows lie 2 * hidden bytes apart and every load asks for 16 lines.)
+  int xtok[4];
   int xrows = 0;
-  auto x_rows = [&](int slot, int c0) {  // pairs c0 .. c0+15 of the expert; past its last one that again
-    const int first = table.off[slot] + c0;
-    xrows = table.off[slot + 1] - first;
+  u32x4 xr[4];
+  auto x_rows = [&](const Place& p) {  // its 16 pairs; past the last one that again
+    xrows = p.count - p.c0;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int at = 4 * i + q < xrows ? 4 * i + q : xrows - 1;
-      xrow[i] = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(table.list[first + at] / a.top_k) * a.hidden * 2;
+      xtok[i] = table.list[p.first + p.c0 + at] / a.top_k;
     }
   };
-  auto x_copy = [&](int hf) {
+  auto x_load = [&](int hf) {
     // 16-byte chunk r ^ row of the row, to LDS chunk r: 16 rows of one chunk
     // column then lie in 16 different columns of banks.  Past the row's end
     // (only Q4_0) the last chunk again: those weights scale by zero.
@@ -539,86 +571,111 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
       if (4 * i < xrows) {
         int at = 16 * hf + (r ^ (4 * i + q));
         at = at < 4 * units ? at : 4 * units - 1;
-        __builtin_amdgcn_global_load_lds((glob_void*)(xrow[i] + 16 * at), (lds_void*)(xw + 64 * i), 16, 0, 0);
+        xr[i] = *(reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(xtok[i]) * (a.hidden * 2ll)) + at);
       }
   };
-  if (busy) {
-    x_rows(static_cast<int>(task / tiles), 0);
-    x_copy(wave);
-  }
-  for (; task < tasks; task += gridDim.x) {
-    const int slot = static_cast<int>(task / tiles), tile = static_cast<int>(task - static_cast<int64_t>(slot) * tiles);
-    const int first = table.off[slot], count = table.off[slot + 1] - first;
-    const int64_t next = task + gridDim.x < tasks ? task + gridDim.x : task;
-    const int next_slot = static_cast<int>(next / tiles);
-    const uint8_t* next_gate = gate_row(next);
-    for (int c0 = 0; c0 < count; c0 += 16) {
-      float4_t ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
-      for (int hf = wave; hf < halves;) {
-        const int nh = hf + kUpWaves;
-        const bool more = nh < halves;
-        // all that is in flight belongs to this half
-        __builtin_amdgcn_s_waitcnt(kWaitLoads);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        u32x4 xa[4];
-        const uint8_t* from = reinterpret_cast<const uint8_t*>(xw) + 256 * r + 8 * (q & 1);
+
+  // The tiles' sums, put together by all waves: lane (row r, quarter q) of
+  // them holds tokens 4q .. 4q+3.
+  auto finish = [&](const Place& p, const float4_t& acc) {
+    red[wave][lane] = acc;
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      const int tok = threadIdx.x >> 4, rr = threadIdx.x & 15;
+      if (p.c0 + tok < p.count) {
+        float gs = 0.0f, us = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const u32x2 l0 = *reinterpret_cast<const u32x2*>(from + 16 * ((4 * u + (q >> 1)) ^ r));
-          const u32x2 l1 = *reinterpret_cast<const u32x2*>(from + 16 * ((4 * u + 2 + (q >> 1)) ^ r));
-          xa[u] = u32x4{l0.x, l0.y, l1.x, l1.y};
+        for (int w = 0; w < kSplit; w++) {
+          gs += red[w][(tok >> 2) * 16 + rr][tok & 3];
+          us += red[kSplit + w][(tok >> 2) * 16 + rr][tok & 3];
         }
-        __builtin_amdgcn_s_waitcnt(kWaitLds);  // read before the next half is copied over it
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_sched_barrier(0);
-        const bool again = c0 + 16 < count;
-        if (!more) x_rows(again ? slot : next_slot, again ? c0 + 16 : 0);
-        x_copy(more ? nh : wave);
-        const uint8_t* ng = more || again ? gate : next_gate;
-        Unit<FMT> g2, v2;
-        g2.load(ng, more ? nh : wave, wu, units);
-        v2.load(ng + up_off, more ? nh : wave, wu, units);
-        const Operand go = to_operand(g, hf, units, stage);
-        const Operand vo = to_operand(v, hf, units, stage);
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const u32x4 op[1] = {xa[u]};
-          const float4_t xs = unit_sum<FMT, F16, 1>(op);
-          mul_unit<FMT, F16, 1>(go, u, op, xs, ga);
-          mul_unit<FMT, F16, 1>(vo, u, op, xs, ua);
-        }
-        g = g2;
-        v = v2;
-        hf = nh;
+        const float h = silu_mul(gs, us);
+        const uint16_t hi = f32_to_bf16_bits(h);
+        const float rest = h - bf16_bits_to_f32(hi);
+        const int tile = static_cast<int>(p.task - static_cast<int64_t>(p.slot) * tiles);
+        // operand order, see h_rows in k_moe_down: unit tile/2 of this expert's pairs
+        uint16_t* out = static_cast<uint16_t*>(a.h) + static_cast<int64_t>(p.first) * a.inter * 2 +
+                        (static_cast<int64_t>((tile & ~1) * 4 + (rr >> 2)) * p.count + p.c0 + tok) * 8 + 4 * (tile & 1) + (rr & 3);
+        out[0] = hi;
+        out[static_cast<int64_t>(p.count) * 32] = __builtin_isfinite(rest) ? f32_to_bf16_bits(rest) : 0;
       }
-      red[wave][0][lane] = ga;
-      red[wave][1][lane] = ua;
-      __syncthreads();
-      // lane (row r, quarter q) of the sums holds tokens 4q .. 4q+3
-      if (threadIdx.x < 256) {
-        const int tok = threadIdx.x >> 4, rr = threadIdx.x & 15;
-        if (c0 + tok < count) {
-          float gs = 0.0f, us = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kUpWaves; w++) {
-            gs += red[w][0][(tok >> 2) * 16 + rr][tok & 3];
-            us += red[w][1][(tok >> 2) * 16 + rr][tok & 3];
-          }
-          const float h = silu_mul(gs, us);
-          const uint16_t hi = f32_to_bf16_bits(h);
-          const float rest = h - bf16_bits_to_f32(hi);
-          // operand order, see h_rows in k_moe_down: unit tile/2 of this expert's pairs
-          uint16_t* out = static_cast<uint16_t*>(a.h) + static_cast<int64_t>(first) * a.inter * 2 +
-                          (static_cast<int64_t>((tile & ~1) * 4 + (rr >> 2)) * count + c0 + tok) * 8 + 4 * (tile & 1) + (rr & 3);
-          out[0] = hi;
-          out[static_cast<int64_t>(count) * 32] = __builtin_isfinite(rest) ? f32_to_bf16_bits(rest) : 0;
-        }
-      }
-      __syncthreads();
     }
-    gate = next_gate;
+    __syncthreads();
+  };
+
+  Place p;  // what is multiplied now
+  at_task(p, blockIdx.x);
+  p.hf = part;
+  float4_t acc = {0, 0, 0, 0};
+  // after the last half of 16 pairs: their sums; false after the last tile
+  auto next_pairs = [&]() {
+    finish(p, acc);
+    acc = float4_t{0, 0, 0, 0};
+    const int64_t done = p.task;
+    p.c0 += 16;
+    if (p.c0 < p.count) return true;
+    if (done + gridDim.x >= tasks) return false;
+    at_task(p, done + gridDim.x);
+    return true;
+  };
+  if (!busy) {
+    while (next_pairs()) {
+    }
+    return;
   }
-  __builtin_amdgcn_s_waitcnt(kWaitLoads);  // no copy to LDS outlives the workgroup
+
+  Place wp = p, xp = p;  // of the weights two halves on, of x one half on
+  const uint8_t* row = row_of(wp);
+  Unit<FMT> w0, w1;
+  // (in the loop's order: the waits in it count what was issued since)
+  w0.load(row, wp.hf, wu, units);
+  __builtin_amdgcn_sched_barrier(0);
+  x_rows(xp);
+  x_load(xp.hf);
+  if (advance(wp)) row = row_of(wp);
+  __builtin_amdgcn_sched_barrier(0);
+  w1.load(row, wp.hf, wu, units);
+  __builtin_amdgcn_sched_barrier(0);
+  bool done = false;
+  // One half.  `w` is emptied into LDS and loaded anew, two halves on, in
+  // place: copying one register set to another would wait for its loads.
+  auto half = [&](Unit<FMT>& w) {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (4 * i < p.count - p.c0) xw[64 * i + lane] = xr[i];
+    const Operand o = to_operand(w, p.hf, units, stage);
+    u32x4 xa[4];
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(xw) + 256 * r + 8 * (q & 1);
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const u32x2 l0 = *reinterpret_cast<const u32x2*>(from + 16 * ((4 * u + (q >> 1)) ^ r));
+      const u32x2 l1 = *reinterpret_cast<const u32x2*>(from + 16 * ((4 * u + 2 + (q >> 1)) ^ r));
+      xa[u] = u32x4{l0.x, l0.y, l1.x, l1.y};
+    }
+    if (advance(xp)) x_rows(xp);
+    x_load(xp.hf);
+    if (advance(wp)) row = row_of(wp);
+    w.load(row, wp.hf, wu, units);
+    __builtin_amdgcn_sched_barrier(0);  // the loads are under way before the multiply
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const u32x4 op[1] = {xa[u]};
+      const float4_t xs = unit_sum<FMT, F16, 1>(op);
+      mul_unit<FMT, F16, 1>(o, u, op, xs, acc);
+    }
+    p.hf += kSplit;
+    if (p.hf >= halves) {
+      p.hf = part;
+      if (!done) done = !next_pairs();
+    }
+  };
+  // Always both: with a way out between them every wait for w0 would also
+  // have to hold where w1 has not been loaded after it.  A half past the last
+  // tile multiplies what is there and is not used.
+  do {
+    half(w0);
+    half(w1);
+  } while (!done);
 }
 
 // -------------------------------------------------------------------- down
@@ -657,8 +714,8 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
   slices = slices < max_slices ? slices : max_slices;
   slices = slices < halves ? slices : halves;
   const int row0 = blockIdx.x * 16, tasks = active * slices;
-  auto row = [&](int task) {
-    return a.down + (static_cast<int64_t>(table.expert[task / slices]) * a.hidden + row0 + wrow) * a.down_row_bytes;
+  auto row = [&](int slot) {
+    return a.down + (static_cast<int64_t>(__builtin_amdgcn_readfirstlane(table.expert[slot])) * a.hidden + row0 + wrow) * a.down_row_bytes;
   };
   // h of an expert's pairs is stored as operands: per unit of 32 columns the hi
   // parts, then the lo parts, each per lane quarter 16 bytes of every pair.
@@ -679,51 +736,83 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
       to[u][1] = *reinterpret_cast<const u32x4*>(h + (2 * at + 1) * hstep);
     }
   };
-  int task = wave;
-  Unit<FMT> s;
-  u32x4 ha[4][2];
-  const uint8_t* w = nullptr;
-  if (task < tasks) {
-    w = row(task);
-    s.load(w, task % slices, wu, units);
-    h_rows(task / slices, 0);
-    h_load(task % slices, ha);
-  }
-  for (; task < tasks; task += kDownWaves) {
-    const int slot = task / slices, slice = task - slot * slices;
-    const int first = table.off[slot], count = table.off[slot + 1] - first;
-    const int next = task + kDownWaves < tasks ? task + kDownWaves : task;
-    const uint8_t* next_w = row(next);
-    for (int c0 = 0; c0 < count; c0 += 16) {
-      float4_t acc = {0, 0, 0, 0};
-      for (int hf = slice; hf < halves; hf += slices) {
-        // the next half, of this task or the next, while this one is multiplied
-        const bool more = hf + slices < halves, again = c0 + 16 < count;
-        const int to = more ? hf + slices : again ? slice : next % slices;
-        if (!more) h_rows(again ? slot : next / slices, again ? c0 + 16 : 0);
-        u32x4 hn[4][2];
-        h_load(to, hn);
-        Unit<FMT> s2;
-        s2.load(more || again ? w : next_w, to, wu, units);
-        const Operand so = to_operand(s, hf, units, stage);
+  // A place in the sequence of halves that this wave multiplies: its tasks,
+  // each expert's pairs 16 at a time, the slice's halves.  At the end it stays
+  // at the last task (loaded, not used).
+  struct Place {
+    int task, slot, slice, first, count, c0, hf;
+  };
+  auto at_task = [&](Place& p, int task) {
+    p.task = task;
+    p.slot = task / slices;
+    p.slice = task - p.slot * slices;
+    p.first = __builtin_amdgcn_readfirstlane(table.off[p.slot]);
+    p.count = __builtin_amdgcn_readfirstlane(table.off[p.slot + 1]) - p.first;
+    p.c0 = 0;
+    p.hf = p.slice;
+  };
+  auto advance = [&](Place& p) {  // whether the task or the 16 pairs changed
+    p.hf += slices;
+    if (p.hf < halves) return false;
+    p.hf = p.slice;
+    p.c0 += 16;
+    if (p.c0 >= p.count) at_task(p, p.task + kDownWaves < tasks ? p.task + kDownWaves : p.task);
+    return true;
+  };
+  if (wave < tasks) {
+    Place p, wp, hp;  // what is multiplied now; of the weights, two halves on; of h, one half on
+    at_task(p, wave);
+    wp = hp = p;
+    const uint8_t* w = row(wp.slot);
+    Unit<FMT> w0, w1;
+    u32x4 h0[4][2], h1[4][2];
+    // (in the loop's order: the waits in it count what was issued since)
+    w0.load(w, wp.hf, wu, units);
+    __builtin_amdgcn_sched_barrier(0);
+    h_rows(hp.slot, hp.c0);
+    h_load(hp.hf, h0);
+    if (advance(wp)) w = row(wp.slot);
+    __builtin_amdgcn_sched_barrier(0);
+    w1.load(w, wp.hf, wu, units);
+    __builtin_amdgcn_sched_barrier(0);
+    float4_t acc = {0, 0, 0, 0};
+    bool done = false;
+    // one half; the weights are emptied into LDS and loaded anew in place, h
+    // changes places (a copy between register sets would wait for its loads)
+    auto half = [&](Unit<FMT>& wn, u32x4(&ha)[4][2], u32x4(&hn)[4][2]) {
+      const Operand so = to_operand(wn, p.hf, units, stage);
+      if (advance(hp)) h_rows(hp.slot, hp.c0);
+      h_load(hp.hf, hn);
+      if (advance(wp)) w = row(wp.slot);
+      wn.load(w, wp.hf, wu, units);
+      __builtin_amdgcn_sched_barrier(0);  // the loads are under way before the multiply
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const float4_t xs = unit_sum<FMT, false, 2>(ha[u]);
-          mul_unit<FMT, false, 2>(so, u, ha[u], xs, acc);
-        }
-        s = s2;
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-          ha[u][0] = hn[u][0];
-          ha[u][1] = hn[u][1];
-        }
+      for (int u = 0; u < 4; u++) {
+        const float4_t xs = unit_sum<FMT, false, 2>(ha[u]);
+        mul_unit<FMT, false, 2>(so, u, ha[u], xs, acc);
       }
+      p.hf += slices;
+      if (p.hf < halves) return;
+      if (!done) {
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (c0 + 4 * q + i < count)
-          slots[(slice * pairs + table.list[first + c0 + 4 * q + i]) * 16 + r] = acc[i];
-    }
-    w = next_w;
+        for (int i = 0; i < 4; i++)
+          if (p.c0 + 4 * q + i < p.count)
+            slots[(p.slice * pairs + table.list[p.first + p.c0 + 4 * q + i]) * 16 + r] = acc[i];
+      }
+      acc = float4_t{0, 0, 0, 0};
+      p.hf = p.slice;
+      p.c0 += 16;
+      if (p.c0 < p.count) return;
+      if (p.task + kDownWaves < tasks)
+        at_task(p, p.task + kDownWaves);
+      else
+        done = true;
+    };
+    // always both, as in k_moe_up; a half past the last task is not used
+    do {
+      half(w0, h0, h1);
+      half(w1, h1, h0);
+    } while (!done);
   }
   __syncthreads();
   for (int o = threadIdx.x; o < a.n * 16; o += kDownWaves * kWave) {
