@@ -49,12 +49,14 @@ constexpr int kDownWaves = 16;  // waves that share the experts of one tile
 constexpr uint32_t kLo4 = 0x0F0F0F0Fu;
 
 // The routing of one piece, in LDS or in the workspace: experts with at least
-// one pair are slots 0 .. active-1; slot s owns list[off[s] .. off[s+1]).
+// one pair are slots 0 .. active-1; slot s owns places off[s] .. off[s+1] - 1
+// of the lists of pairs (token * top_k + choice) and of their tokens.
 struct Table {
   int active;
   int expert[kMoeMaxExperts];
   int off[kMoeMaxExperts + 1];
-  int list[kMoeMaxPairs];
+  uint16_t pair[kMoeMaxPairs];
+  uint16_t token[kMoeMaxPairs];
 };
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __builtin_expf(-g)) * u; }
@@ -350,7 +352,7 @@ __device__ void route_tokens(const MoeArgs& a, int token, int* ids, bool write) 
 
 // The table of up to 64 pairs, by one wave: the pairs of the first expert that
 // is left, found by comparing with it, until none is.
-__device__ void few_pairs_table(const int* ids, int pairs, Table& t) {
+__device__ void few_pairs_table(const int* ids, int pairs, int top_k, Table& t) {
   const int lane = threadIdx.x & 63;
   const int id = lane < pairs ? ids[lane] : -1;
   uint64_t left = __builtin_amdgcn_ballot_w64(id >= 0);
@@ -362,7 +364,11 @@ __device__ void few_pairs_table(const int* ids, int pairs, Table& t) {
       t.expert[slot] = e;
       t.off[slot] = off;
     }
-    if (id == e) t.list[off + __popcll(same & ((uint64_t(1) << lane) - 1))] = lane;
+    if (id == e) {
+      const int at = off + __popcll(same & ((uint64_t(1) << lane) - 1));
+      t.pair[at] = static_cast<uint16_t>(lane);
+      t.token[at] = static_cast<uint16_t>(lane / top_k);
+    }
     off += __popcll(same);
     slot++;
     left &= ~same;
@@ -383,7 +389,7 @@ struct TableScratch {
   uint16_t count[kMoeMaxPairs / 64][kMoeMaxExperts];
 };
 
-__device__ void build_table(int pairs, int experts, Table& t, TableScratch& z) {
+__device__ void build_table(int pairs, int experts, int top_k, Table& t, TableScratch& z) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, blocks = (pairs + 63) / 64;
   constexpr int kRounds = (kMoeMaxPairs / 64 + kUpWaves - 1) / kUpWaves;
   for (int i = threadIdx.x; i < blocks * kMoeMaxExperts; i += blockDim.x) (&z.count[0][0])[i] = 0;
@@ -444,7 +450,9 @@ __device__ void build_table(int pairs, int experts, Table& t, TableScratch& z) {
   for (int k = 0; k < kRounds; k++)
     if (id[k] >= 0) {
       const int b = wave + k * kUpWaves;
-      t.list[z.base[id[k]] + z.count[b][id[k]] + rank[k]] = 64 * b + lane;
+      const int at = z.base[id[k]] + z.count[b][id[k]] + rank[k], p = 64 * b + lane;
+      t.pair[at] = static_cast<uint16_t>(p);
+      t.token[at] = static_cast<uint16_t>(p / top_k);
     }
   __syncthreads();
 }
@@ -495,10 +503,10 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   }
   __syncthreads();
   if (pairs <= 64) {
-    if (wave == 0) few_pairs_table(ids, pairs, table);
+    if (wave == 0) few_pairs_table(ids, pairs, a.top_k, table);
     __syncthreads();
   } else {
-    build_table(pairs, a.experts, table, scratch);
+    build_table(pairs, a.experts, a.top_k, table, scratch);
   }
   if (blockIdx.x == 0) {
     Table* t = static_cast<Table*>(a.table);
@@ -506,13 +514,15 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
       if (s < table.active) t->expert[s] = table.expert[s];
       t->off[s] = table.off[s];
     }
-    for (int p = threadIdx.x; p < table.off[table.active]; p += blockDim.x) t->list[p] = table.list[p];
+    for (int p = threadIdx.x; p < table.off[table.active]; p += blockDim.x) t->pair[p] = table.pair[p];
     if (threadIdx.x == 0) t->active = table.active;
   }
 
   const int tiles = a.inter / 16, units = a.hidden / 32, halves = (units + 3) / 4;
-  const int64_t tasks = static_cast<int64_t>(table.active) * tiles;
+  // tiles of all experts in a row; at most 2^31 (512 experts, 2^26 rows)
+  const uint32_t tasks = static_cast<uint32_t>(table.active) * static_cast<uint32_t>(tiles);
   if (blockIdx.x >= tasks) return;
+  const int slot_step = gridDim.x / tiles, tile_step = gridDim.x % tiles;
   const int side = wave / kSplit, part = wave % kSplit;  // gate or up; share of the columns
   const bool busy = part < halves;
   u32x4* const xw = lds.tiles.x[wave];
@@ -523,35 +533,48 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   // workgroup's tiles, each expert's pairs 16 at a time, halves part, part +
   // kSplit, ...  At the end it stays at the last tile (loaded, not used).
   struct Place {
-    int64_t task;
-    int slot, first, count, c0, hf;
+    uint32_t task;
+    int slot, tile, first, count, c0, hf;
   };
-  auto at_task = [&](Place& p, int64_t task) {
-    p.task = task;
-    p.slot = __builtin_amdgcn_readfirstlane(static_cast<int>(task / tiles));
+  auto pairs_of = [&](Place& p) {
     p.first = __builtin_amdgcn_readfirstlane(table.off[p.slot]);
     p.count = __builtin_amdgcn_readfirstlane(table.off[p.slot + 1]) - p.first;
     p.c0 = 0;
+  };
+  auto next_task = [&](Place& p) {  // false at the last
+    p.c0 = 0;
+    if (p.task + gridDim.x >= tasks) return false;
+    p.task += gridDim.x;
+    p.slot += slot_step;
+    p.tile += tile_step;
+    if (p.tile >= tiles) {
+      p.tile -= tiles;
+      p.slot++;
+    }
+    pairs_of(p);
+    return true;
   };
   auto advance = [&](Place& p) {  // whether the tile or the 16 pairs changed
     p.hf += kSplit;
     if (p.hf < halves) return false;
     p.hf = part;
     p.c0 += 16;
-    if (p.c0 >= p.count) at_task(p, p.task + gridDim.x < tasks ? p.task + gridDim.x : p.task);
+    if (p.c0 >= p.count) next_task(p);
     return true;
   };
   auto row_of = [&](const Place& p) {
-    const int tile = static_cast<int>(p.task - static_cast<int64_t>(p.slot) * tiles);
     const int64_t e = __builtin_amdgcn_readfirstlane(table.expert[p.slot]);
-    return a.gate_up + (e * 2 * a.inter + static_cast<int64_t>(side) * a.inter + 16 * tile + wrow) * a.up_row_bytes;
+    return a.gate_up + (e * 2 * a.inter + static_cast<int64_t>(side) * a.inter + 16 * p.tile + wrow) * a.up_row_bytes;
   };
 
   // x by halves (128 columns), whole rows at a time: 16 lanes load 256 bytes of
   // a token's row, four rows an instruction and only as many as the expert
   // has; through LDS they become operands.  (Loaded as operands from memory,
   // 16 rows lie 2 * hidden bytes apart and every load asks for 16 lines.)
-  int xtok[4];
+  // Row i of the four: token row 4i + q, its 16-byte chunk r ^ row going to LDS
+  // chunk r: 16 rows of one chunk column then lie in 16 different columns of
+  // banks.
+  const uint8_t* xp4[4];
   int xrows = 0;
   u32x4 xr[4];
   auto x_rows = [&](const Place& p) {  // its 16 pairs; past the last one that again
@@ -559,19 +582,21 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int at = 4 * i + q < xrows ? 4 * i + q : xrows - 1;
-      xtok[i] = table.list[p.first + p.c0 + at] / a.top_k;
+      xp4[i] = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(table.token[p.first + p.c0 + at]) * (a.hidden * 2ll) +
+               16 * (r ^ (4 * i + q));
     }
   };
   auto x_load = [&](int hf) {
-    // 16-byte chunk r ^ row of the row, to LDS chunk r: 16 rows of one chunk
-    // column then lie in 16 different columns of banks.  Past the row's end
-    // (only Q4_0) the last chunk again: those weights scale by zero.
 #pragma unroll
     for (int i = 0; i < 4; i++)
       if (4 * i < xrows) {
-        int at = 16 * hf + (r ^ (4 * i + q));
-        at = at < 4 * units ? at : 4 * units - 1;
-        xr[i] = *(reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(xtok[i]) * (a.hidden * 2ll)) + at);
+        int at = 256 * hf;
+        if constexpr (FMT == QBLK_Q4_0) {
+          // past the row's end the last chunk again: those weights scale by zero
+          const int chunk = 16 * hf + (r ^ (4 * i + q));
+          if (chunk >= 4 * units) at = 64 * units - 16 - 16 * (r ^ (4 * i + q));
+        }
+        xr[i] = *reinterpret_cast<const u32x4*>(xp4[i] + at);
       }
   };
 
@@ -592,7 +617,7 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
         const float h = silu_mul(gs, us);
         const uint16_t hi = f32_to_bf16_bits(h);
         const float rest = h - bf16_bits_to_f32(hi);
-        const int tile = static_cast<int>(p.task - static_cast<int64_t>(p.slot) * tiles);
+        const int tile = p.tile;
         // operand order, see h_rows in k_moe_down: unit tile/2 of this expert's pairs
         uint16_t* out = static_cast<uint16_t*>(a.h) + static_cast<int64_t>(p.first) * a.inter * 2 +
                         (static_cast<int64_t>((tile & ~1) * 4 + (rr >> 2)) * p.count + p.c0 + tok) * 8 + 4 * (tile & 1) + (rr & 3);
@@ -604,19 +629,18 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   };
 
   Place p;  // what is multiplied now
-  at_task(p, blockIdx.x);
+  p.task = blockIdx.x;
+  p.slot = blockIdx.x / tiles;
+  p.tile = blockIdx.x % tiles;
   p.hf = part;
+  pairs_of(p);
   float4_t acc = {0, 0, 0, 0};
   // after the last half of 16 pairs: their sums; false after the last tile
   auto next_pairs = [&]() {
     finish(p, acc);
     acc = float4_t{0, 0, 0, 0};
-    const int64_t done = p.task;
     p.c0 += 16;
-    if (p.c0 < p.count) return true;
-    if (done + gridDim.x >= tasks) return false;
-    at_task(p, done + gridDim.x);
-    return true;
+    return p.c0 < p.count || next_task(p);
   };
   if (!busy) {
     while (next_pairs()) {
@@ -701,7 +725,7 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
       table.expert[i < most ? i : 0] = t->expert[i < most ? i : 0];
       table.off[i] = t->off[i];
     }
-    for (int i = threadIdx.x; i < pairs; i += kDownWaves * kWave) table.list[i] = t->list[i];
+    for (int i = threadIdx.x; i < pairs; i += kDownWaves * kWave) table.pair[i] = t->pair[i];
     __syncthreads();
   }
   const int active = table.active;
@@ -721,19 +745,20 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
   // parts, then the lo parts, each per lane quarter 16 bytes of every pair.
   // Lanes past the last pair repeat it: not used.
   const uint8_t* h = nullptr;
-  int64_t hstep = 0;
+  int64_t hstep = 0;  // between the parts of a unit
   auto h_rows = [&](int slot, int c0) {
     const int first = table.off[slot], count = table.off[slot + 1] - first;
     h = static_cast<const uint8_t*>(a.h) + static_cast<int64_t>(first) * a.inter * 4 +
         (static_cast<int64_t>(q) * count + (c0 + r < count ? c0 + r : count - 1)) * 16;
-    hstep = static_cast<int64_t>(count) * 64;
+    hstep = count * 64;
   };
   auto h_load = [&](int hf, u32x4(&to)[4][2]) {
 #pragma unroll
     for (int u = 0; u < 4; u++) {
-      const int at = 4 * hf + u < units ? 4 * hf + u : units - 1;
-      to[u][0] = *reinterpret_cast<const u32x4*>(h + 2 * at * hstep);
-      to[u][1] = *reinterpret_cast<const u32x4*>(h + (2 * at + 1) * hstep);
+      const int at = FMT != QBLK_Q4_0 || 4 * hf + u < units ? 4 * hf + u : units - 1;
+      const uint8_t* p = h + 2 * at * hstep;
+      to[u][0] = *reinterpret_cast<const u32x4*>(p);
+      to[u][1] = *reinterpret_cast<const u32x4*>(p + hstep);
     }
   };
   // A place in the sequence of halves that this wave multiplies: its tasks,
@@ -797,7 +822,7 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
 #pragma unroll
         for (int i = 0; i < 4; i++)
           if (p.c0 + 4 * q + i < p.count)
-            slots[(p.slice * pairs + table.list[p.first + p.c0 + 4 * q + i]) * 16 + r] = acc[i];
+            slots[(p.slice * pairs + table.pair[p.first + p.c0 + 4 * q + i]) * 16 + r] = acc[i];
       }
       acc = float4_t{0, 0, 0, 0};
       p.hf = p.slice;
