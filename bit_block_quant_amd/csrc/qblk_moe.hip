@@ -108,16 +108,22 @@ __device__ __forceinline__ u32x4 codes8_op(uint32_t t) {
 template <int FMT>
 struct Unit;
 
+__device__ __forceinline__ void pin1(uint32_t& v) { asm volatile("" : "+v"(v)); }
+
 // 16 bytes at a 2-byte aligned address, put in order only when they are used
 // (load16_a2 in two steps: the first does not wait for its loads)
 struct Raw16 {
   u32x4_a4 v;
   uint32_t tail, shift;
   __device__ __forceinline__ void load(const uint8_t* p) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    v = *reinterpret_cast<const u32x4_a4*>(a & ~uintptr_t(3));
+    // (the pointer is moved, not masked: a masked one makes flat loads, which
+    // count as LDS accesses too and return in no order to wait by)
+    shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);  // 0 or 2
+    v = *reinterpret_cast<const u32x4_a4*>(p - shift);
     tail = *reinterpret_cast<const uint16_t*>(p + 14);
-    shift = static_cast<uint32_t>(a & 3u);  // 0 or 2
+  }
+  __device__ __forceinline__ void pin() {
+    asm volatile("" : "+v"(v), "+v"(tail), "+v"(shift));
   }
   __device__ __forceinline__ u32x4 get() const {
     return u32x4{__builtin_amdgcn_alignbyte(v.y, v.x, shift), __builtin_amdgcn_alignbyte(v.z, v.y, shift),
@@ -137,6 +143,11 @@ struct Unit<QBLK_SB4> {
     s = load_u16(p);
     c = p[2 + j];
   }
+  __device__ __forceinline__ void pin() {
+    raw.pin();
+    pin1(s);
+    pin1(c);
+  }
   __device__ __forceinline__ u32x4 codes() const { return raw.get(); }
   __device__ __forceinline__ float scale(int, int, int) const {
     return f16_bits_to_f32(s) * static_cast<float>(static_cast<int8_t>(c));
@@ -148,21 +159,25 @@ template <>
 struct Unit<QBLK_SB4_AFFINE> {
   static constexpr bool affine = true;
   u32x4_a4 raw;
-  uint32_t s, c, o;
+  uint32_t h;
+  __device__ __forceinline__ void pin() { asm volatile("" : "+v"(raw), "+v"(h)); }
   __device__ __forceinline__ u32x4 codes() const { return raw; }
+  template <int I>
+  __device__ __forceinline__ uint32_t head() const {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(h), I * 0x55, 0xF, 0xF, true));
+  }
   __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int) {
     const uint8_t* p = row + static_cast<int64_t>(hf >> 1) * 148;  // a multiple of 4: codes are dword aligned
     const int j = 4 * (hf & 1) + u;
     raw = *reinterpret_cast<const u32x4_a4*>(p + 20 + 16 * j);
-    s = *reinterpret_cast<const uint32_t*>(p);
-    c = p[4 + j];
-    o = p[12 + j];
+    // dword 0 (both super-scales), the half's four sub-scales and its four offsets, one to a lane
+    h = reinterpret_cast<const uint32_t*>(p)[u == 0 ? 0 : u == 1 ? 1 + (hf & 1) : 3 + (hf & 1)];
   }
-  __device__ __forceinline__ float scale(int, int, int) const {
-    return f16_bits_to_f32(s & 0xffffu) * static_cast<float>(static_cast<int8_t>(c));
+  __device__ __forceinline__ float scale(int, int u, int) const {
+    return f16_bits_to_f32(head<0>() & 0xffffu) * static_cast<float>(static_cast<int8_t>(head<1>() >> (8 * u)));
   }
-  __device__ __forceinline__ float offset(int, int) const {
-    return f16_bits_to_f32(s >> 16) * static_cast<float>(static_cast<int8_t>(o));
+  __device__ __forceinline__ float offset(int, int u) const {
+    return f16_bits_to_f32(head<0>() >> 16) * static_cast<float>(static_cast<int8_t>(head<2>() >> (8 * u)));
   }
 };
 
@@ -171,6 +186,7 @@ struct Unit<QBLK_Q4_K> {
   static constexpr bool affine = true;
   u32x4 raw;
   uint32_t h;
+  __device__ __forceinline__ void pin() { asm volatile("" : "+v"(raw), "+v"(h)); }
   __device__ __forceinline__ u32x4 codes() const { return raw; }
   __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int) {
     const u32x4* p = reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(hf >> 1) * 144);  // 16-byte aligned
@@ -194,6 +210,10 @@ struct Unit<QBLK_Q4_0> {
   static constexpr bool affine = false;
   Raw16 raw;
   uint32_t d;
+  __device__ __forceinline__ void pin() {
+    raw.pin();
+    pin1(d);
+  }
   __device__ __forceinline__ u32x4 codes() const { return raw.get(); }
   __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int units) {
     const int at = 4 * hf + u;
@@ -219,7 +239,10 @@ struct Operand {
   float4_t s, o;
 };
 template <int FMT>
-__device__ __forceinline__ Operand to_operand(const Unit<FMT>& w, int hf, int units, Stage& st) {
+__device__ __forceinline__ Operand to_operand(Unit<FMT>& w, int hf, int units, Stage& st) {
+  // What was loaded is looked at from here on: without this the compiler
+  // decodes it where it was loaded, a loop turn earlier, and waits there.
+  w.pin();
   const int lane = threadIdx.x & 63, row = lane >> 2, u = lane & 3, r = lane & 15, q = lane >> 4;
   st.codes[4 * row + (u ^ ((row >> 2) & 3))] = w.codes();
   st.scale[lane] = w.scale(hf, u, units);
