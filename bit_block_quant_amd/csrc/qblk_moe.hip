@@ -493,7 +493,7 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   // two workgroups to a CU: at most 80 KB each
   __shared__ Table table;
   struct Tiles {
-    float4_t red[kUpWaves][64];
+    float4_t red[2][kUpWaves][64];
     u32x4 x[kUpWaves][256];
     Stage stage[kUpWaves];
   };
@@ -550,7 +550,6 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   const bool busy = part < halves;
   u32x4* const xw = lds.tiles.x[wave];
   Stage& stage = lds.tiles.stage[wave];
-  auto& red = lds.tiles.red;
 
   // A place in the sequence of halves that this wave multiplies: for its
   // workgroup's tiles, each expert's pairs 16 at a time, halves part, part +
@@ -623,13 +622,19 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
       }
   };
 
-  // The tiles' sums, put together by all waves: lane (row r, quarter q) of
-  // them holds tokens 4q .. 4q+3.
+  // The tile's sums, put together by four of the waves, another four (and in
+  // them another first one: few tokens keep only it busy) each time.  One
+  // barrier: the other buffer is read by nobody any more once it is passed.
+  int turn = 0;
   auto finish = [&](const Place& p, const float4_t& acc) {
+    auto& red = lds.tiles.red[turn & 1];
     red[wave][lane] = acc;
     __syncthreads();
-    if (threadIdx.x < 256) {
-      const int tok = threadIdx.x >> 4, rr = threadIdx.x & 15;
+    const int duty = (wave + 3 * turn) & (kUpWaves - 1);
+    turn++;
+    if (duty < 4) {
+      // lane (row r, quarter q) of the sums holds tokens 4q .. 4q+3
+      const int tok = 4 * duty + (lane >> 4), rr = lane & 15;
       if (p.c0 + tok < p.count) {
         float gs = 0.0f, us = 0.0f;
 #pragma unroll
@@ -648,7 +653,6 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
         out[static_cast<int64_t>(p.count) * 32] = __builtin_isfinite(rest) ? f32_to_bf16_bits(rest) : 0;
       }
     }
-    __syncthreads();
   };
 
   Place p;  // what is multiplied now
