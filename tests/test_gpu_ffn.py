@@ -333,7 +333,8 @@ MOE = [("sb4", 5, 512, 256, 1, 2), ("sb4", 8, 256, 768, 4, 3), ("sb4_affine", 5,
        ("q4_k", 6, 256, 512, 7, 4), ("q4_0", 5, 512, 256, 2, 2), ("q4_0", 4, 96, 160, 5, 2),
        ("q4_0", 3, 32, 32, 1, 1), ("q4_0", 7, 288, 416, 19, 3), ("sb4", 2, 256, 256, 40, 2),
        ("sb4_affine", 70, 256, 256, 9, 8), ("q4_k", 1, 256, 256, 17, 1), ("q4_0", 130, 64, 64, 16, 6),
-       ("q4_k", 3, 2304, 256, 6, 2), ("sb4", 3, 256, 2560, 6, 2)]
+       ("q4_k", 3, 2304, 256, 6, 2), ("sb4", 3, 256, 2560, 6, 2), ("sb4", 3, 4096, 256, 20, 2),
+       ("q4_0", 9, 4128, 96, 33, 3)]
 
 
 @pytest.mark.parametrize("fmt,experts,hidden,inter,n,top_k", MOE)
