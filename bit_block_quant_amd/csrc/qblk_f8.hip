@@ -394,14 +394,21 @@ struct Stage {
   uint8_t a[kTileRows * kGroup];
   uint8_t b[64 * NT * kGroup];
 };
-// sx * sw of 4 groups, for the two row halves and every token
+// The scales of 4 groups: every token's, and (in the first 8) the two row
+// halves'; as the copies to LDS leave them, 64 consecutive floats each.
 template <int NT>
 struct Scales {
-  float s[2][4][64 * NT];
+  float x[64 * NT][4];
+  float w[64];
 };
+// Stages in LDS: what a copy has to reach memory and come back is a stage's
+// work with two of them.  The smaller tiles work that much shorter on one, and
+// have room for three.
+template <int NT>
+constexpr int kStages = NT == 4 ? 2 : 3;
 template <int NT>
 struct TileLds {
-  Stage<NT> st[2];
+  Stage<NT> st[kStages<NT>];
   Scales<NT> sc[2];
 };
 
@@ -508,36 +515,26 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
   };
 
   const int wm = wave & 1, wn = wave >> 1;
-  // Scales, 4 groups at a time: a thread takes the tokens and groups
-  // threadIdx.x + 512 u of [token][4], loads early in one run of 4 stages and
-  // leaves the products with both row halves' scales in LDS for the next.
-  constexpr int kPer = (NT + 1) / 2;
-  const float* swp[2];
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
+  // Scales, 4 groups at a time (the 16 bytes of a token that lie together),
+  // copied to LDS like the codes: read from memory a group at a time they were
+  // as many accesses as the codes.
+  const float* swp;
+  {
+    const int h = (lane >> 2) & 1;
     int64_t row = GATE ? row0 + static_cast<int64_t>(h) * p.up : row0 + 128 * h;
     if (row > p.m - 1) row = p.m - 1;
-    swp[h] = p.ws + row / kGroup * G;
+    swp = p.ws + row / kGroup * G;
   }
-  float xv[kPer], wv[2];
-  auto scales_load = [&](int g) {
-    const int gg = g + (threadIdx.x & 3) < g1 ? g + (threadIdx.x & 3) : g1 - 1;
+  auto copy_scales = [&](Scales<NT>& s, int g) {
+    const int gg = g + (lane & 3) < g1 ? g + (lane & 3) : g1 - 1;
 #pragma unroll
-    for (int u = 0; u < kPer; u++) {
-      int tok = t0 + (((threadIdx.x + 512 * u) >> 2) & (64 * NT - 1));
+    for (int u = 0; u < (NT + 1) / 2; u++) {
+      const int first = ((wave + 8 * u) & (4 * NT - 1)) * 16;
+      int tok = t0 + first + (lane >> 2);
       if (tok > p.n - 1) tok = p.n - 1;
-      xv[u] = p.xs[static_cast<int64_t>(tok) * G + gg];
+      __builtin_amdgcn_global_load_lds((glob_void*)(p.xs + static_cast<int64_t>(tok) * G + gg), (lds_void*)(s.x[first]), 4, 0, 0);
     }
-    wv[0] = swp[0][gg];
-    wv[1] = swp[1][gg];
-  };
-  auto scales_store = [&](Scales<NT>& s) {
-#pragma unroll
-    for (int u = 0; u < kPer; u++) {
-      const int tok = ((threadIdx.x + 512 * u) >> 2) & (64 * NT - 1);  // 64 tokens: both halves of the threads write the same
-      s.s[0][threadIdx.x & 3][tok] = xv[u] * wv[0];
-      s.s[1][threadIdx.x & 3][tok] = xv[u] * wv[1];
-    }
+    if (wave == 0) __builtin_amdgcn_global_load_lds((glob_void*)(swp + gg), (lds_void*)(s.w), 4, 0, 0);
   };
 
   float4_t acc[8][NT];
@@ -560,35 +557,55 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
 #pragma unroll
     for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(c[i & 1][j][e], sc[i >> 2][j], acc[i][j][e]);
   };
-  scales_load(g0);
+  copy_scales(scl[0], g0);
 #pragma unroll
   for (int i = 0; i < 4 + NT; i++) copy(st[0], g0, i);
-  scales_store(scl[0]);
+  if constexpr (kStages<NT> == 3) {
+#pragma unroll
+    for (int i = 0; i < 4 + NT; i++) copy(st[1], g0 + 1 < g1 ? g0 + 1 : g0, i);
+  }
   __syncthreads();
-  copy(st[1], g0 + 1 < g1 ? g0 + 1 : g0, 0);
-  copy(st[1], g0 + 1 < g1 ? g0 + 1 : g0, 1);
+  constexpr int kAhead = kStages<NT> - 1;  // stages whose copies are on their way
+  auto group_at = [&](int step) { return g0 + step < g1 ? g0 + step : g1 - 1; };
+  copy(st[kAhead], group_at(kAhead), 0);
+  copy(st[kAhead], group_at(kAhead), 1);
   af[0].load(st[0].a, arow(0), q);
 #pragma unroll
   for (int j = 0; j < NT; j++) bf[j].load(st[0].b, (wn * NT + j) * 16 + r, q);
+  int now = 0;
   for (int g = g0; g < g1; g++) {
     const int step = g - g0;
-    Stage<NT>& cur = st[step & 1];
-    Stage<NT>& nxt = st[(step + 1) & 1];
-    const int gn = g + 1 < g1 ? g + 1 : g1 - 1, gc = g + 2 < g1 ? g + 2 : g1 - 1;
+    Stage<NT>& cur = st[now];
+    Stage<NT>& nxt = st[now + 1 < kStages<NT> ? now + 1 : 0];
+    Stage<NT>& far = st[now > 0 ? now - 1 : kStages<NT> - 1];  // the one before, filled kAhead stages on
+    const int gf = group_at(step + kAhead), gc = group_at(step + kAhead + 1);
+    now = now + 1 < kStages<NT> ? now + 1 : 0;
+    {
+      const Scales<NT>& l = scl[(step >> 2) & 1];
+      const float w0 = l.w[step & 3], w1 = l.w[4 + (step & 3)];
 #pragma unroll
-    for (int j = 0; j < NT; j++) {
-      sc[0][j] = scl[(step >> 2) & 1].s[0][step & 3][(wn * NT + j) * 16 + r];
-      sc[1][j] = scl[(step >> 2) & 1].s[1][step & 3][(wn * NT + j) * 16 + r];
+      for (int j = 0; j < NT; j++) {
+        const float x = l.x[(wn * NT + j) * 16 + r][step & 3];
+        sc[0][j] = x * w0;
+        sc[1][j] = x * w1;
+      }
     }
-    if ((step & 3) == 0) scales_load(g + 4 < g1 ? g + 4 : g1 - 1);
-    if ((step & 3) == 2) scales_store(scl[((step >> 2) + 1) & 1]);
+    if ((step & 3) == 0) copy_scales(scl[((step >> 2) + 1) & 1], g + 4 < g1 ? g + 4 : g1 - 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       if (i + 1 < 8) {
         af[(i + 1) & 1].load(cur.a, arow(i + 1), q);
-      } else {
+      } else if constexpr (kStages<NT> == 2) {
         __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
+        // as __syncthreads, but leaving the newest 4 + NT loads under way: the
+        // copies of the stage after next (all older ones are the next stage's)
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_s_waitcnt(0x0070 | (4 + NT));  // vmcnt(4 + NT) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -603,8 +620,8 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
       // over four row tiles: issued at once they hold up the waves' issue.
       if (i + 1 < 8) {
         if (i < 3) {
-          copy(nxt, gn, 2 * i + 2);
-          copy(nxt, gn, 2 * i + 3);
+          copy(far, gf, 2 * i + 2);
+          copy(far, gf, 2 * i + 3);
         }
 #pragma unroll
         for (int j = 0; j < NT && !EXACT; j++) {
