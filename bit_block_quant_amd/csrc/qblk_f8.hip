@@ -24,21 +24,6 @@ constexpr int kGroup = 128;
 constexpr float kF8Max = 448.0f;
 
 // -------------------------------------------------------------- inputs
-template <int XT>
-struct Src;  // element type of x as stored
-template <>
-struct Src<QBLK_F32> {
-  typedef float type;
-};
-template <>
-struct Src<QBLK_F16> {
-  typedef uint16_t type;
-};
-template <>
-struct Src<QBLK_BF16> {
-  typedef uint16_t type;
-};
-
 // 8 consecutive elements (16-byte aligned for the 16-bit types, 32 for fp32's two halves)
 template <int XT>
 __device__ __forceinline__ void load8(const void* x, int64_t at, float v[8]) {
@@ -124,9 +109,12 @@ __device__ __forceinline__ float quant_group(const float v[8], uint32_t code[2])
 // ------------------------------------------------------ activation codes
 // HBM bound: 2 or 4 bytes read and 1 + 1/32 written per value; 16 lanes to a
 // group, so a wave reads 1 KB (16-bit input) of consecutive values at once.
+// The scales go out token by token, or (per > 0, the groups of a token) group
+// by group, as k_f8_few reads them with neighbouring lanes.
 template <int XT>
 __global__ __launch_bounds__(256) void k_quant_act_f8(const void* __restrict__ x, int64_t group0, int64_t groups,
-                                                      uint8_t* __restrict__ xq, float* __restrict__ scale) {
+                                                      uint8_t* __restrict__ xq, float* __restrict__ scale, int per,
+                                                      int tokens) {
   int64_t g = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
   const bool on = g < groups;
   g = group0 + (on ? g : groups - 1);  // whole waves take part in the row reductions
@@ -137,7 +125,14 @@ __global__ __launch_bounds__(256) void k_quant_act_f8(const void* __restrict__ x
   const float s = quant_group(v, code);
   if (on) {
     *reinterpret_cast<u32x2*>(xq + g * kGroup + 8 * l) = u32x2{code[0], code[1]};
-    if (l == 0) scale[g] = s;
+    if (l == 0) {
+      int64_t at = g;
+      if (per > 0) {  // few tokens: g fits 32 bits
+        const uint32_t t = static_cast<uint32_t>(g) / static_cast<uint32_t>(per);
+        at = static_cast<int64_t>(static_cast<uint32_t>(g) - t * per) * tokens + t;
+      }
+      scale[at] = s;
+    }
   }
 }
 
@@ -209,78 +204,161 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int yt) {
 // sum|qw qx|); with so few tokens the widening and the matrix work hide
 // behind the weight stream.
 //
-// A lane's 16-byte loads are 16 consecutive codes of one row (weights: row
-// l & 15; tokens: token l & 15; quarter l >> 4 of a 64-code run), and the two
-// operands meet in the same order, so no lane exchange is needed.
+// A load takes 8 rows of a group's 128 codes, 8 neighbouring lanes a row: the
+// vector cache counts an access per 64 bytes of neighbouring lanes, 16 for
+// these against 64 where every lane reads its own row, which held 32 tokens to
+// half the memory's rate.  The rows change lanes through 2 KB of LDS of the
+// wave's own (its LDS operations stay in order, so the next tile may follow at
+// once); both operands are read in the same order.  A wave has the operands of
+// its next two groups in flight, in registers: each set is loaded again where
+// it has just been used.
 //
 // GATE: the tiles are 16 gate rows and the 16 up rows i further on; the
 // result is h = silu(gate) * up in fp32 (n x i).
-// XSRC: kCodes = x given as codes and scales; else the element type of x,
-// which the workgroup quantizes into LDS itself (one launch less; every
-// workgroup repeats it, so only for few values, see launch_linear_f8).
+// XSRC: kCodes = x given as codes and scales (token t's of group g at
+// t * xs_tok + g * xs_group); else the element type of x, which the workgroup
+// quantizes into LDS itself (one launch less; every workgroup repeats it, so
+// only for few values, see launch_linear_f8).
 constexpr int kCodes = 3;
-constexpr int kDepth = 4;  // groups of a wave whose loads are in flight together
+
+// What a wave keeps in LDS: an operand's tile while it changes lanes, then its
+// partial sums.
+constexpr int few_region(int T, int NR) { return T * NR < 2 ? 2048 : T * NR * 1024; }
+
+template <int T, int NR, int XT>  // XT = T where x comes as codes, else 1 (unused)
+struct FewSet {
+  u32x4 w[NR][2], x[XT][2];
+  float sw[NR], sx[XT];
+};
 
 template <int T, int NR, int WAVES, bool GATE, int XSRC>
 __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restrict__ w, const float* __restrict__ ws,
                                                          int m, int k, const void* __restrict__ xv,
-                                                         const float* __restrict__ xs, int n, void* __restrict__ y,
-                                                         int yt, int64_t up_row) {
+                                                         const float* __restrict__ xs, int xs_tok, int xs_group,
+                                                         int n, void* __restrict__ y, int yt, int64_t up_row) {
   extern __shared__ __align__(16) uint8_t lds[];
+  constexpr bool CODES = XSRC == kCodes;
+  constexpr int kRegion = few_region(T, NR);
+  using Set = FewSet<T, NR, CODES ? T : 1>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = k / kGroup;
   const int t0 = blockIdx.y * 16 * T;
   const int row0 = blockIdx.x * (GATE ? 16 : 16 * NR);
   const int r = lane & 15, q = lane >> 4;
   n -= t0;
+  uint8_t* const region = lds + wave * kRegion;
 
-  const uint8_t* wp[NR];
+  // Rows and tokens past the last repeat it; their results are not stored.
+  int zero;  // in a vector register, so that the scales come with the codes and in their order
+  asm("v_mov_b32 %0, 0" : "=v"(zero));
+  const uint8_t* wb[NR];
   const float* sp[NR];
+  uint32_t wo[NR][2], xo[CODES ? T : 1][2], xso[CODES ? T : 1];
 #pragma unroll
   for (int a = 0; a < NR; a++) {
     const int64_t base = GATE ? row0 + a * up_row : row0 + 16 * a;
-    const int64_t last = GATE ? base + 15 : m - 1;
-    const int64_t row = base + r < last ? base + r : last;
-    wp[a] = w + row * k + 16 * q;
-    sp[a] = ws + (base < last ? base : last) / kGroup * G;
+    const int64_t first = GATE || base < m ? base : m - 1;
+    const int last = GATE || m - first > 15 ? 15 : static_cast<int>(m - 1 - first);
+    wb[a] = w + first * k;
+    sp[a] = ws + first / kGroup * G;
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      const int row = 8 * u + (lane >> 3) < last ? 8 * u + (lane >> 3) : last;
+      wo[a][u] = static_cast<uint32_t>(row) * static_cast<uint32_t>(k) + 16 * (lane & 7);
+    }
   }
+  const uint8_t* xb = static_cast<const uint8_t*>(xv);
+  if constexpr (CODES) {
+    xb += static_cast<int64_t>(t0) * k;
+    xs += static_cast<int64_t>(t0) * xs_tok;
+#pragma unroll
+    for (int t = 0; t < T; t++) {
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        const int tok = 16 * t + 8 * u + (lane >> 3);
+        xo[t][u] = static_cast<uint32_t>(tok < n ? tok : n - 1) * static_cast<uint32_t>(k) + 16 * (lane & 7);
+      }
+      xso[t] = static_cast<uint32_t>(16 * t + r < n ? 16 * t + r : n - 1) * static_cast<uint32_t>(xs_tok);
+    }
+  }
+  auto load = [&](Set& s, int step) {
+    int g = wave + step * WAVES;
+    if (g > G - 1) g = G - 1;
+    const int64_t at = static_cast<int64_t>(g) * kGroup;
+#pragma unroll
+    for (int a = 0; a < NR; a++) {
+#pragma unroll
+      for (int u = 0; u < 2; u++) s.w[a][u] = *reinterpret_cast<const u32x4*>(wb[a] + at + wo[a][u]);
+      s.sw[a] = sp[a][g + zero];
+    }
+    if constexpr (CODES) {
+#pragma unroll
+      for (int t = 0; t < T; t++) {
+#pragma unroll
+        for (int u = 0; u < 2; u++) s.x[t][u] = *reinterpret_cast<const u32x4*>(xb + at + xo[t][u]);
+        s.sx[t] = xs[static_cast<int64_t>(g) * xs_group + xso[t]];
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // row l >> 3 (and 8 further), chunk l & 7 -> row r, chunks q and q + 4
+  auto turn = [&](const u32x4 v[2], u32x4 out[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      const int row = 8 * u + (lane >> 3);
+      *reinterpret_cast<u32x4*>(region + row * kGroup + (((lane & 7) ^ ((row >> 1) & 7)) << 4)) = v[u];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const int key = (r >> 1) & 7;
+    out[0] = *reinterpret_cast<const u32x4*>(region + r * kGroup + ((q ^ key) << 4));
+    out[1] = *reinterpret_cast<const u32x4*>(region + r * kGroup + (((q + 4) ^ key) << 4));
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
 
+  Set A, B;
   const uint8_t* xq = nullptr;
-  int xstride = 0;
-  if constexpr (XSRC != kCodes) {
-    xstride = k + 16;
-    float* sl = reinterpret_cast<float*>(lds);
-    uint8_t* ql = lds + ((n < 16 * T ? n : 16 * T) * G * 4 + 15) / 16 * 16;
+  const float* sl = nullptr;
+  const int xstride = k + 16;
+  if constexpr (!CODES) {
     const int nt = n < 16 * T ? n : 16 * T;
-    for (int u = threadIdx.x >> 4; u < (nt * G + 3) / 4 * 4; u += WAVES * 4) {
-      const bool on = u < nt * G;
-      const int uu = on ? u : nt * G - 1;
-      const int t = uu / G, g = uu - t * G;
-      float v[8];
-      load8<XSRC>(xv, static_cast<int64_t>(t0 + t) * k + g * kGroup + 8 * r, v);
-      uint32_t c[2];
-      const float s = quant_group(v, c);
-      if (on) {
-        *reinterpret_cast<u32x2*>(ql + t * xstride + g * kGroup + 8 * r) = u32x2{c[0], c[1]};
-        if (r == 0) sl[uu] = s;
+    float* const scales = reinterpret_cast<float*>(lds + WAVES * kRegion);
+    uint8_t* const codes = lds + WAVES * kRegion + (nt * G * 4 + 15) / 16 * 16;
+    xq = codes;
+    sl = scales;
+    const int units = nt * G;
+    for (int u0 = 0; u0 < units; u0 += WAVES * 8) {  // two groups a row of 16 lanes
+      float v[2][8];
+      int unit[2];
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        unit[i] = u0 + i * WAVES * 4 + (threadIdx.x >> 4);
+        const int uu = unit[i] < units ? unit[i] : units - 1;
+        load8<XSRC>(xv, (static_cast<int64_t>(t0) * G + uu) * kGroup + 8 * r, v[i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (u0 == 0) {
+        load(A, 0);
+        load(B, 1);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        uint32_t c[2];
+        const float s = quant_group(v[i], c);
+        if (unit[i] < units) {
+          const int t = unit[i] / G, g = unit[i] - t * G;
+          *reinterpret_cast<u32x2*>(codes + t * xstride + g * kGroup + 8 * r) = u32x2{c[0], c[1]};
+          if (r == 0) scales[unit[i]] = s;
+        }
       }
     }
     __syncthreads();
-    xq = ql;
-  }
-
-  const uint8_t* xp[T];
-  const float* xsp[T];
-#pragma unroll
-  for (int t = 0; t < T; t++) {
-    const int tok = 16 * t + r < n ? 16 * t + r : n - 1;
-    if constexpr (XSRC == kCodes) {
-      xp[t] = static_cast<const uint8_t*>(xv) + static_cast<int64_t>(t0 + tok) * k + 16 * q;
-      xsp[t] = xs + static_cast<int64_t>(t0 + tok) * G;
-    } else {
-      xp[t] = xq + tok * xstride + 16 * q;
-      xsp[t] = reinterpret_cast<const float*>(lds) + tok * G;
-    }
+  } else {
+    load(A, 0);
+    load(B, 1);
   }
 
   float4_t acc[NR][T];
@@ -289,53 +367,67 @@ __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restri
 #pragma unroll
     for (int t = 0; t < T; t++) acc[a][t] = float4_t{0, 0, 0, 0};
 
-  for (int g0 = wave; g0 < G; g0 += WAVES * kDepth) {
-    u32x4 wr[kDepth][NR][2];
-    float sw[kDepth][NR];
+  auto use = [&](const Set& s, int step) {
+    const bool on = wave + step * WAVES < G;
+    const int g = on ? wave + step * WAVES : G - 1;
+    bf16x8_n wv[NR][4];
 #pragma unroll
-    for (int d = 0; d < kDepth; d++) {
-      const int g = g0 + d * WAVES < G ? g0 + d * WAVES : G - 1;
+    for (int a = 0; a < NR; a++) {
+      u32x4 c[2];
+      turn(s.w[a], c);
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        wv[a][2 * j] = widen8(c[j].x, c[j].y);
+        wv[a][2 * j + 1] = widen8(c[j].z, c[j].w);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < T; t++) {
+      u32x4 c[2];
+      float sx;
+      if constexpr (CODES) {
+        turn(s.x[t], c);
+        sx = s.sx[t];
+      } else {
+        const int tok = 16 * t + r < n ? 16 * t + r : n - 1;
+        const uint8_t* at = xq + tok * xstride + g * kGroup + 16 * q;
+        c[0] = *reinterpret_cast<const u32x4*>(at);
+        c[1] = *reinterpret_cast<const u32x4*>(at + 64);
+        sx = sl[tok * G + g];
+      }
+      bf16x8_n xw[4];
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        xw[2 * j] = widen8(c[j].x, c[j].y);
+        xw[2 * j + 1] = widen8(c[j].z, c[j].w);
+      }
 #pragma unroll
       for (int a = 0; a < NR; a++) {
-        wr[d][a][0] = *reinterpret_cast<const u32x4*>(wp[a] + g * kGroup);
-        wr[d][a][1] = *reinterpret_cast<const u32x4*>(wp[a] + g * kGroup + 64);
-        sw[d][a] = sp[a][g];
+        float4_t p = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; j++) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[a][j], xw[j], p, 0, 0, 0);
+        const float sc = on ? sx * s.sw[a] : 0.0f;  // a group past the last repeats that one
+#pragma unroll
+        for (int i = 0; i < 4; i++) acc[a][t][i] = __builtin_fmaf(p[i], sc, acc[a][t][i]);
       }
     }
-#pragma unroll
-    for (int d = 0; d < kDepth; d++) {
-      const bool on = g0 + d * WAVES < G;
-      const int g = on ? g0 + d * WAVES : G - 1;
-#pragma unroll
-      for (int t = 0; t < T; t++) {
-        const u32x4 x0 = *reinterpret_cast<const u32x4*>(xp[t] + g * kGroup);
-        const u32x4 x1 = *reinterpret_cast<const u32x4*>(xp[t] + g * kGroup + 64);
-        const float sx = on ? xsp[t][g] : 0.0f;
-        const bf16x8_n b0 = widen8(x0.x, x0.y), b1 = widen8(x0.z, x0.w);
-        const bf16x8_n b2 = widen8(x1.x, x1.y), b3 = widen8(x1.z, x1.w);
-#pragma unroll
-        for (int a = 0; a < NR; a++) {
-          const u32x4 w0 = wr[d][a][0], w1 = wr[d][a][1];
-          float4_t p = {0, 0, 0, 0};
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w0.x, w0.y), b0, p, 0, 0, 0);
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w0.z, w0.w), b1, p, 0, 0, 0);
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w1.x, w1.y), b2, p, 0, 0, 0);
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w1.z, w1.w), b3, p, 0, 0, 0);
-          const float s = sx * sw[d][a];
-#pragma unroll
-          for (int i = 0; i < 4; i++) acc[a][t][i] = __builtin_fmaf(p[i], s, acc[a][t][i]);
-        }
-      }
-    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  const int steps = (G + WAVES - 1) / WAVES;
+  for (int step = 0; step < steps; step += 2) {
+    use(A, step);
+    load(A, step + 2);
+    use(B, step + 1);
+    load(B, step + 3);
   }
 
   // lane (r, q) holds rows 4q..4q+3 of each tile for token r of each 16
-  if constexpr (XSRC != kCodes) __syncthreads();  // the codes in LDS are read
-  float4_t* red = reinterpret_cast<float4_t*>(lds);
+  float4_t* red = reinterpret_cast<float4_t*>(region);
 #pragma unroll
   for (int a = 0; a < NR; a++)
 #pragma unroll
-    for (int t = 0; t < T; t++) red[((wave * NR + a) * T + t) * 64 + lane] = acc[a][t];
+    for (int t = 0; t < T; t++) red[(a * T + t) * 64 + lane] = acc[a][t];
   __syncthreads();
   const float* rf = reinterpret_cast<const float*>(lds);
   const int tiles = GATE ? 1 : NR;
@@ -345,8 +437,8 @@ __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restri
     float sum = 0.0f, up = 0.0f;
 #pragma unroll
     for (int v = 0; v < WAVES; v++) {
-      sum += rf[v * NR * T * 256 + at];
-      if constexpr (GATE) up += rf[(v * NR + 1) * T * 256 + at];
+      sum += rf[v * (kRegion / 4) + at];
+      if constexpr (GATE) up += rf[v * (kRegion / 4) + T * 256 + at];
     }
     if (tok >= n) continue;
     const int row = row0 + 16 * a + rr;
@@ -739,72 +831,127 @@ __global__ __launch_bounds__(256) void k_f8_join(const float* __restrict__ part,
   store_y(y, i, v, yt);
 }
 
-// LDS of k_f8_few: the waves' partial sums, or the quantized x before them
-constexpr int kFewWaves = 8;
-size_t few_lds(int T, int NR, bool codes, int n, int k) {
-  const size_t red = static_cast<size_t>(kFewWaves) * NR * T * 1024;
-  const int nt = n < 16 * T ? n : 16 * T;
-  const size_t xq = codes ? 0 : (static_cast<size_t>(nt) * (k / kGroup) * 4 + 15) / 16 * 16 + static_cast<size_t>(nt) * (k + 16);
-  return red > xq ? red : xq;
+// The codes and scales of H = silu(gate) * up from the splits' partial products
+// of the rows [gate; up]: 16 lanes to a group of 128, like k_quant_act_f8.
+// Group g's scale of token t goes to t * s_tok + g * s_group.
+__global__ __launch_bounds__(256) void k_f8_join_gate(const float* __restrict__ part, int64_t stride, int splits,
+                                                      int inter, int64_t groups, uint8_t* __restrict__ hq,
+                                                      float* __restrict__ hs, int64_t s_tok, int64_t s_group) {
+  const int64_t all = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const bool on = all < groups;
+  const int64_t u = on ? all : groups - 1;  // whole waves take part in the row reductions
+  const int per = inter / kGroup, l = threadIdx.x & 15;
+  const int64_t t = u / per;
+  const int g = static_cast<int>(u - t * per);
+  const float* p = part + t * 2 * inter + g * kGroup + 8 * l;
+  float gate[8], up[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) gate[i] = up[i] = 0.0f;
+  for (int s = 0; s < splits; s++, p += stride) {
+    float a[8], b[8];
+    load8<QBLK_F32>(p, 0, a);
+    load8<QBLK_F32>(p, inter, b);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      gate[i] += a[i];
+      up[i] += b[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) gate[i] = silu_mul(gate[i], up[i]);
+  uint32_t code[2];
+  const float s = quant_group(gate, code);
+  if (on) {
+    *reinterpret_cast<u32x2*>(hq + u * kGroup + 8 * l) = u32x2{code[0], code[1]};
+    if (l == 0) hs[t * s_tok + g * s_group] = s;
+  }
 }
 
-template <int T, int NR, bool GATE, int XSRC>
-hipError_t few(const uint8_t* w, const float* ws, int64_t m, int64_t k, const void* x, const float* xs, int64_t n,
-               void* y, int yt, int64_t up_row, hipStream_t s) {
+// What a few-tokens product takes besides its matrix: x as values, or as codes
+// with scales at the given strides.
+struct FewX {
+  const void* x;
+  int xt;
+  const float* xs;
+  int64_t xs_tok, xs_group;
+};
+
+template <int T, int NR, int WAVES, bool GATE, int XSRC>
+hipError_t few(const uint8_t* w, const float* ws, int64_t m, int64_t k, const FewX& x, int64_t n, void* y, int yt,
+               int64_t up_row, hipStream_t s) {
   const int per = GATE ? 16 : 16 * NR;
   const int64_t rows = GATE ? up_row : m;
   const dim3 grid(static_cast<unsigned>((rows + per - 1) / per), static_cast<unsigned>((n + 16 * T - 1) / (16 * T)));
-  const size_t lds = few_lds(T, NR, XSRC == kCodes, static_cast<int>(n), static_cast<int>(k));
-  log_launch("f8 few%s rows=%lld k=%lld n=%lld T=%d NR=%d x=%d lds=%zu", GATE ? " gate" : "", (long long)m,
-             (long long)k, (long long)n, T, NR, XSRC, lds);
-  k_f8_few<T, NR, kFewWaves, GATE, XSRC><<<grid, kFewWaves * kWave, lds, s>>>(
-      w, ws, static_cast<int>(m), static_cast<int>(k), x, xs, static_cast<int>(n), y, yt, up_row);
+  const size_t nt = static_cast<size_t>(n < 16 * T ? n : 16 * T), G = static_cast<size_t>(k / kGroup);
+  const size_t lds = static_cast<size_t>(WAVES) * few_region(T, NR) +
+                     (XSRC == kCodes ? 0 : (nt * G * 4 + 15) / 16 * 16 + nt * (static_cast<size_t>(k) + 16));
+  static const hipError_t allowed =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(k_f8_few<T, NR, WAVES, GATE, XSRC>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+  if (allowed != hipSuccess) return allowed;
+  log_launch("f8 few%s rows=%lld k=%lld n=%lld T=%d NR=%d waves=%d x=%d lds=%zu", GATE ? " gate" : "", (long long)m,
+             (long long)k, (long long)n, T, NR, WAVES, XSRC, lds);
+  k_f8_few<T, NR, WAVES, GATE, XSRC><<<grid, WAVES * kWave, lds, s>>>(
+      w, ws, static_cast<int>(m), static_cast<int>(k), x.x, x.xs, static_cast<int>(x.xs_tok),
+      static_cast<int>(x.xs_group), static_cast<int>(n), y, yt, up_row);
   return hipGetLastError();
 }
 
-template <bool GATE>
-hipError_t few_codes(const uint8_t* w, const float* ws, int64_t m, int64_t k, const uint8_t* xq, const float* xs,
-                     int64_t n, void* y, int yt, int64_t up_row, hipStream_t s) {
-  constexpr int NR = GATE ? 2 : 1;
-  if (n <= 16) return few<1, NR, GATE, kCodes>(w, ws, m, k, xq, xs, n, y, yt, up_row, s);
-  if (n <= 32) return few<2, NR, GATE, kCodes>(w, ws, m, k, xq, xs, n, y, yt, up_row, s);
-  return few<4, NR, GATE, kCodes>(w, ws, m, k, xq, xs, n, y, yt, up_row, s);
+template <int NR, int WAVES, bool GATE>
+hipError_t few_src(const uint8_t* w, const float* ws, int64_t m, int64_t k, const FewX& x, int64_t n, void* y, int yt,
+                   int64_t up_row, hipStream_t s) {
+  switch (x.xt) {
+    case QBLK_F32: return few<1, NR, WAVES, GATE, QBLK_F32>(w, ws, m, k, x, n, y, yt, up_row, s);
+    case QBLK_F16: return few<1, NR, WAVES, GATE, QBLK_F16>(w, ws, m, k, x, n, y, yt, up_row, s);
+    case QBLK_BF16: return few<1, NR, WAVES, GATE, QBLK_BF16>(w, ws, m, k, x, n, y, yt, up_row, s);
+  }
+  if (n <= 16) return few<1, NR, WAVES, GATE, kCodes>(w, ws, m, k, x, n, y, yt, up_row, s);
+  if (n <= 32) return few<2, NR, WAVES, GATE, kCodes>(w, ws, m, k, x, n, y, yt, up_row, s);
+  // (16 waves have 128 registers each, too few for these tokens' sets)
+  return few<4, NR, 8, GATE, kCodes>(w, ws, m, k, x, n, y, yt, up_row, s);
 }
 
-template <bool GATE>
-hipError_t few_values(const uint8_t* w, const float* ws, int64_t m, int64_t k, const void* x, int xt, int64_t n,
-                      void* y, int yt, int64_t up_row, hipStream_t s) {
-  constexpr int NR = GATE ? 2 : 1;
-  switch (xt) {
-    case QBLK_F32: return few<1, NR, GATE, QBLK_F32>(w, ws, m, k, x, nullptr, n, y, yt, up_row, s);
-    case QBLK_F16: return few<1, NR, GATE, QBLK_F16>(w, ws, m, k, x, nullptr, n, y, yt, up_row, s);
-    default: return few<1, NR, GATE, QBLK_BF16>(w, ws, m, k, x, nullptr, n, y, yt, up_row, s);
-  }
+// Y = W X^T (or, for up_row > 0, H) by k_f8_few.  With no more row tiles than
+// compute units one workgroup is all that a unit gets: 16 waves then, so that
+// it has as much in flight as two of 8.
+hipError_t few_product(const uint8_t* w, const float* ws, int64_t m, int64_t k, const FewX& x, int64_t n, void* y,
+                       int yt, int64_t up_row, hipStream_t s) {
+  if (up_row > 0) return few_src<2, 8, true>(w, ws, m, k, x, n, y, yt, up_row, s);
+  if ((m + 15) / 16 <= cu_count()) return few_src<1, 16, false>(w, ws, m, k, x, n, y, yt, 0, s);
+  return few_src<1, 8, false>(w, ws, m, k, x, n, y, yt, 0, s);
 }
 
 // The tile kernel's shape for a product: tokens per tile and splits of K.
 struct Plan {
   int nt, splits, per;  // 64 nt tokens; groups per split
+  double us;            // the estimate by which it was taken
 };
 
-Plan tile_plan(int64_t m, int64_t k, int64_t n, bool gate, bool exact) {
+//
+// The time of each is estimated from what was measured for the kernel's
+// variants (us: a stage of a tile, then the rest of a tile's time, for 64, 128
+// and 256 tokens; a stage is bound by the matrix cores only in the widest) and
+// the least taken.  (A gated product's split tiles leave gate and up apart in the
+// partial sums, and the join forms h.)  A split is worth its join where tiles leave compute units
+// without work: m = k = 4096, n = 128: 64-token tiles unsplit 24.0 us, split by
+// 4 16.5; n = 1024: 29.5 against 65.  Wide tiles pay with many tokens: m = 14336,
+// k = 4096, n = 4096: 64 tokens 400 us, 128 293, 256 270; n = 512: 58, 41, 69.
+// Over 26 shapes (65 to 4096 tokens, both kinds of sums) the choice was never
+// more than 11% behind the best of all, and 0.5% on average.
+Plan tile_plan(int64_t m, int64_t k, int64_t n, bool exact) {
   const int64_t rt = (m + kTileRows - 1) / kTileRows, G = k / kGroup;
   const int cus = cu_count();
-  Plan best{1, 1, static_cast<int>(G)};
-  double cost = 1e30;
+  constexpr double stage[2][3] = {{0.68, 0.9, 1.65}, {1.15, 1.55, 0}}, ends[2][3] = {{5, 8, 11}, {5, 7, 0}};
+  Plan best{1, 1, static_cast<int>(G), 1e30};
   for (int nt = 1; nt <= (exact ? 2 : 4); nt *= 2) {
     const int64_t tiles = rt * ((n + 64 * nt - 1) / (64 * nt));
     for (int sp = 1; sp <= 8; sp *= 2) {
-      if (sp > 1 && (gate || G / sp < 4)) break;
+      if (sp > 1 && G / sp < 4) break;
       const int64_t per = (G + sp - 1) / sp;
       const int64_t rounds = (tiles * sp + cus - 1) / cus;
-      // us: a stage of a tile (matrix cores, or the copies where nt is small), a tile's start and end, the partial sums
-      const double stage = nt == 4 ? 1.9 : nt == 2 ? (exact ? 1.6 : 1.1) : 0.8;
-      const double c = rounds * (per * stage + 4.0) + (sp > 1 ? 3.0 + 2.0 * sp * n * m * 4 / 4.0e6 : 0.0);
-      if (c < cost) {
-        cost = c;
-        best = Plan{nt, sp, static_cast<int>(per)};
-      }
+      const double c = rounds * (per * stage[exact][nt >> 1] + ends[exact][nt >> 1]) +
+                       (sp > 1 ? 2.5 + 0.4e-6 * sp * n * m * 4 : 0.0);
+      if (c < best.us) best = Plan{nt, sp, static_cast<int>(per), c};
     }
   }
   best.splits = static_cast<int>((G + best.per - 1) / best.per);
@@ -832,27 +979,51 @@ hipError_t tile_nt(int nt, bool exact, const TileArgs& a, int splits, hipStream_
   }
 }
 
+// Where the scales of codes go or are: token t's of group g at t * tok + g * group.
+struct ScaleAt {
+  int64_t tok, group;
+};
+
 // Y (or, for `up` > 0, the codes and scales of H) by the tile kernel
 hipError_t tile_product(const uint8_t* w, const float* ws, int64_t m, int64_t k, const uint8_t* xq, const float* xs,
-                        int64_t n, void* y, int yt, int64_t up, float* hs, bool exact, void* work, hipStream_t s) {
-  const Plan plan = tile_plan(m, k, n, up > 0, exact);
+                        int64_t n, void* y, int yt, int64_t up, float* hs, ScaleAt at, bool exact, void* work,
+                        hipStream_t s) {
+  const Plan plan = tile_plan(m, k, n, exact);
+  const bool split = plan.splits > 1;
   TileArgs a{w, ws, xq, xs, y, hs, static_cast<float*>(work), static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt,
-             static_cast<int>(up), static_cast<int>((m + kTileRows - 1) / kTileRows),
+             static_cast<int>(split ? 0 : up), static_cast<int>((m + kTileRows - 1) / kTileRows),
              static_cast<int>((n + 64 * plan.nt - 1) / (64 * plan.nt)), plan.per};
   log_launch("f8 tile%s%s m=%lld k=%lld n=%lld tokens=%d splits=%d", up > 0 ? " gate" : "", exact ? " exact" : "",
              (long long)m, (long long)k, (long long)n, 64 * plan.nt, plan.splits);
-  if (up > 0) return tile_nt<true, false>(plan.nt, exact, a, 1, s);
-  if (plan.splits == 1) return tile_nt<false, false>(plan.nt, exact, a, 1, s);
+  if (!split) return up > 0 ? tile_nt<true, false>(plan.nt, exact, a, 1, s) : tile_nt<false, false>(plan.nt, exact, a, 1, s);
   const hipError_t e = tile_nt<false, true>(plan.nt, exact, a, plan.splits, s);
   if (e != hipSuccess) return e;
+  if (up > 0) {  // (one launch: only a product of few tiles is split)
+    const int64_t groups = n * (up / kGroup);
+    k_f8_join_gate<<<dim3(static_cast<unsigned>((groups + 15) / 16)), 256, 0, s>>>(
+        a.part, m * n, plan.splits, static_cast<int>(up), groups, static_cast<uint8_t*>(y), hs, at.tok, at.group);
+    return hipGetLastError();
+  }
   return in_pieces(m * n, 256, 256, [&](int64_t first, int64_t c) {
     k_f8_join<<<dim3(static_cast<unsigned>((c + 255) / 256)), 256, 0, s>>>(a.part, first, c, m * n, plan.splits, y, yt);
     return hipGetLastError();
   });
 }
 
-// Products up to this many tokens run k_f8_few.
-constexpr int64_t kFewTokens = 64;
+// Products of up to this many tokens are exact to fp32 rounding.
+constexpr int64_t kExactTokens = 64;
+
+// Whether a product runs k_f8_few: up to 16 tokens always (one operand of x per
+// 16 rows); up to 64 where its estimate is below the tile kernel's.  It keeps all
+// compute units busy with few rows, but reads x again for every 16 of them
+// (us, few and tiles: 32 tokens, m = k = 4096: 9.8, 14.6; m = 8192, k = 8192:
+// 24.8, 22.5; m = 22016, k = 4096: 37.8, 29.5; 64 tokens: 11.9, 17.4; 42.8, 26.0;
+// 72.0, 32.9).
+bool use_few(int64_t m, int64_t k, int64_t n) {
+  if (n <= 16 || n > kExactTokens) return n <= 16;
+  const double us = n <= 32 ? 3.5 + 0.36e-6 * m * k : 1.0 + 0.68e-6 * m * k;
+  return us <= tile_plan(m, k, n, true).us;
+}
 
 // Whether a product quantizes its x inside every workgroup.
 bool fused_quant(int64_t n, int64_t k) { return n <= 4 && n * k <= 32768; }
@@ -866,21 +1037,34 @@ __global__ __launch_bounds__(256) void k_zero(uint8_t* __restrict__ y, int64_t b
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 int64_t code_bytes(int64_t n, int64_t k) { return align256(n * k) + align256(n * (k / kGroup) * 4); }
 
-}  // namespace
-
-hipError_t launch_quantize_act_f8(const void* x, int xt, int64_t n, int64_t k, uint8_t* xq, float* scale,
-                                  hipStream_t s) {
+hipError_t quantize_act(const void* x, int xt, int64_t n, int64_t k, uint8_t* xq, float* scale,
+                        bool by_group, hipStream_t s) {
   const int64_t groups = n * (k / kGroup);
+  const int per = by_group ? static_cast<int>(k / kGroup) : 0;
   log_launch("quantize_act_f8 n=%lld k=%lld", (long long)n, (long long)k);
   return in_pieces(groups, 16, 256, [&](int64_t g0, int64_t c) {
     const dim3 grid(static_cast<unsigned>((c + 15) / 16));
     switch (xt) {
-      case QBLK_F32: k_quant_act_f8<QBLK_F32><<<grid, 256, 0, s>>>(x, g0, c, xq, scale); break;
-      case QBLK_F16: k_quant_act_f8<QBLK_F16><<<grid, 256, 0, s>>>(x, g0, c, xq, scale); break;
-      default: k_quant_act_f8<QBLK_BF16><<<grid, 256, 0, s>>>(x, g0, c, xq, scale); break;
+      case QBLK_F32: k_quant_act_f8<QBLK_F32><<<grid, 256, 0, s>>>(x, g0, c, xq, scale, per, static_cast<int>(n)); break;
+      case QBLK_F16: k_quant_act_f8<QBLK_F16><<<grid, 256, 0, s>>>(x, g0, c, xq, scale, per, static_cast<int>(n)); break;
+      default: k_quant_act_f8<QBLK_BF16><<<grid, 256, 0, s>>>(x, g0, c, xq, scale, per, static_cast<int>(n)); break;
     }
     return hipGetLastError();
   });
+}
+
+// Y = W X^T from codes, by one kernel or the other
+hipError_t code_product(const uint8_t* w, const float* ws, int64_t m, int64_t k, const uint8_t* xq, const float* xs,
+                        ScaleAt at, int64_t n, void* y, int yt, void* work, hipStream_t s) {
+  if (use_few(m, k, n)) return few_product(w, ws, m, k, FewX{xq, kCodes, xs, at.tok, at.group}, n, y, yt, 0, s);
+  return tile_product(w, ws, m, k, xq, xs, n, y, yt, 0, nullptr, at, yt == QBLK_F32 || n <= kExactTokens, work, s);
+}
+
+}  // namespace
+
+hipError_t launch_quantize_act_f8(const void* x, int xt, int64_t n, int64_t k, uint8_t* xq, float* scale,
+                                  hipStream_t s) {
+  return quantize_act(x, xt, n, k, xq, scale, false, s);
 }
 
 hipError_t launch_quantize_f8(const void* w, int wt, int64_t rows, int64_t k, uint8_t* codes, float* scale,
@@ -907,16 +1091,15 @@ hipError_t launch_zero_bytes(void* y, int64_t bytes, hipStream_t s) {
 
 // (for either kind of result: the one that splits more decides)
 int64_t gemm_f8_workspace(int64_t m, int64_t k, int64_t n) {
-  if (n <= kFewTokens) return 0;
-  const int a = tile_plan(m, k, n, false, false).splits, b = tile_plan(m, k, n, false, true).splits;
+  if (use_few(m, k, n)) return 0;
+  const int a = tile_plan(m, k, n, false).splits, b = tile_plan(m, k, n, true).splits;
   const int most = a > b ? a : b;
   return most > 1 ? align256(most * n * m * 4) : 0;
 }
 
 hipError_t launch_gemm_f8(const uint8_t* w, const float* ws, int64_t m, int64_t k, const uint8_t* xq,
                           const float* xs, int64_t n, void* y, int yt, void* work, hipStream_t s) {
-  if (n <= kFewTokens) return few_codes<false>(w, ws, m, k, xq, xs, n, y, yt, 0, s);
-  return tile_product(w, ws, m, k, xq, xs, n, y, yt, 0, nullptr, yt == QBLK_F32, work, s);
+  return code_product(w, ws, m, k, xq, xs, ScaleAt{k / kGroup, 1}, n, y, yt, work, s);
 }
 
 int64_t linear_f8_workspace(int64_t m, int64_t k, int64_t n) {
@@ -926,46 +1109,55 @@ int64_t linear_f8_workspace(int64_t m, int64_t k, int64_t n) {
 
 hipError_t launch_linear_f8(const uint8_t* w, const float* ws, int64_t m, int64_t k, const void* x, int xt,
                             int64_t n, void* y, int yt, void* work, hipStream_t s) {
-  if (fused_quant(n, k)) return few_values<false>(w, ws, m, k, x, xt, n, y, yt, 0, s);
+  if (fused_quant(n, k)) return few_product(w, ws, m, k, FewX{x, xt, nullptr, 0, 0}, n, y, yt, 0, s);
   uint8_t* xq = static_cast<uint8_t*>(work);
   float* xs = reinterpret_cast<float*>(xq + align256(n * k));
-  const hipError_t e = launch_quantize_act_f8(x, xt, n, k, xq, xs, s);
+  const bool few = use_few(m, k, n);
+  const hipError_t e = quantize_act(x, xt, n, k, xq, xs, few, s);
   if (e != hipSuccess) return e;
-  return launch_gemm_f8(w, ws, m, k, xq, xs, n, y, yt, xq + code_bytes(n, k), s);
+  return code_product(w, ws, m, k, xq, xs, few ? ScaleAt{1, n} : ScaleAt{k / kGroup, 1}, n, y, yt,
+                      xq + code_bytes(n, k), s);
 }
 
-// ffn workspace: few tokens: h in fp32, then what its two products need, one
-// after the other; else the codes of x, those of h, and the second product's
+// ffn workspace.  First product by k_f8_few: h in fp32, then what the two
+// products need, one after the other.  Else the codes of x, those of h, and the
+// partial sums of one product or the other.
 int64_t ffn_f8_workspace(int64_t h, int64_t i, int64_t n) {
-  if (n > kFewTokens) return code_bytes(n, h) + code_bytes(n, i) + gemm_f8_workspace(h, i, n);
-  const int64_t up = fused_quant(n, h) ? 0 : code_bytes(n, h);
-  const int64_t down = linear_f8_workspace(h, i, n);
-  return align256(n * i * 4) + (up > down ? up : down);
+  const int64_t up = gemm_f8_workspace(2 * i, h, n), down = gemm_f8_workspace(h, i, n);
+  if (!use_few(2 * i, h, n)) return code_bytes(n, h) + code_bytes(n, i) + (up > down ? up : down);
+  const int64_t first = fused_quant(n, h) ? 0 : code_bytes(n, h);
+  const int64_t second = linear_f8_workspace(h, i, n);
+  return align256(n * i * 4) + (first > second ? first : second);
 }
 
 hipError_t launch_ffn_f8(const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2, int64_t h,
                          int64_t i, const void* x, int xt, int64_t n, void* y, int yt, void* work, hipStream_t s) {
   hipError_t e;
-  if (n > kFewTokens) {
+  if (!use_few(2 * i, h, n)) {
     uint8_t* xq = static_cast<uint8_t*>(work);
     float* xs = reinterpret_cast<float*>(xq + align256(n * h));
     uint8_t* hq = xq + code_bytes(n, h);
     float* hs = reinterpret_cast<float*>(hq + align256(n * i));
-    e = launch_quantize_act_f8(x, xt, n, h, xq, xs, s);
+    void* rest = hq + code_bytes(n, i);
     // (the codes of h turn on the last bits of the first product: see k_f8_tile)
-    if (e == hipSuccess) e = tile_product(w13, s13, 2 * i, h, xq, xs, n, hq, 0, i, hs, yt != QBLK_BF16, nullptr, s);
+    const bool exact = yt != QBLK_BF16 || n <= kExactTokens;
+    // only a join can write the scales group by group
+    const bool joined = tile_plan(2 * i, h, n, exact).splits > 1;
+    const ScaleAt at = joined && use_few(h, i, n) ? ScaleAt{1, n} : ScaleAt{i / kGroup, 1};
+    e = quantize_act(x, xt, n, h, xq, xs, false, s);
+    if (e == hipSuccess) e = tile_product(w13, s13, 2 * i, h, xq, xs, n, hq, 0, i, hs, at, exact, rest, s);
     if (e != hipSuccess) return e;
-    return launch_gemm_f8(w2, s2, h, i, hq, hs, n, y, yt, hq + code_bytes(n, i), s);
+    return code_product(w2, s2, h, i, hq, hs, at, n, y, yt, rest, s);
   }
   float* mid = static_cast<float*>(work);
   uint8_t* rest = static_cast<uint8_t*>(work) + align256(n * i * 4);
   if (fused_quant(n, h)) {
-    e = few_values<true>(w13, s13, 2 * i, h, x, xt, n, mid, QBLK_F32, i, s);
+    e = few_product(w13, s13, 2 * i, h, FewX{x, xt, nullptr, 0, 0}, n, mid, QBLK_F32, i, s);
   } else {
     float* xs = reinterpret_cast<float*>(rest + align256(n * h));
-    e = launch_quantize_act_f8(x, xt, n, h, rest, xs, s);
+    e = quantize_act(x, xt, n, h, rest, xs, true, s);
     if (e != hipSuccess) return e;
-    e = few_codes<true>(w13, s13, 2 * i, h, rest, xs, n, mid, QBLK_F32, i, s);
+    e = few_product(w13, s13, 2 * i, h, FewX{rest, kCodes, xs, 1, n}, n, mid, QBLK_F32, i, s);
   }
   if (e != hipSuccess) return e;
   return launch_linear_f8(w2, s2, h, i, mid, QBLK_F32, n, y, yt, rest, s);

@@ -13,6 +13,8 @@ constexpr int kF8Group = 128;
 // Rows of one 8-bit matrix: a workgroup of 512 threads takes 16 of them, and
 // a launch holds at most 2^32 - 1 threads.
 constexpr int64_t kMaxF8Rows = int64_t(1) << 26;
+// Columns of a product: a tile's 256 rows are addressed by 32-bit offsets.
+constexpr int64_t kMaxF8Cols = int64_t(1) << 24;
 
 // An 8-bit matrix of rows x k codes (k a multiple of 128).
 qblk_status_t check_f8(int64_t rows, int64_t k) {
@@ -38,7 +40,8 @@ qblk_status_t check_work(const void* work, size_t have, int64_t need) {
 int64_t bytes_of_type(int t) { return t == QBLK_F32 ? 4 : 2; }
 
 bool gemm_shape_ok(int64_t m, int64_t k, int64_t n) {
-  return check_f8(m, k) == QBLK_OK && m <= kMaxF8Rows && check_rows(n, k) == QBLK_OK && check_rows(n, m) == QBLK_OK;
+  return check_f8(m, k) == QBLK_OK && m <= kMaxF8Rows && k <= kMaxF8Cols && check_rows(n, k) == QBLK_OK &&
+         check_rows(n, m) == QBLK_OK;
 }
 
 // hidden and inter of a gated layer: each is the columns of one matrix

@@ -273,14 +273,16 @@ int qblk_deterministic(void);
  * fp32), or 128 columns of one token (xscale[t][c/128], n x k/128 fp32).
  * Rule: scale = max|v| / 448 in fp32; code = e4m3(clamp(v / scale, +-448)),
  * round to nearest even, both divisions IEEE fp32; a zero scale gives code 0.
- * k must be a multiple of 128 (QBLK_ERR_SHAPE), a matrix at most 2^26 rows.
+ * k must be a multiple of 128, a product's matrix at most 2^26 rows of at most
+ * 2^24 columns (QBLK_ERR_SHAPE).
  *
  * The products: Y[t,r] = sum_g xscale[t,g] wscale[r/128,g] *
  * (sum over the 128 columns of g of code * code), Y n x m row-major of type
  * yt in {F32, F16, BF16}, one rounding at the end.  Sums over groups are fp32
- * in a fixed order, so equal inputs give bitwise equal outputs.  Up to 64
- * tokens the sum inside a group is fp32 too.  Beyond, it is formed by the fp8
- * matrix instructions, which keep a group's sum to about 2^-17 of
+ * in a fixed order, so equal inputs give bitwise equal outputs.  The sum inside
+ * a group is exact to fp32 rounding too up to 64 tokens, and for F32 results
+ * at any number.  F16 and BF16 results of more than 64 tokens are formed by
+ * the fp8 matrix instructions, which keep a group's sum to about 2^-17 of
  * sum|code * code| (2^-13 where the codes of one group differ by many orders
  * of magnitude).
  *
@@ -321,7 +323,9 @@ qblk_status_t qblk_linear_f8(const uint8_t* w, const float* wscale, int64_t m,
 /* A gated feed-forward layer: H = silu(Wg X) * (Wu X) in fp32, Y = W2 H, with X
  * and H quantized per token and 128 columns.  w13 is (2*inter) x hidden, the
  * inter rows of Wg before those of Wu; w2 is hidden x inter; hidden and inter
- * are multiples of 128; X and Y are n x hidden.  silu(v) = v / (1 + exp(-v)). */
+ * are multiples of 128; X and Y are n x hidden.  silu(v) = v / (1 + exp(-v)).
+ * The sums of the first product use the fp8 matrix instructions for BF16
+ * results of more than 64 tokens only, because the codes of H turn on them. */
 size_t qblk_ffn_f8_workspace(int64_t hidden, int64_t inter, int64_t n);
 qblk_status_t qblk_ffn_f8(const uint8_t* w13, const float* s13,
                           const uint8_t* w2, const float* s2, int64_t hidden,

@@ -257,6 +257,40 @@ def test_ffn_f8(q, hidden, inter, n, dtype):
     assert torch.equal(y, q.ffn_f8(x, w13, s13, w2, s2))
 
 
+@pytest.mark.parametrize("hidden,inter,n", [(2048, 384, 100), (2048, 14336, 24), (2048, 14336, 64), (1152, 128, 129),
+                                            (4096, 128, 65)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_ffn_f8_long_sums(q, hidden, inter, n, dtype):
+    """Enough columns for the first product's sums to be split; same bound as above."""
+    gen = torch.Generator("cuda").manual_seed(hidden + inter + n)
+    x = torch.randn(n, hidden, device="cuda", generator=gen).to(TYPES[dtype])
+    w13, s13 = q.quantize_f8(torch.randn(2 * inter, hidden, device="cuda", generator=gen) * 0.1)
+    w2, s2 = q.quantize_f8(torch.randn(hidden, inter, device="cuda", generator=gen) * 0.1)
+    y = q.ffn_f8(x, w13, s13, w2, s2)
+    back = lambda c, s, rows: (torch.from_numpy(E4M3).cuda()[c.view(torch.uint8).long()]
+                               * s.double().repeat_interleave(rows, 0)[:c.shape[0]].repeat_interleave(128, 1))
+    xv, xsc = act_ref(x.float().cpu().numpy())
+    gu = torch.from_numpy(xv * np.repeat(xsc.astype(np.float64), 128, 1)).cuda() @ back(w13, s13, 128).T
+    hv, hs = act_ref(f64((gu[:, :inter] / (1 + torch.exp(-gu[:, :inter])) * gu[:, inter:]).float()).astype(np.float32))
+    ref = f64(torch.from_numpy(hv * np.repeat(hs.astype(np.float64), 128, 1)).cuda() @ back(w2, s2, 128).T)
+    err = np.linalg.norm(f64(y) - ref) / np.linalg.norm(ref)
+    assert err <= 4e-3 + HALF_ULP[x.dtype], err
+    assert torch.equal(y, q.ffn_f8(x, w13, s13, w2, s2))
+
+
+@pytest.mark.parametrize("m,k,n", [(9000, 8192, 17), (9000, 8192, 64), (40, 11008, 7), (5000, 11008, 333)])
+def test_gemm_f8_large(q, m, k, n):
+    """Sizes on the tile kernel's side up to 64 tokens, long sums, many splits."""
+    wq, ws, xq, xs, _ = f8_operands(q, m, k, n, 3)
+    t = torch.from_numpy(E4M3).cuda()
+    W = t[wq.view(torch.uint8).long()] * ws.double().repeat_interleave(128, 0)[:m].repeat_interleave(128, 1)
+    X = t[xq.view(torch.uint8).long()] * xs.double().repeat_interleave(128, 1)
+    ref, mag = f64(X @ W.T), f64(X.abs() @ W.abs().T)
+    for dtype in (torch.float32, torch.bfloat16):
+        got = f64(q.gemm_f8(wq, ws, xq, xs, dtype=dtype))
+        assert np.all(np.abs(got - ref) <= product_bound(n) * mag + 2 * HALF_ULP[dtype] * np.abs(ref) + 1e-38)
+
+
 def test_ffn_f8_large_gates(q):
     """Gates far beyond exp's range on both sides: silu is 0 or the gate itself, never NaN."""
     x = torch.ones(3, 128, device="cuda")
