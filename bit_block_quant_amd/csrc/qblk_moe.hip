@@ -381,7 +381,7 @@ __device__ void few_pairs_table(const int* ids, int pairs, int top_k, Table& t) 
   uint64_t left = __builtin_amdgcn_ballot_w64(id >= 0);
   int slot = 0, off = 0;
   while (left != 0) {
-    const int e = __shfl(id, __builtin_ctzll(left), kWave);
+    const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
     const uint64_t same = __builtin_amdgcn_ballot_w64(id == e);
     if (lane == 0) {
       t.expert[slot] = e;
@@ -746,6 +746,8 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
   extern __shared__ __align__(16) float slots[];  // [slice][pair][ROWS]
   __shared__ Table table;
   __shared__ Stage stages[kDownWaves];
+  __shared__ float share[kMoeMaxPairs];  // a pair's weight
+  __shared__ bool valid[kMoeMaxPairs];   // and whether it has an expert
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4, wrow = lane >> 2, wu = lane & 3;
   Stage& stage = stages[wave];
@@ -759,7 +761,13 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
       if (i < most) table.expert[i] = t->expert[i];
       table.off[i] = t->off[i];
     }
-    for (int i = threadIdx.x; i < pairs; i += kDownWaves * kWave) table.pair[i] = t->pair[i];
+    for (int i = threadIdx.x; i < pairs; i += kDownWaves * kWave) {
+      table.pair[i] = t->pair[i];
+      const int e = a.ids[i];
+      const float w = a.weights[i];
+      valid[i] = e >= 0 && e < a.experts;
+      share[i] = w;
+    }
     __syncthreads();
   }
   const int active = table.active, groups = (active + SPAN - 1) / SPAN;
@@ -895,17 +903,20 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
     } while (!done);
   }
   __syncthreads();
+  // the slices of a pair, then the pairs of a token, each in order
+  for (int o = threadIdx.x; o < pairs * ROWS; o += kDownWaves * kWave) {
+    const int p = o / ROWS;
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < slices; s++) sum += slots[s * pairs * ROWS + o];
+    slots[o] = valid[p] ? share[p] * sum : 0.0f;
+  }
+  __syncthreads();
   for (int o = threadIdx.x; o < a.n * ROWS; o += kDownWaves * kWave) {
     const int t = o / ROWS, rr = o & (ROWS - 1);
     float y = 0.0f;
-    for (int j = 0; j < a.top_k; j++) {
-      const int p = t * a.top_k + j;
-      const int e = a.ids[p];
-      if (e < 0 || e >= a.experts) continue;
-      float sum = 0.0f;
-      for (int s = 0; s < slices; s++) sum += slots[(s * pairs + p) * ROWS + rr];
-      y = __builtin_fmaf(a.weights[p], sum, y);
-    }
+#pragma unroll 4
+    for (int j = 0; j < a.top_k; j++) y += slots[(t * a.top_k + j) * ROWS + rr];
     const int64_t at = static_cast<int64_t>(t) * a.hidden + row0 + rr;
     if (a.yt == QBLK_F32)
       static_cast<float*>(a.y)[at] = y;
