@@ -56,7 +56,7 @@ qblk_status_t moe_shape(const qblk_moe_t& a) {
   if (a.fmt == QBLK_W4G128) return QBLK_ERR_UNSUPPORTED;  // its products take 8-bit activations
   if (a.n < 0 || a.n > kMaxDim || a.hidden < 0 || a.inter < 0 || a.hidden % e != 0 || a.inter % e != 0)
     return QBLK_ERR_SHAPE;
-  if (a.hidden > kMaxF8Rows || a.inter > kMaxF8Rows) return QBLK_ERR_SHAPE;
+  if (a.hidden > qblk::kMoeMaxDim || a.inter > qblk::kMoeMaxDim) return QBLK_ERR_SHAPE;
   if (a.experts < 1 || a.experts > qblk::kMoeMaxExperts || a.top_k < 1 || a.top_k > qblk::kMoeMaxTopK ||
       a.top_k > a.experts)
     return QBLK_ERR_SHAPE;

@@ -12,6 +12,9 @@ constexpr int kMoeMaxTopK = 32;
 // partial rows fit the 64 KB of LDS that k_moe_down uses.  More tokens run in
 // pieces, in stream order.
 constexpr int kMoeMaxPairs = 1024;
+// Largest hidden and inter: the intermediate of those pairs is at most 2 GB,
+// which k_moe_down addresses by 32-bit offsets.
+constexpr int64_t kMoeMaxDim = int64_t(1) << 19;
 
 struct MoeArgs {
   const void* x;

@@ -108,49 +108,29 @@ __device__ __forceinline__ u32x4 codes8_op(uint32_t t) {
 template <int FMT>
 struct Unit;
 
-__device__ __forceinline__ void pin1(uint32_t& v) { asm volatile("" : "+v"(v)); }
-
-// 16 bytes at a 2-byte aligned address, put in order only when they are used
-// (load16_a2 in two steps: the first does not wait for its loads)
-struct Raw16 {
-  u32x4_a4 v;
-  uint32_t tail, shift;
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    // (the pointer is moved, not masked: a masked one makes flat loads, which
-    // count as LDS accesses too and return in no order to wait by)
-    shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);  // 0 or 2
-    v = *reinterpret_cast<const u32x4_a4*>(p - shift);
-    tail = *reinterpret_cast<const uint16_t*>(p + 14);
-  }
-  __device__ __forceinline__ void pin() {
-    asm volatile("" : "+v"(v), "+v"(tail), "+v"(shift));
-  }
-  __device__ __forceinline__ u32x4 get() const {
-    return u32x4{__builtin_amdgcn_alignbyte(v.y, v.x, shift), __builtin_amdgcn_alignbyte(v.z, v.y, shift),
-                 __builtin_amdgcn_alignbyte(v.w, v.z, shift), __builtin_amdgcn_alignbyte(tail, v.w, shift)};
-  }
-};
+// (global loads take any address: blocks of 18 and 138 bytes start at every other byte)
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
 
 template <>
 struct Unit<QBLK_SB4> {
   static constexpr bool affine = false;
-  Raw16 raw;
-  uint32_t s, c;
+  u32x4_a2 raw;
+  uint32_t h;
+  __device__ __forceinline__ void pin() { asm volatile("" : "+v"(raw), "+v"(h)); }
+  __device__ __forceinline__ u32x4 codes() const { return raw; }
+  template <int I>
+  __device__ __forceinline__ uint32_t head() const {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(h), I * 0x55, 0xF, 0xF, true));
+  }
   __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int) {
     const uint8_t* p = row + static_cast<int64_t>(hf >> 1) * 138;
-    const int j = 4 * (hf & 1) + u;
-    raw.load(p + 10 + 16 * j);
-    s = load_u16(p);
-    c = p[2 + j];
+    raw = *reinterpret_cast<const u32x4_a2*>(p + 10 + 64 * (hf & 1) + 16 * u);
+    // the first lane the super-scale, the others the half's four sub-scales
+    h = *reinterpret_cast<const u32_a2*>(p + (u == 0 ? 0 : 2 + 4 * (hf & 1)));
   }
-  __device__ __forceinline__ void pin() {
-    raw.pin();
-    pin1(s);
-    pin1(c);
-  }
-  __device__ __forceinline__ u32x4 codes() const { return raw.get(); }
-  __device__ __forceinline__ float scale(int, int, int) const {
-    return f16_bits_to_f32(s) * static_cast<float>(static_cast<int8_t>(c));
+  __device__ __forceinline__ float scale(int, int u, int) const {
+    return f16_bits_to_f32(head<0>() & 0xffffu) * static_cast<float>(static_cast<int8_t>(head<1>() >> (8 * u)));
   }
   __device__ __forceinline__ float offset(int, int) const { return 0.0f; }
 };
@@ -208,17 +188,14 @@ struct Unit<QBLK_Q4_K> {
 template <>
 struct Unit<QBLK_Q4_0> {
   static constexpr bool affine = false;
-  Raw16 raw;
+  u32x4_a2 raw;
   uint32_t d;
-  __device__ __forceinline__ void pin() {
-    raw.pin();
-    pin1(d);
-  }
-  __device__ __forceinline__ u32x4 codes() const { return raw.get(); }
+  __device__ __forceinline__ void pin() { asm volatile("" : "+v"(raw), "+v"(d)); }
+  __device__ __forceinline__ u32x4 codes() const { return raw; }
   __device__ __forceinline__ void load(const uint8_t* row, int hf, int u, int units) {
     const int at = 4 * hf + u;
     const uint8_t* p = row + static_cast<int64_t>(at < units ? at : units - 1) * 18;
-    raw.load(p + 2);
+    raw = *reinterpret_cast<const u32x4_a2*>(p + 2);
     d = load_u16(p);
   }
   __device__ __forceinline__ float scale(int hf, int u, int units) const {
@@ -794,24 +771,33 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
   };
   // h of an expert's pairs is stored as operands: per unit of 32 columns the hi
   // parts, then the lo parts, each per lane quarter 16 bytes of every pair.
-  // Lanes past the last pair repeat it: not used.
-  const uint8_t* h = nullptr;
-  int64_t hstep = 0;  // between the parts of a unit
+  // Buffer loads: a lane past the last pair has an offset past the buffer's end,
+  // gets zeros and costs the vector cache no access (16 for a load by all lanes,
+  // 4 for up to 4 pairs), and the waits stay countable as they would not behind
+  // a branch.  h is at most 2 GB (kMoeMaxDim).
+  const auto hbuf = __builtin_amdgcn_make_buffer_rsrc(a.h, 0, static_cast<uint32_t>(pairs) * static_cast<uint32_t>(a.inter) * 4u,
+                                                      0x00027000);
+  uint32_t h = 0, hstep = 0;  // offset; between the parts of a unit
   auto h_rows = [&](int group, int c0) {
     const int slot = slot_of(group, r >> 3);
-    const int first = table.off[slot], count = table.off[slot + 1] - first;
-    const int at = c0 + (r & (ROWS - 1));
-    h = static_cast<const uint8_t*>(a.h) + static_cast<int64_t>(first) * a.inter * 4 +
-        (static_cast<int64_t>(q) * count + (at < count ? at : count - 1)) * 16;
+    uint32_t first = table.off[slot], count = table.off[slot + 1] - first;
+    if constexpr (SPAN == 1) {
+      first = __builtin_amdgcn_readfirstlane(first);
+      count = __builtin_amdgcn_readfirstlane(count);
+    }
+    const uint32_t at = c0 + (r & (ROWS - 1));
+    h = at < count ? first * static_cast<uint32_t>(a.inter) * 4u + (q * count + at) * 16u : 0x80000000u;
     hstep = count * 64;
   };
   auto h_load = [&](int hf, u32x4(&to)[4][2]) {
 #pragma unroll
     for (int u = 0; u < 4; u++) {
-      const int at = FMT != QBLK_Q4_0 || 4 * hf + u < units ? 4 * hf + u : units - 1;
-      const uint8_t* p = h + 2 * at * hstep;
-      to[u][0] = *reinterpret_cast<const u32x4*>(p);
-      to[u][1] = *reinterpret_cast<const u32x4*>(p + hstep);
+      const uint32_t at = 2 * hstep * (FMT != QBLK_Q4_0 || 4 * hf + u < units ? 4 * hf + u : units - 1);
+      const uint32_t v = SPAN == 1 ? h : h + at, s = SPAN == 1 ? at : 0;
+#pragma unroll
+      for (int part = 0; part < 2; part++)
+        to[u][part] = SPAN == 1 ? __builtin_amdgcn_raw_buffer_load_b128(hbuf, v, s + part * hstep, 0)
+                                : __builtin_amdgcn_raw_buffer_load_b128(hbuf, v + part * hstep, s, 0);
     }
   };
   // A place in the sequence of halves that this wave multiplies: its tasks,
@@ -949,10 +935,11 @@ hipError_t run(const MoeArgs& a, hipStream_t s) {
     k_moe_up<FMT, false><<<grid, kUpWaves * kWave, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // 8 rows a workgroup where 16 leave compute units idle (16 tokens of 64
-  // experts, 2048 rows: 39 against 60 us), unless the experts are too few to
-  // fill the waves two at a time (one token, 8 experts: 13.7 against 12.7 us).
-  return a.hidden / 16 < cu_count() && a.n * a.top_k > kDownWaves ? down<FMT, 2>(a, s) : down<FMT, 1>(a, s);
+  // 8 rows a workgroup where 16 leave compute units idle (64 experts, 8 of them
+  // a token, 2048 rows; us, whole call: 16 tokens 82 against 104, 2 tokens 27.6
+  // against 33.3), unless the pairs are too few to fill the waves two experts at
+  // a time (16 experts, 2 of them, one token: 18.6 against 16.9).
+  return a.hidden / 16 < cu_count() && a.n * a.top_k >= kDownWaves ? down<FMT, 2>(a, s) : down<FMT, 1>(a, s);
 }
 
 }  // namespace

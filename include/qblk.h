@@ -341,8 +341,8 @@ qblk_status_t qblk_ffn_f8(const uint8_t* w13, const float* s13,
  * gate_up holds experts x (2*inter) rows of hidden weights (per expert the
  * inter rows of G before those of U), down experts x hidden rows of inter
  * weights, both packed in fmt (QBLK_Q4_0, QBLK_SB4, QBLK_SB4_AFFINE or
- * QBLK_Q4_K; hidden and inter multiples of its block).  X is n x hidden of
- * type xt in {F16, BF16}, Y n x hidden of type yt.
+ * QBLK_Q4_K; hidden and inter multiples of its block, at most 2^19).  X is
+ * n x hidden of type xt in {F16, BF16}, Y n x hidden of type yt.
  *
  * Routing.  With logits (n x experts fp32) the call chooses each token's
  * top_k experts itself, in descending order of the logit, equal logits in

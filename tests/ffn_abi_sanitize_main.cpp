@@ -108,6 +108,7 @@ int main() {
   REJECTS(qblk_gemm_f8(A, S, 4, 100, C, S, 2, Y, QBLK_F32, nullptr, 0, s), QBLK_ERR_SHAPE);
   REJECTS(qblk_gemm_f8(A, S, 4, 128, C, S, -2, Y, QBLK_F32, nullptr, 0, s), QBLK_ERR_SHAPE);
   REJECTS(qblk_gemm_f8(A, S, (int64_t(1) << 26) + 1, 128, C, S, 2, Y, QBLK_F32, nullptr, 0, s), QBLK_ERR_SHAPE);
+  REJECTS(qblk_gemm_f8(A, S, 16, (int64_t(1) << 24) + 128, C, S, 2, Y, QBLK_F32, nullptr, 0, s), QBLK_ERR_SHAPE);
   REJECTS(qblk_gemm_f8(A, S, int64_t(1) << 26, 128, C, S, kMax, Y, QBLK_F32, nullptr, 0, s), QBLK_ERR_SHAPE);
   REJECTS(qblk_gemm_f8(A, S, 4, 128, C, S, 2, Y, bad, nullptr, 0, s), QBLK_ERR_DTYPE);
   REJECTS(qblk_gemm_f8(nullptr, S, 4, 128, C, S, 2, Y, QBLK_F32, nullptr, 0, s), QBLK_ERR_NULL);
@@ -180,6 +181,8 @@ int main() {
   WITH(hidden, INT64_MAX / 256 * 256, QBLK_ERR_SHAPE);
   WITH(inter, -256, QBLK_ERR_SHAPE);
   WITH(inter, int64_t(1) << 40, QBLK_ERR_SHAPE);
+  WITH(inter, (int64_t(1) << 19) + 256, QBLK_ERR_SHAPE);
+  WITH(hidden, (int64_t(1) << 19) + 256, QBLK_ERR_SHAPE);
   WITH(experts, 0, QBLK_ERR_SHAPE);
   WITH(experts, 513, QBLK_ERR_SHAPE);
   WITH(top_k, 0, QBLK_ERR_SHAPE);
