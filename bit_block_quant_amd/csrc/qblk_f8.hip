@@ -912,12 +912,17 @@ hipError_t few_src(const uint8_t* w, const float* ws, int64_t m, int64_t k, cons
 }
 
 // Y = W X^T (or, for up_row > 0, H) by k_f8_few.  With no more row tiles than
-// compute units one workgroup is all that a unit gets: 16 waves then, so that
-// it has as much in flight as two of 8.
+// compute units one workgroup is all that a unit gets: 16 waves then, if 8 had
+// more than four groups each or more than one round of x to quantize (m = 4096,
+// us, 16 and 8 waves: k = 11008, n = 1: 13.2 and 14.6; k = 4096, n = 4: 6.5 and
+// 7.4; but n = 1: 6.3 and 5.8).  With more rows 8 (m = 22016, k = 4096, n = 4
+// as codes: 23.0, with 16 28.6).
 hipError_t few_product(const uint8_t* w, const float* ws, int64_t m, int64_t k, const FewX& x, int64_t n, void* y,
                        int yt, int64_t up_row, hipStream_t s) {
   if (up_row > 0) return few_src<2, 8, true>(w, ws, m, k, x, n, y, yt, up_row, s);
-  if ((m + 15) / 16 <= cu_count()) return few_src<1, 16, false>(w, ws, m, k, x, n, y, yt, 0, s);
+  const int64_t G = k / kGroup;
+  if ((m + 15) / 16 <= cu_count() && (G > 32 || (x.xt != kCodes && n * G > 64)))
+    return few_src<1, 16, false>(w, ws, m, k, x, n, y, yt, 0, s);
   return few_src<1, 8, false>(w, ws, m, k, x, n, y, yt, 0, s);
 }
 
@@ -1025,7 +1030,11 @@ bool use_few(int64_t m, int64_t k, int64_t n) {
   return us <= tile_plan(m, k, n, true).us;
 }
 
-// Whether a product quantizes its x inside every workgroup.
+// Whether a product quantizes its x inside every workgroup: that saves a launch
+// (k = 4096, us, with and without: n = 1, m = 4096 5.8, 7.5; m = 22016 21.2,
+// 22.9; n = 4, m = 4096 6.5, 8.0), but each of them does it again (n = 8, m =
+// 4096 8.7, 8.0; n = 4, m = 22016 24.3, 23.0; k = 11008, m = 4096, n = 2 14.9,
+// 15.3; n = 4 16.8, 15.5).
 bool fused_quant(int64_t n, int64_t k) { return n <= 4 && n * k <= 32768; }
 
 // y = 0 (an empty sum), any element type

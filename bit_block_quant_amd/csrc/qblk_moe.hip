@@ -935,11 +935,13 @@ hipError_t run(const MoeArgs& a, hipStream_t s) {
     k_moe_up<FMT, false><<<grid, kUpWaves * kWave, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // 8 rows a workgroup where 16 leave compute units idle (64 experts, 8 of them
-  // a token, 2048 rows; us, whole call: 16 tokens 82 against 104, 2 tokens 27.6
-  // against 33.3), unless the pairs are too few to fill the waves two experts at
-  // a time (16 experts, 2 of them, one token: 18.6 against 16.9).
-  return a.hidden / 16 < cu_count() && a.n * a.top_k >= kDownWaves ? down<FMT, 2>(a, s) : down<FMT, 1>(a, s);
+  // 8 rows of two experts a workgroup where 16 rows leave compute units idle
+  // (hidden 2048, us, whole call: 64 experts, 8 of them a token: 16 tokens 86
+  // against 112 with 16 rows, 2 tokens 27.7 and 30.9, one 20.6 and 23.1; 16
+  // experts, 2 of them, one token: 16.8 and 16.7).  Where they do not, half of
+  // the tile's products are for nothing (hidden 4096: 64 tokens 253 and 184, one
+  // token 31.5 and 26.4).
+  return a.hidden / 16 < cu_count() ? down<FMT, 2>(a, s) : down<FMT, 1>(a, s);
 }
 
 }  // namespace
