@@ -471,20 +471,27 @@ __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restri
 // exact to fp32 rounding.  It is taken for fp32 results and for the first
 // product of a gated layer with an fp16 or fp32 result.
 //
-// LDS layout: 128 bytes per row, the row's 16-byte chunk c at c ^ (row & 7),
-// so that the 16 rows of an operand read hit 8 different chunk columns.  The
-// stages are filled by loads straight to LDS, which write 64 x 16 consecutive
-// bytes: the exchange of chunks is made on the global address.
+// LDS layout.  The stages are filled by loads straight to LDS, which write what
+// 64 lanes load to 64 x 16 consecutive bytes: 8 whole rows of 128 bytes.  The
+// banks are spread by where the loads' KBs lie, 32 bytes apart, each with every
+// eighth row of 64: row 16 t + r is row 2 t + (r >> 3 ^ r >> 2 & 1) of KB r & 7.
+// The 16 rows of an operand then start at 8 of the 16 columns of banks, and the
+// two quarters that one phase of a read takes (8 rows of each) lie next to one
+// another; every operand is at a constant distance from a lane's place.  (The 16-
+// byte chunks of a row exchanged instead: as few conflicts, 1-3% slower at 4096
+// tokens.)
 typedef int int8v __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void glob_void;
 
 constexpr int kTileRows = 256;
 
+// 64 rows of a stage: see above.
+constexpr int kSlice = 8 * kGroup + 32, kBlock64 = 8 * kSlice;
 template <int NT>
 struct Stage {
-  uint8_t a[kTileRows * kGroup];
-  uint8_t b[64 * NT * kGroup];
+  uint8_t a[kTileRows / 64 * kBlock64];
+  uint8_t b[NT * kBlock64];
 };
 // The scales of 4 groups: every token's, and (in the first 8) the two row
 // halves'; as the copies to LDS leave them, 64 consecutive floats each.
@@ -504,17 +511,18 @@ struct TileLds {
   Scales<NT> sc[2];
 };
 
-// A group's operands of a 16-row tile: lane (row r, quarter q) gives the row's
-// chunks q and q + 4 (both sides in the same order).  EXACT: widened to bf16.
+// A group's operands of 16-row tile `tile`: lane (row r, quarter q), whose place
+// in a tile is `at`, gives the row's chunks q and q + 4 (both sides in the same
+// order).  EXACT: widened to bf16.
 template <bool EXACT>
 struct Frag;
 template <>
 struct Frag<false> {
   int8v v;
-  __device__ __forceinline__ void load(const uint8_t* base, int row, int q) {
-    const int key = (row >> 1) & 7;
-    const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * kGroup + ((q ^ key) << 4));
-    const u32x4 hi = *reinterpret_cast<const u32x4*>(base + row * kGroup + (((q + 4) ^ key) << 4));
+  __device__ __forceinline__ void load(const uint8_t* base, int tile, int at) {
+    const uint8_t* p = base + (tile >> 2) * kBlock64 + (tile & 3) * 2 * kGroup + at;
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(p);
+    const u32x4 hi = *reinterpret_cast<const u32x4*>(p + kGroup / 2);
     v = int8v{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
               static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
   }
@@ -522,10 +530,10 @@ struct Frag<false> {
 template <>
 struct Frag<true> {
   bf16x8_n v[4];
-  __device__ __forceinline__ void load(const uint8_t* base, int row, int q) {
-    const int key = (row >> 1) & 7;
-    const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * kGroup + ((q ^ key) << 4));
-    const u32x4 hi = *reinterpret_cast<const u32x4*>(base + row * kGroup + (((q + 4) ^ key) << 4));
+  __device__ __forceinline__ void load(const uint8_t* base, int tile, int at) {
+    const uint8_t* p = base + (tile >> 2) * kBlock64 + (tile & 3) * 2 * kGroup + at;
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(p);
+    const u32x4 hi = *reinterpret_cast<const u32x4*>(p + kGroup / 2);
     v[0] = widen8(lo.x, lo.y);
     v[1] = widen8(lo.z, lo.w);
     v[2] = widen8(hi.x, hi.y);
@@ -582,28 +590,30 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
   const uint8_t* abase[2] = {p.w + static_cast<int64_t>(row0) * p.k, p.w + second * p.k};
   const uint8_t* bbase = p.xq + static_cast<int64_t>(t0) * p.k;
   uint32_t ao[4], bo[NT];
+  // this lane's row of 64
+  const int row64 = 16 * (lane >> 4) + 8 * (((lane >> 3) ^ (wave >> 2)) & 1) + wave;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int row = 64 * i + 8 * wave + (lane >> 3);
+    const int row = 64 * i + row64;
     int at = GATE ? row & 127 : row;
     if (!GATE && at > p.m - 1 - row0) at = p.m - 1 - row0;
-    ao[i] = static_cast<uint32_t>(at) * static_cast<uint32_t>(p.k) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+    ao[i] = static_cast<uint32_t>(at) * static_cast<uint32_t>(p.k) + ((lane & 7) << 4);
   }
 #pragma unroll
   for (int i = 0; i < NT; i++) {
-    const int row = 64 * i + 8 * wave + (lane >> 3);
+    const int row = 64 * i + row64;
     const int at = t0 + row < p.n ? row : p.n - 1 - t0;
-    bo[i] = static_cast<uint32_t>(at) * static_cast<uint32_t>(p.k) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+    bo[i] = static_cast<uint32_t>(at) * static_cast<uint32_t>(p.k) + ((lane & 7) << 4);
   }
   // chunk i of 4 + NT: the rows of A, then those of B
   auto copy = [&](Stage<NT>& s, int g, int i) {
     const int64_t at = static_cast<int64_t>(g) * kGroup;
     if (i < 4)
       __builtin_amdgcn_global_load_lds((glob_void*)((i < 2 ? abase[0] : abase[1]) + at + ao[i & 3]),
-                                       (lds_void*)(s.a + (64 * i + 8 * wave) * kGroup), 16, 0, 0);
+                                       (lds_void*)(s.a + i * kBlock64 + wave * kSlice), 16, 0, 0);
     else if (i < 4 + NT)
       __builtin_amdgcn_global_load_lds((glob_void*)(bbase + at + bo[i - 4]),
-                                       (lds_void*)(s.b + (64 * (i - 4) + 8 * wave) * kGroup), 16, 0, 0);
+                                       (lds_void*)(s.b + (i - 4) * kBlock64 + wave * kSlice), 16, 0, 0);
   };
 
   const int wm = wave & 1, wn = wave >> 1;
@@ -644,7 +654,8 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
   Frag<EXACT> bf[NT], af[2];
   float4_t c[2][NT];
   float sc[2][NT];
-  auto arow = [&](int i) { return (i >> 2) * 128 + wm * 64 + (i & 3) * 16 + r; };
+  auto atile = [&](int i) { return (i >> 2) * 8 + wm * 4 + (i & 3); };
+  const int place = (r & 7) * kSlice + (((r >> 3) ^ (r >> 2)) & 1) * kGroup + 16 * q;
   auto scale = [&](int i, int j) {
 #pragma unroll
     for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(c[i & 1][j][e], sc[i >> 2][j], acc[i][j][e]);
@@ -661,9 +672,9 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
   auto group_at = [&](int step) { return g0 + step < g1 ? g0 + step : g1 - 1; };
   copy(st[kAhead], group_at(kAhead), 0);
   copy(st[kAhead], group_at(kAhead), 1);
-  af[0].load(st[0].a, arow(0), q);
+  af[0].load(st[0].a, atile(0), place);
 #pragma unroll
-  for (int j = 0; j < NT; j++) bf[j].load(st[0].b, (wn * NT + j) * 16 + r, q);
+  for (int j = 0; j < NT; j++) bf[j].load(st[0].b, wn * NT + j, place);
   int now = 0;
   for (int g = g0; g < g1; g++) {
     const int step = g - g0;
@@ -687,7 +698,7 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       if (i + 1 < 8) {
-        af[(i + 1) & 1].load(cur.a, arow(i + 1), q);
+        af[(i + 1) & 1].load(cur.a, atile(i + 1), place);
       } else if constexpr (kStages<NT> == 2) {
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
@@ -704,7 +715,7 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
       for (int j = 0; j < NT; j++) {
         c[i & 1][j] = group_product(af[i & 1], bf[j]);
         if (i > 0) scale(i - 1, j);
-        if (i + 1 == 8) bf[j].load(nxt.b, (wn * NT + j) * 16 + r, q);
+        if (i + 1 == 8) bf[j].load(nxt.b, wn * NT + j, place);
       }
       // Each matrix instruction with the four multiply-adds of a finished tile
       // behind it; the LDS reads after the first (before it they would be
@@ -723,7 +734,7 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
           if (j < 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
       } else {
-        af[0].load(nxt.a, arow(0), q);
+        af[0].load(nxt.a, atile(0), place);
         copy(cur, gc, 0);
         copy(cur, gc, 1);
 #pragma unroll
