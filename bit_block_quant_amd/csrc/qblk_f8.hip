@@ -646,12 +646,12 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
     for (int j = 0; j < NT; j++) acc[i][j] = float4_t{0, 0, 0, 0};
 
   // Software pipeline.  Within a stage: while the matrix cores work on row
-  // tile i, its successor's operand is read from LDS and tile i - 1 is scaled.
-  // Across stages: at the last row tile every operand of the stage is in
-  // registers, so one barrier there frees its buffer for the copies two
-  // stages on and shows the next stage's, whose first operands are read
-  // behind the last matrix instructions.
-  Frag<EXACT> bf[NT], af[2];
+  // tile i, the operand of tile i + 2 is read from LDS and tile i - 1 is scaled.
+  // Across stages: before the last two row tiles every operand of the stage is
+  // in registers, so one barrier there frees its buffer for the copies of a
+  // later stage and shows the next stage's, whose first operands are read
+  // behind the matrix instructions of those two.
+  Frag<EXACT> bf[NT], af[4];
   float4_t c[2][NT];
   float sc[2][NT];
   auto atile = [&](int i) { return (i >> 2) * 8 + wm * 4 + (i & 3); };
@@ -669,10 +669,12 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
   }
   __syncthreads();
   constexpr int kAhead = kStages<NT> - 1;  // stages whose copies are on their way
+  constexpr int kEarly = kStages<NT> == 2 ? 4 : 2;  // copies that go out behind the barrier
   auto group_at = [&](int step) { return g0 + step < g1 ? g0 + step : g1 - 1; };
-  copy(st[kAhead], group_at(kAhead), 0);
-  copy(st[kAhead], group_at(kAhead), 1);
+#pragma unroll
+  for (int e = 0; e < kEarly; e++) copy(st[kAhead], group_at(kAhead), e);
   af[0].load(st[0].a, atile(0), place);
+  af[1].load(st[0].a, atile(1), place);
 #pragma unroll
   for (int j = 0; j < NT; j++) bf[j].load(st[0].b, wn * NT + j, place);
   int now = 0;
@@ -697,52 +699,50 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      if (i + 1 < 8) {
-        af[(i + 1) & 1].load(cur.a, atile(i + 1), place);
-      } else if constexpr (kStages<NT> == 2) {
-        __syncthreads();
+      if (i < 6) {
+        af[(i + 2) & 3].load(cur.a, atile(i + 2), place);
+      } else if (i == 6) {
+        if constexpr (kStages<NT> == 2) {
+          __syncthreads();
+        } else {
+          // as __syncthreads, but leaving the newest 4 + NT loads under way: the
+          // copies of the stage after next (all older ones are the next stage's)
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+          __builtin_amdgcn_s_waitcnt(0x0070 | (4 + NT));  // vmcnt(4 + NT) lgkmcnt(0)
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
         __builtin_amdgcn_sched_barrier(0);
+        af[0].load(nxt.a, atile(0), place);
+#pragma unroll
+        for (int e = 0; e < kEarly / 2; e++) copy(cur, gc, e);
       } else {
-        // as __syncthreads, but leaving the newest 4 + NT loads under way: the
-        // copies of the stage after next (all older ones are the next stage's)
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_s_waitcnt(0x0070 | (4 + NT));  // vmcnt(4 + NT) lgkmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        __builtin_amdgcn_sched_barrier(0);
+        af[1].load(nxt.a, atile(1), place);
+#pragma unroll
+        for (int e = kEarly / 2; e < kEarly; e++) copy(cur, gc, e);
       }
 #pragma unroll
       for (int j = 0; j < NT; j++) {
-        c[i & 1][j] = group_product(af[i & 1], bf[j]);
+        c[i & 1][j] = group_product(af[i & 3], bf[j]);
         if (i > 0) scale(i - 1, j);
-        if (i + 1 == 8) bf[j].load(nxt.b, wn * NT + j, place);
+        if (i == 7) bf[j].load(nxt.b, wn * NT + j, place);
       }
       // Each matrix instruction with the four multiply-adds of a finished tile
       // behind it; the LDS reads after the first (before it they would be
-      // waited for together with the operand it needs).  The copies are spread
-      // over four row tiles: issued at once they hold up the waves' issue.
-      if (i + 1 < 8) {
-        if (i < 3) {
-          copy(far, gf, 2 * i + 2);
-          copy(far, gf, 2 * i + 3);
-        }
+      // waited for together with the operand it needs).  The copies are spread,
+      // two a row tile: all at once they hold up the waves' issue (m = n = k =
+      // 8192: 454 us; four a tile 512, one a tile 492), and with three stages
+      // the first ones one a tile (m = 4096, k = 11008, n = 1501: 72 and 74 us).
+      if (i < 3) {
+        copy(far, gf, kEarly + 2 * i);
+        copy(far, gf, kEarly + 2 * i + 1);
+      }
 #pragma unroll
-        for (int j = 0; j < NT && !EXACT; j++) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          if (j == 0) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-          if (j < 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        }
-      } else {
-        af[0].load(nxt.a, atile(0), place);
-        copy(cur, gc, 0);
-        copy(cur, gc, 1);
-#pragma unroll
-        for (int j = 0; j < NT && !EXACT; j++) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-        }
+      for (int j = 0; j < NT && !EXACT; j++) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (j == 0 || i == 7) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        if (j < 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
