@@ -188,6 +188,16 @@ __device__ __forceinline__ bf16x8_n widen8(uint32_t a, uint32_t b) {
   return bf16x8_n{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 }
 
+__device__ __forceinline__ u32x2 bits16(const float4_t& v, int yt) {
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) h[e] = yt == QBLK_F16 ? f32_to_f16_bits(v[e]) : f32_to_bf16_bits(v[e]);
+  return u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+}
+
+// floats from one token's partial sums to the next one's
+__host__ __device__ __forceinline__ int64_t part_pitch(int64_t m) { return (m + 3) & ~int64_t(3); }
+
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int yt) {
   if (yt == QBLK_F32)
     static_cast<float*>(y)[at] = v;
@@ -802,10 +812,15 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
       for (int i = 0; i < 8; i++) {
         const int row = row0 + (i >> 2) * 128 + wm * 64 + (i & 3) * 16 + 4 * q;
         if (row >= p.m) continue;
+        if constexpr (SPLIT) {  // rows of partial sums lie 16-byte aligned
+          float* part = p.part + (static_cast<int64_t>(blockIdx.y) * p.n + tok) * part_pitch(p.m) + row;
+          *reinterpret_cast<float4_t*>(part) = acc[i][j];
+          continue;
+        }
         const int64_t at = static_cast<int64_t>(tok) * p.m + row;
         const bool whole = row + 4 <= p.m && (p.m & 3) == 0;  // 4 consecutive values, aligned
-        if (SPLIT || p.yt == QBLK_F32) {
-          float* y = SPLIT ? p.part + static_cast<int64_t>(blockIdx.y) * p.n * p.m : static_cast<float*>(p.y);
+        if (p.yt == QBLK_F32) {
+          float* y = static_cast<float*>(p.y);
           if (whole) {
             *reinterpret_cast<float4_t*>(y + at) = acc[i][j];
           } else {
@@ -814,16 +829,14 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
               if (row + e < p.m) y[at + e] = acc[i][j][e];
           }
         } else {
-          uint16_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; e++) h[e] = p.yt == QBLK_F16 ? f32_to_f16_bits(acc[i][j][e]) : f32_to_bf16_bits(acc[i][j][e]);
+          const u32x2 h = bits16(acc[i][j], p.yt);
           uint16_t* y = static_cast<uint16_t*>(p.y) + at;
           if (whole) {
-            *reinterpret_cast<u32x2*>(y) = u32x2{h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16)};
+            *reinterpret_cast<u32x2*>(y) = h;
           } else {
 #pragma unroll
             for (int e = 0; e < 4; e++)
-              if (row + e < p.m) y[e] = h[e];
+              if (row + e < p.m) y[e] = static_cast<uint16_t>(h[e >> 1] >> (16 * (e & 1)));
           }
         }
       }
@@ -831,15 +844,34 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
   }
 }
 
-// y = the sum of the splits' partial products, in their order
-__global__ __launch_bounds__(256) void k_f8_join(const float* __restrict__ part, int64_t first, int64_t count,
+// y = the sum of the splits' partial products, in their order: a thread takes 4
+// rows of a token.
+__global__ __launch_bounds__(256) void k_f8_join(const float* __restrict__ part, int64_t first, int64_t count, int m,
                                                  int64_t stride, int splits, void* __restrict__ y, int yt) {
   int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= count) return;
   i += first;
-  float v = 0.0f;
-  for (int s = 0; s < splits; s++) v += part[s * stride + i];
-  store_y(y, i, v, yt);
+  const uint32_t chunks = static_cast<uint32_t>(part_pitch(m) / 4);
+  const int64_t tok = i / chunks;
+  const int row = 4 * static_cast<int>(i - tok * chunks);
+  const float* p = part + 4 * i;
+  float4_t v = *reinterpret_cast<const float4_t*>(p);
+  for (int s = 1; s < splits; s++) {
+    const float4_t o = *reinterpret_cast<const float4_t*>(p + s * stride);
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] += o[e];
+  }
+  const int64_t at = tok * m + row;
+  if ((m & 3) == 0) {  // 4 consecutive values, aligned
+    if (yt == QBLK_F32)
+      *reinterpret_cast<float4_t*>(static_cast<float*>(y) + at) = v;
+    else
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(y) + at) = bits16(v, yt);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (row + e < m) store_y(y, at + e, v[e], yt);
+  }
 }
 
 // The codes and scales of H = silu(gate) * up from the splits' partial products
@@ -1020,8 +1052,10 @@ hipError_t tile_product(const uint8_t* w, const float* ws, int64_t m, int64_t k,
         a.part, m * n, plan.splits, static_cast<int>(up), groups, static_cast<uint8_t*>(y), hs, at.tok, at.group);
     return hipGetLastError();
   }
-  return in_pieces(m * n, 256, 256, [&](int64_t first, int64_t c) {
-    k_f8_join<<<dim3(static_cast<unsigned>((c + 255) / 256)), 256, 0, s>>>(a.part, first, c, m * n, plan.splits, y, yt);
+  const int64_t pitch = part_pitch(m);
+  return in_pieces(n * pitch / 4, 256, 256, [&](int64_t first, int64_t c) {
+    k_f8_join<<<dim3(static_cast<unsigned>((c + 255) / 256)), 256, 0, s>>>(a.part, first, c, static_cast<int>(m), n * pitch,
+                                                                         plan.splits, y, yt);
     return hipGetLastError();
   });
 }
@@ -1114,7 +1148,7 @@ int64_t gemm_f8_workspace(int64_t m, int64_t k, int64_t n) {
   if (use_few(m, k, n)) return 0;
   const int a = tile_plan(m, k, n, false).splits, b = tile_plan(m, k, n, true).splits;
   const int most = a > b ? a : b;
-  return most > 1 ? align256(most * n * m * 4) : 0;
+  return most > 1 ? align256(most * n * part_pitch(m) * 4) : 0;
 }
 
 hipError_t launch_gemm_f8(const uint8_t* w, const float* ws, int64_t m, int64_t k, const uint8_t* xq,
