@@ -981,21 +981,19 @@ struct Plan {
   double us;            // the estimate by which it was taken
 };
 
-//
-// The time of each is estimated from what was measured for the kernel's
+// The time of each shape is estimated from what was measured for the kernel's
 // variants (us: a stage of a tile, then the rest of a tile's time, for 64, 128
-// and 256 tokens; a stage is bound by the matrix cores only in the widest) and
-// the least taken.  (A gated product's split tiles leave gate and up apart in the
-// partial sums, and the join forms h.)  A split is worth its join where tiles leave compute units
-// without work: m = k = 4096, n = 128: 64-token tiles unsplit 24.0 us, split by
-// 4 16.5; n = 1024: 29.5 against 65.  Wide tiles pay with many tokens: m = 14336,
-// k = 4096, n = 4096: 64 tokens 400 us, 128 293, 256 270; n = 512: 58, 41, 69.
-// Over 26 shapes (65 to 4096 tokens, both kinds of sums) the choice was never
-// more than 11% behind the best of all, and 0.5% on average.
+// and 256 tokens) and the least taken.  (A gated product's split tiles leave gate
+// and up apart in the partial sums, and the join forms h.)  A split is worth its
+// join where tiles leave compute units without work: m = k = 4096, n = 128:
+// 64-token tiles unsplit 22.5 us, split by 4 15.6; n = 1024: 28.8 against 61.  Wide tiles pay with many tokens: m = 14336,
+// k = 4096, n = 4096: 64 tokens 391 us, 128 288, 256 257; n = 512: 59, 41, 66.
+// Over 32 shapes (32 to 4096 tokens, both kinds of sums) the choice was never
+// more than 12% behind the best of all, and 0.6% on average.
 Plan tile_plan(int64_t m, int64_t k, int64_t n, bool exact) {
   const int64_t rt = (m + kTileRows - 1) / kTileRows, G = k / kGroup;
   const int cus = cu_count();
-  constexpr double stage[2][3] = {{0.68, 0.9, 1.65}, {1.15, 1.55, 0}}, ends[2][3] = {{5, 8, 11}, {5, 7, 0}};
+  constexpr double stage[2][3] = {{0.66, 0.8, 1.5}, {1.15, 1.6, 0}}, ends[2][3] = {{5, 8, 9}, {5, 7, 0}};
   Plan best{1, 1, static_cast<int>(G), 1e30};
   for (int nt = 1; nt <= (exact ? 2 : 4); nt *= 2) {
     const int64_t tiles = rt * ((n + 64 * nt - 1) / (64 * nt));
@@ -1004,7 +1002,7 @@ Plan tile_plan(int64_t m, int64_t k, int64_t n, bool exact) {
       const int64_t per = (G + sp - 1) / sp;
       const int64_t rounds = (tiles * sp + cus - 1) / cus;
       const double c = rounds * (per * stage[exact][nt >> 1] + ends[exact][nt >> 1]) +
-                       (sp > 1 ? 2.5 + 0.4e-6 * sp * n * m * 4 : 0.0);
+                       (sp > 1 ? 2.0 + 0.35e-6 * sp * n * m * 4 : 0.0);
       if (c < best.us) best = Plan{nt, sp, static_cast<int>(per), c};
     }
   }
@@ -1073,11 +1071,12 @@ constexpr int64_t kExactTokens = 64;
 // 16 rows); up to 64 where its estimate is below the tile kernel's.  It keeps all
 // compute units busy with few rows, but reads x again for every 16 of them
 // (us, few and tiles: 32 tokens, m = k = 4096: 9.8, 14.6; m = 8192, k = 8192:
-// 24.8, 22.5; m = 22016, k = 4096: 37.8, 29.5; 64 tokens: 11.9, 17.4; 42.8, 26.0;
-// 72.0, 32.9).
+// 24.8, 22.5; m = 22016, k = 4096: 37.8, 29.5; m = 4096, k = 14336: 19.6, 24; 64
+// tokens: 11.9, 17.4; 42.8, 26.0; 72.0, 32.9).
 bool use_few(int64_t m, int64_t k, int64_t n) {
   if (n <= 16 || n > kExactTokens) return n <= 16;
-  const double us = n <= 32 ? 3.5 + 0.36e-6 * m * k : 1.0 + 0.68e-6 * m * k;
+  const double rate = n > 32 ? 0.68e-6 : (m + 15) / 16 <= cu_count() ? 0.28e-6 : 0.36e-6;
+  const double us = (n > 32 ? 1.0 : 3.5) + rate * m * k;
   return us <= tile_plan(m, k, n, true).us;
 }
 
