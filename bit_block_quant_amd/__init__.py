@@ -172,6 +172,7 @@ def _need_current(dev):
     cur = torch.cuda.current_device()
     if dev.index is not None and dev.index != cur:
         raise ValueError(f"tensors on {dev}, but the current device is cuda:{cur}")
+    return cur
 
 
 def _need_dims(**dims):
@@ -190,11 +191,11 @@ def _packed(fmt, rows, k):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
+def _stream(stream=None, cur=None):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:  # 0.3 us; the stream object takes 2.8, half a small product's kernel time
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if cur is None else cur)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -389,8 +390,8 @@ def quantize_f8(w, out=None, scale=None, stream=None):
         scale = torch.empty((-(-rows // 128), k // 128), dtype=torch.float32, device=w.device)
     _need_f8(out, scale, "out", dev)
     _need(out, "out", numel=rows * k)
-    _need_current(dev)
-    _check(_lib.qblk_quantize_f8(_ptr(w), _dtype(w), rows, k, _ptr(out), _ptr(scale), _stream(stream)),
+    cur = _need_current(dev)
+    _check(_lib.qblk_quantize_f8(_ptr(w), _dtype(w), rows, k, _ptr(out), _ptr(scale), _stream(stream, cur)),
            "qblk_quantize_f8")
     return out, scale
 
@@ -407,8 +408,8 @@ def quantize_act_f8(x, out=None, scale=None, stream=None):
         scale = torch.empty((n, k // 128), dtype=torch.float32, device=x.device)
     _need(out, "out", _F8_IN, numel=n * k, device=dev)
     _need(scale, "scale", (torch.float32,), numel=n * (k // 128), device=dev)
-    _need_current(dev)
-    _check(_lib.qblk_quantize_act_f8(_ptr(x), _dtype(x), n, k, _ptr(out), _ptr(scale), _stream(stream)),
+    cur = _need_current(dev)
+    _check(_lib.qblk_quantize_act_f8(_ptr(x), _dtype(x), n, k, _ptr(out), _ptr(scale), _stream(stream, cur)),
            "qblk_quantize_act_f8")
     return out, scale
 
@@ -421,9 +422,9 @@ def gemm_f8(wq, ws, xq, xs, dtype=torch.float32, out=None, workspace=None, strea
     _need(xs, "xs", (torch.float32,), numel=n * (k // 128), device=dev)
     out = _out(out, (n, m), dtype, dev)
     work = _workspace(workspace, _lib.qblk_gemm_f8_workspace(m, k, n), dev)
-    _need_current(dev)
+    cur = _need_current(dev)
     _check(_lib.qblk_gemm_f8(_ptr(wq), _ptr(ws), m, k, _ptr(xq), _ptr(xs), n, _ptr(out), _dtype(out), _ptr(work),
-                             _nbytes(work), _stream(stream)), "qblk_gemm_f8")
+                             _nbytes(work), _stream(stream, cur)), "qblk_gemm_f8")
     return out
 
 
@@ -435,9 +436,9 @@ def linear_f8(x, wq, ws, dtype=None, out=None, workspace=None, stream=None):
     n = x.shape[0]
     out = _out(out, (n, m), dtype or x.dtype, dev)
     work = _workspace(workspace, _lib.qblk_linear_f8_workspace(m, k, n), dev)
-    _need_current(dev)
+    cur = _need_current(dev)
     _check(_lib.qblk_linear_f8(_ptr(wq), _ptr(ws), m, k, _ptr(x), _dtype(x), n, _ptr(out), _dtype(out), _ptr(work),
-                               _nbytes(work), _stream(stream)), "qblk_linear_f8")
+                               _nbytes(work), _stream(stream, cur)), "qblk_linear_f8")
     return out
 
 
@@ -454,9 +455,9 @@ def ffn_f8(x, w13, s13, w2, s2, dtype=None, out=None, workspace=None, stream=Non
     n = x.shape[0]
     out = _out(out, (n, hidden), dtype or x.dtype, dev)
     work = _workspace(workspace, _lib.qblk_ffn_f8_workspace(hidden, inter, n), dev)
-    _need_current(dev)
+    cur = _need_current(dev)
     _check(_lib.qblk_ffn_f8(_ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), hidden, inter, _ptr(x), _dtype(x), n, _ptr(out),
-                            _dtype(out), _ptr(work), _nbytes(work), _stream(stream)), "qblk_ffn_f8")
+                            _dtype(out), _ptr(work), _nbytes(work), _stream(stream, cur)), "qblk_ffn_f8")
     return out
 
 
@@ -496,11 +497,13 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
     else:
         _need_dims(experts=experts)
     if ids is None:
-        ids = torch.empty((n, top_k), dtype=torch.int32, device=x.device)
+        ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
+    else:
+        _need(ids, "ids", (torch.int32,), numel=n * top_k, device=dev)
     if weights is None:
-        weights = torch.empty((n, top_k), dtype=torch.float32, device=x.device)
-    _need(ids, "ids", (torch.int32,), numel=n * top_k, device=dev)
-    _need(weights, "weights", (torch.float32,), numel=n * top_k, device=dev)
+        weights = torch.empty((n, top_k), dtype=torch.float32, device=dev)
+    else:
+        _need(weights, "weights", (torch.float32,), numel=n * top_k, device=dev)
     _need(gate_up, "gate_up", (torch.uint8,), min_numel=_packed(fmt, experts * 2 * inter, hidden), device=dev)
     _need(down, "down", (torch.uint8,), min_numel=_packed(fmt, experts * hidden, inter), device=dev)
     out = _out(out, (n, hidden), dtype or x.dtype, dev)
@@ -509,6 +512,6 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
     a.x, a.xt, a.logits, a.renorm, a.weight_scale = _ptr(x), _DT[x.dtype], _ptr(logits), int(renorm), weight_scale
     a.gate_up, a.down, a.ids, a.weights = _ptr(gate_up), _ptr(down), _ptr(ids), _ptr(weights)
     a.y, a.yt, a.workspace, a.workspace_bytes = _ptr(out), _dtype(out), _ptr(work), _nbytes(work)
-    _need_current(dev)
-    _check(_lib.qblk_moe(C.byref(a), _stream(stream)), "qblk_moe")
+    cur = _need_current(dev)
+    _check(_lib.qblk_moe(C.byref(a), _stream(stream, cur)), "qblk_moe")
     return out, ids, weights

@@ -278,7 +278,8 @@ def test_ffn_f8_long_sums(q, hidden, inter, n, dtype):
     assert torch.equal(y, q.ffn_f8(x, w13, s13, w2, s2))
 
 
-@pytest.mark.parametrize("m,k,n", [(9000, 8192, 17), (9000, 8192, 64), (40, 11008, 7), (5000, 11008, 333)])
+@pytest.mark.parametrize("m,k,n", [(9000, 8192, 17), (9000, 8192, 64), (40, 11008, 7), (5000, 11008, 333), (1003, 4096, 70),
+                                   (2, 4096, 300), (4097, 8192, 31)])
 def test_gemm_f8_large(q, m, k, n):
     """Sizes on the tile kernel's side up to 64 tokens, long sums, many splits."""
     wq, ws, xq, xs, _ = f8_operands(q, m, k, n, 3)
@@ -549,7 +550,8 @@ class Padded:
         return bool(np.all(w[:MARGIN] == 0xFF) and np.all(w[MARGIN + self.n:] == 0xFF))
 
 
-@pytest.mark.parametrize("m,k,n", [(1, 128, 1), (37, 256, 3), (130, 384, 18), (515, 256, 70), (257, 640, 300), (1000, 1152, 513)])
+@pytest.mark.parametrize("m,k,n", [(1, 128, 1), (37, 256, 3), (130, 384, 18), (515, 256, 70), (257, 640, 300), (1000, 1152, 513),
+                                   (1003, 2048, 70), (254, 2048, 129), (1, 1024, 65), (3, 128, 200)])
 def test_f8_bounds(q, m, k, n):
     wq, ws, xq, xs, x = f8_operands(q, m, k, n, 1)
     want = q.gemm_f8(wq, ws, xq, xs)
