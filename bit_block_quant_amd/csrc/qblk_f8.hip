@@ -52,12 +52,16 @@ __device__ __forceinline__ void load8(const void* x, int64_t at, float v[8]) {
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __builtin_expf(-g)) * u; }
 
+// The larger, NaN if one is: a NaN among 128 values makes their scale NaN and so
+// every result that they enter, where a maximum of numbers would pass over it.
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // max over the 16 lanes of a DPP row, in every lane
 __device__ __forceinline__ float row16_max(float v) {
-  v = __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, true)));
-  v = __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, true)));
-  v = __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xF, 0xF, true)));
-  v = __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x140, 0xF, 0xF, true)));
+  v = max_nan(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, true)));
+  v = max_nan(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, true)));
+  v = max_nan(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xF, 0xF, true)));
+  v = max_nan(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x140, 0xF, 0xF, true)));
   return v;
 }
 
@@ -87,7 +91,7 @@ __device__ __forceinline__ void codes_f8(const float v[N], float s, uint32_t out
     for (int i = 0; i < N; i++) q[i] = qdiv(v[i], s);
   }
 #pragma unroll
-  for (int i = 0; i < N; i++) q[i] = __builtin_amdgcn_fmed3f(q[i], -kF8Max, kF8Max);
+  for (int i = 0; i < N; i++) q[i] = __builtin_elementwise_minimum(max_nan(q[i], -kF8Max), kF8Max);
 #pragma unroll
   for (int i = 0; i < N / 4; i++) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
@@ -100,7 +104,7 @@ __device__ __forceinline__ void codes_f8(const float v[N], float s, uint32_t out
 __device__ __forceinline__ float quant_group(const float v[8], uint32_t code[2]) {
   float a = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; i++) a = __builtin_fmaxf(a, __builtin_fabsf(v[i]));
+  for (int i = 0; i < 8; i++) a = max_nan(a, __builtin_fabsf(v[i]));
   const float s = row16_max(a) / kF8Max;
   codes_f8<8>(v, s, code);
   return s;
@@ -157,16 +161,18 @@ __global__ __launch_bounds__(256) void k_quant_f8(const void* __restrict__ w, in
     if (row < rows) {
       load8<XT>(w, row * k + bc * kGroup + 8 * l, v[j]);
 #pragma unroll
-      for (int i = 0; i < 8; i++) a = __builtin_fmaxf(a, __builtin_fabsf(v[j][i]));
+      for (int i = 0; i < 8; i++) a = max_nan(a, __builtin_fabsf(v[j][i]));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; i++) v[j][i] = 0.0f;
     }
   }
-  a = group_max<kWave>(a);
+  a = row16_max(a);
+  a = max_nan(a, __shfl_xor(a, 16, kWave));
+  a = max_nan(a, __shfl_xor(a, 32, kWave));
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
   __syncthreads();
-  a = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), __builtin_fmaxf(part[2], part[3]));
+  a = max_nan(max_nan(part[0], part[1]), max_nan(part[2], part[3]));
   const float s = a / kF8Max;
 #pragma unroll
   for (int j = 0; j < 8; j++) {
@@ -779,10 +785,10 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
 #pragma unroll
         for (int e = 0; e < 4; e++) {
           acc[i][j][e] = silu_mul(acc[i][j][e], acc[i + 4][j][e]);
-          a = __builtin_fmaxf(a, __builtin_fabsf(acc[i][j][e]));
+          a = max_nan(a, __builtin_fabsf(acc[i][j][e]));
         }
-      a = __builtin_fmaxf(a, __shfl_xor(a, 16, kWave));
-      top[j] = __builtin_fmaxf(a, __shfl_xor(a, 32, kWave));
+      a = max_nan(a, __shfl_xor(a, 16, kWave));
+      top[j] = max_nan(a, __shfl_xor(a, 32, kWave));
     }
     float* m2 = reinterpret_cast<float*>(lds);  // [2][64 NT]
     __syncthreads();
@@ -794,7 +800,7 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
 #pragma unroll
     for (int j = 0; j < NT; j++) {
       const int in = (wn * NT + j) * 16 + r, tok = t0 + in;
-      const float s = __builtin_fmaxf(m2[in], m2[64 * NT + in]) / kF8Max;
+      const float s = max_nan(m2[in], m2[64 * NT + in]) / kF8Max;
       float v[16];
       uint32_t c[4];
 #pragma unroll

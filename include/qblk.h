@@ -273,6 +273,8 @@ int qblk_deterministic(void);
  * fp32), or 128 columns of one token (xscale[t][c/128], n x k/128 fp32).
  * Rule: scale = max|v| / 448 in fp32; code = e4m3(clamp(v / scale, +-448)),
  * round to nearest even, both divisions IEEE fp32; a zero scale gives code 0.
+ * A NaN makes the scale of its block NaN, and so what the block enters; with an
+ * infinity the scale is infinite, its own code NaN and the others' 0.
  * k must be a multiple of 128, a product's matrix at most 2^26 rows of at most
  * 2^24 columns (QBLK_ERR_SHAPE).
  *

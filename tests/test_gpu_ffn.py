@@ -180,6 +180,48 @@ def check_product(y, W, X, n):
     assert np.all(np.abs(got - ref) <= product_bound(n) * mag + 2 * HALF_ULP[y.dtype] * np.abs(ref) + 1e-38)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_f8_of_nan_and_infinity(q, dtype):
+    """A NaN or an infinity shows in its group's scale or codes, and nowhere else."""
+    x = torch.randn(5, 384, device="cuda").to(TYPES[dtype])
+    plain, scale = q.quantize_act_f8(x)
+    x[1, 130] = float("nan")
+    x[2, 0] = float("inf")
+    x[3, 383] = -float("inf")
+    x[4, 256:] = float("nan")
+    got, s = q.quantize_act_f8(x)
+    s, c = s.cpu(), got.float().cpu()
+    assert torch.isnan(s[1, 1]) and torch.isnan(s[4, 2]) and torch.isinf(s[2, 0]) and torch.isinf(s[3, 2])
+    assert torch.isnan(c[2, 0]) and torch.all(c[2, 1:128] == 0) and torch.isnan(c[3, 383])
+    for t, g in [(1, 1), (2, 0), (3, 2), (4, 2)]:
+        keep = [i for i in range(3) if i != g]
+        assert torch.equal(s[t, keep], scale.cpu()[t, keep])
+        cols = torch.cat([torch.arange(128 * i, 128 * i + 128) for i in keep])
+        assert torch.equal(c[t, cols], plain.float().cpu()[t, cols])
+    w = torch.randn(256, 384, device="cuda").to(TYPES[dtype])
+    w[200, 7] = float("nan")
+    _, ws = q.quantize_f8(w)
+    assert torch.isnan(ws).sum() == 1 and torch.isnan(ws[1, 0])
+
+
+@pytest.mark.parametrize("n", [3, 9, 40, 100, 300])
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+def test_f8_products_of_nan(q, n, bad):
+    """Every result of a token with a NaN or an infinity is NaN, every other token's is as without."""
+    rng = np.random.default_rng(n)
+    wq, ws, _, _, x = f8_operands(q, 300, 2048, n, n)
+    w13, s13, _, _, _ = f8_operands(q, 512, 2048, 1, n)
+    w2, s2, _, _, _ = f8_operands(q, 2048, 256, 1, n)
+    keep = torch.arange(n, device="cuda") != n // 2
+    for dtype in (torch.float32, torch.bfloat16):
+        x = x.to(dtype)
+        poisoned = x.clone()
+        poisoned[n // 2, 1000] = float(bad)
+        for call in (lambda v: q.linear_f8(v, wq, ws), lambda v: q.ffn_f8(v, w13, s13, w2, s2)):
+            y, z = call(x), call(poisoned)
+            assert torch.equal(y[keep], z[keep]) and torch.isnan(z[n // 2]).all()
+
+
 SIZES = [(1, 128, 1), (16, 128, 3), (100, 384, 2), (257, 1152, 5), (128, 4224, 16), (48, 256, 17), (272, 384, 33),
          (1000, 640, 64), (100, 128, 65), (256, 384, 100), (300, 1152, 129), (257, 256, 300), (640, 2176, 257),
          (515, 128, 700), (1024, 1024, 1024)]
