@@ -580,7 +580,7 @@ struct TileArgs {
   void* y;        // n x m (GATE: codes of h, n x up)
   float* hs;      // GATE: scales of h
   float* part;    // split K: partial sums, [split][n][m]
-  int m, k, n, yt, up, row_tiles, tok_tiles, groups_per_split;
+  int m, k, n, yt, up, row_tiles, tok_tiles, groups_per_split, first_row_tile;
 };
 
 template <int NT, bool GATE, bool SPLIT, bool EXACT>
@@ -600,7 +600,7 @@ __global__ __launch_bounds__(512, 2) void k_f8_tile(TileArgs p) {
   const int tile = xcd * (tiles >> 3) + (xcd < (tiles & 7) ? xcd : (tiles & 7)) + (b >> 3);
   const int band = tile / (8 * p.row_tiles), in_band = tile - band * 8 * p.row_tiles;
   const int wide = p.tok_tiles - 8 * band < 8 ? p.tok_tiles - 8 * band : 8;
-  const int rt = in_band / wide, tt = 8 * band + in_band - rt * wide;
+  const int in_rt = in_band / wide, tt = 8 * band + in_band - in_rt * wide, rt = p.first_row_tile + in_rt;
   const int row0 = rt * (GATE ? 128 : kTileRows), t0 = tt * 64 * NT;
   const int g0 = SPLIT ? blockIdx.y * p.groups_per_split : 0;
   const int g1 = SPLIT ? (g0 + p.groups_per_split < G ? g0 + p.groups_per_split : G) : G;
@@ -996,23 +996,51 @@ struct Plan {
 // k = 4096, n = 4096: 64 tokens 391 us, 128 288, 256 257; n = 512: 59, 41, 66.
 // Over 32 shapes (32 to 4096 tokens, both kinds of sums) the choice was never
 // more than 12% behind the best of all, and 0.6% on average.
+double tile_us(int64_t row_tiles, int64_t n, int nt, int64_t splits, int64_t groups, bool exact) {
+  constexpr double stage[2][3] = {{0.66, 0.8, 1.5}, {1.15, 1.6, 0}}, ends[2][3] = {{5, 8, 9}, {5, 7, 0}};
+  const int64_t rounds = (row_tiles * ((n + 64 * nt - 1) / (64 * nt)) * splits + cu_count() - 1) / cu_count();
+  return rounds * (groups * stage[exact][nt >> 1] + ends[exact][nt >> 1]);
+}
 Plan tile_plan(int64_t m, int64_t k, int64_t n, bool exact) {
   const int64_t rt = (m + kTileRows - 1) / kTileRows, G = k / kGroup;
-  const int cus = cu_count();
-  constexpr double stage[2][3] = {{0.66, 0.8, 1.5}, {1.15, 1.6, 0}}, ends[2][3] = {{5, 8, 9}, {5, 7, 0}};
   Plan best{1, 1, static_cast<int>(G), 1e30};
-  for (int nt = 1; nt <= (exact ? 2 : 4); nt *= 2) {
-    const int64_t tiles = rt * ((n + 64 * nt - 1) / (64 * nt));
+  for (int nt = 1; nt <= (exact ? 2 : 4); nt *= 2)
     for (int sp = 1; sp <= 8; sp *= 2) {
       if (sp > 1 && G / sp < 4) break;
       const int64_t per = (G + sp - 1) / sp;
-      const int64_t rounds = (tiles * sp + cus - 1) / cus;
-      const double c = rounds * (per * stage[exact][nt >> 1] + ends[exact][nt >> 1]) +
-                       (sp > 1 ? 2.0 + 0.35e-6 * sp * n * m * 4 : 0.0);
+      const double c = tile_us(rt, n, nt, sp, per, exact) + (sp > 1 ? 2.0 + 0.35e-6 * sp * n * m * 4 : 0.0);
       if (c < best.us) best = Plan{nt, sp, static_cast<int>(per), c};
     }
-  }
   best.splits = static_cast<int>((G + best.per - 1) / best.per);
+  return best;
+}
+
+// Where an unsplit product's tiles leave most of their last round of compute
+// units empty: the row tiles that fill whole rounds with `nt`, and a second
+// launch of the rest with narrower tiles (`rest_nt`).  Us, cut and whole: m =
+// 22016, k = 4096, n = 1501 (516 wide tiles) 160 and 183; m = 5003, k = 4096, n =
+// 4096 94 and 109; m = 14336, n = 4096 245 and 259; m = 8192, k = 8192, n = 3000
+// 209 and 210.
+struct Cut {
+  int64_t rows;  // row tiles of the first launch; 0: do not cut
+  int nt, rest_nt;
+};
+Cut tile_cut(const Plan& plan, int64_t m, int64_t k, int64_t n, bool exact) {
+  Cut best{0, 0, 0};
+  if (plan.splits > 1) return best;
+  const int64_t rt = (m + kTileRows - 1) / kTileRows, G = k / kGroup;
+  double us = plan.us;
+  for (int nt = 1; nt <= (exact ? 2 : 4); nt *= 2) {
+    const int64_t wide = (n + 64 * nt - 1) / (64 * nt), rounds = rt * wide / cu_count(), rows = rounds * cu_count() / wide;
+    if (rows <= 0 || rows >= rt) continue;
+    for (int rest = 1; rest <= nt; rest *= 2) {
+      const double c = tile_us(rows, n, nt, 1, G, exact) + tile_us(rt - rows, n, rest, 1, G, exact) + 3.0;
+      if (c < us) {
+        us = c;
+        best = Cut{rows, nt, rest};
+      }
+    }
+  }
   return best;
 }
 
@@ -1050,10 +1078,23 @@ hipError_t tile_product(const uint8_t* w, const float* ws, int64_t m, int64_t k,
   const bool split = plan.splits > 1;
   TileArgs a{w, ws, xq, xs, y, hs, static_cast<float*>(work), static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt,
              static_cast<int>(split ? 0 : up), static_cast<int>((m + kTileRows - 1) / kTileRows),
-             static_cast<int>((n + 64 * plan.nt - 1) / (64 * plan.nt)), plan.per};
+             static_cast<int>((n + 64 * plan.nt - 1) / (64 * plan.nt)), plan.per, 0};
   log_launch("f8 tile%s%s m=%lld k=%lld n=%lld tokens=%d splits=%d", up > 0 ? " gate" : "", exact ? " exact" : "",
              (long long)m, (long long)k, (long long)n, 64 * plan.nt, plan.splits);
-  if (!split) return up > 0 ? tile_nt<true, false>(plan.nt, exact, a, 1, s) : tile_nt<false, false>(plan.nt, exact, a, 1, s);
+  auto whole = [&](int nt, int64_t first, int64_t rows) {
+    a.first_row_tile = static_cast<int>(first);
+    a.row_tiles = static_cast<int>(rows);
+    a.tok_tiles = static_cast<int>((n + 64 * nt - 1) / (64 * nt));
+    return up > 0 ? tile_nt<true, false>(nt, exact, a, 1, s) : tile_nt<false, false>(nt, exact, a, 1, s);
+  };
+  if (!split) {
+    const int64_t rt = a.row_tiles;
+    const Cut cut = tile_cut(plan, m, k, n, exact);
+    if (cut.rows == 0) return whole(plan.nt, 0, rt);
+    log_launch("  cut: %lld row tiles, tokens=%d, then tokens=%d", (long long)cut.rows, 64 * cut.nt, 64 * cut.rest_nt);
+    const hipError_t e = whole(cut.nt, 0, cut.rows);
+    return e == hipSuccess ? whole(cut.rest_nt, cut.rows, rt - cut.rows) : e;
+  }
   const hipError_t e = tile_nt<false, true>(plan.nt, exact, a, plan.splits, s);
   if (e != hipSuccess) return e;
   if (up > 0) {  // (one launch: only a product of few tiles is split)

@@ -300,7 +300,7 @@ def test_ffn_f8(q, hidden, inter, n, dtype):
 
 
 @pytest.mark.parametrize("hidden,inter,n", [(2048, 384, 100), (2048, 14336, 24), (2048, 14336, 64), (1152, 128, 129),
-                                            (4096, 128, 65)])
+                                            (4096, 128, 65), (1024, 2816, 1600)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_ffn_f8_long_sums(q, hidden, inter, n, dtype):
     """Enough columns for the first product's sums to be split; same bound as above."""
@@ -321,7 +321,7 @@ def test_ffn_f8_long_sums(q, hidden, inter, n, dtype):
 
 
 @pytest.mark.parametrize("m,k,n", [(9000, 8192, 17), (9000, 8192, 64), (40, 11008, 7), (5000, 11008, 333), (1003, 4096, 70),
-                                   (2, 4096, 300), (4097, 8192, 31)])
+                                   (2, 4096, 300), (4097, 8192, 31), (5003, 1024, 4096)])
 def test_gemm_f8_large(q, m, k, n):
     """Sizes on the tile kernel's side up to 64 tokens, long sums, many splits."""
     wq, ws, xq, xs, _ = f8_operands(q, m, k, n, 3)
