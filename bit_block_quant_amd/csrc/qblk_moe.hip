@@ -465,6 +465,12 @@ __device__ void build_table(int pairs, int experts, int top_k, Table& t, TableSc
 // weights two halves ahead of the multiply: what bounds the kernel is how many
 // bytes are on their way.  Workgroups are persistent, so the routing is worked
 // out once in each rather than by a launch of its own.
+//
+// Measured: one token, 8 of 64 experts of 2048/1024, Type 0: 11.9 us, 2.5 of them
+// the routing, 1 the table; the 18 MB of weights come in 3.6.  64 tokens, 4 of 32
+// experts of 4096/2048, Type 1: 106 us, 2.9 TB/s: about 75 VALU operations for 1.1
+// KB of weights take as long to issue as those take to come (without the weights'
+// loads 78 us, with nothing but them 75).
 template <int FMT, bool F16>
 __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   // two workgroups to a CU: at most 80 KB each
@@ -717,6 +723,9 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
 // then holds both products on its diagonal (and products of one expert's rows
 // with the other's pairs off it, which nobody reads).  Twice the workgroups
 // for the same weights, where 16 rows each would leave compute units idle.
+//
+// Measured, same layers: one token 9.2 us; 64 tokens 75 us, 2.1 TB/s (45 without
+// the loads of h, of which a half takes 8 and of weights 2).
 template <int FMT, int SPAN>
 __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int max_slices) {
   constexpr int ROWS = 16 / SPAN;
