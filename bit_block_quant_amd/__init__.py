@@ -361,10 +361,19 @@ def _need_f8(codes, scale, name, device=None):
     return dev, rows, k
 
 
-def _workspace(work, nbytes, dev):
+def _empty(shape, dtype, dev, stream):
+    """New memory that belongs to the stream of the call: another stream's might
+    still be in use there, and would be given away as soon as the call returns."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _workspace(work, nbytes, dev, stream):
     """The caller's workspace, checked, or a new one of nbytes."""
     if work is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        return _empty(nbytes, torch.uint8, dev, stream) if nbytes else None
     _need(work, "workspace", (torch.uint8,), min_numel=nbytes, device=dev)
     return work
 
@@ -373,9 +382,9 @@ def _nbytes(work):
     return work.numel() if work is not None else 0
 
 
-def _out(out, shape, dtype, dev):
+def _out(out, shape, dtype, dev, stream):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _empty(shape, dtype, dev, stream)
     _need(out, "out", _FLOAT_IN, numel=shape[0] * shape[1], device=dev)
     return out
 
@@ -385,9 +394,9 @@ def quantize_f8(w, out=None, scale=None, stream=None):
     dev = _need(w, "w", _FLOAT_IN, ndim=2)
     rows, k = w.shape
     if out is None:
-        out = torch.empty((rows, k), dtype=F8, device=w.device)
+        out = _empty((rows, k), F8, dev, stream)
     if scale is None:
-        scale = torch.empty((-(-rows // 128), k // 128), dtype=torch.float32, device=w.device)
+        scale = _empty((-(-rows // 128), k // 128), torch.float32, dev, stream)
     _need_f8(out, scale, "out", dev)
     _need(out, "out", numel=rows * k)
     cur = _need_current(dev)
@@ -403,9 +412,9 @@ def quantize_act_f8(x, out=None, scale=None, stream=None):
     if k % 128:
         raise ValueError(f"x: the number of columns must be a multiple of 128, got {k}")
     if out is None:
-        out = torch.empty((n, k), dtype=F8, device=x.device)
+        out = _empty((n, k), F8, dev, stream)
     if scale is None:
-        scale = torch.empty((n, k // 128), dtype=torch.float32, device=x.device)
+        scale = _empty((n, k // 128), torch.float32, dev, stream)
     _need(out, "out", _F8_IN, numel=n * k, device=dev)
     _need(scale, "scale", (torch.float32,), numel=n * (k // 128), device=dev)
     cur = _need_current(dev)
@@ -420,8 +429,8 @@ def gemm_f8(wq, ws, xq, xs, dtype=torch.float32, out=None, workspace=None, strea
     _need(xq, "xq", _F8_IN, ndim=2, dim1=k, device=dev)
     n = xq.shape[0]
     _need(xs, "xs", (torch.float32,), numel=n * (k // 128), device=dev)
-    out = _out(out, (n, m), dtype, dev)
-    work = _workspace(workspace, _lib.qblk_gemm_f8_workspace(m, k, n), dev)
+    out = _out(out, (n, m), dtype, dev, stream)
+    work = _workspace(workspace, _lib.qblk_gemm_f8_workspace(m, k, n), dev, stream)
     cur = _need_current(dev)
     _check(_lib.qblk_gemm_f8(_ptr(wq), _ptr(ws), m, k, _ptr(xq), _ptr(xs), n, _ptr(out), _dtype(out), _ptr(work),
                              _nbytes(work), _stream(stream, cur)), "qblk_gemm_f8")
@@ -434,8 +443,8 @@ def linear_f8(x, wq, ws, dtype=None, out=None, workspace=None, stream=None):
     dev, m, k = _need_f8(wq, ws, "wq")
     _need(x, "x", _FLOAT_IN, ndim=2, dim1=k, device=dev)
     n = x.shape[0]
-    out = _out(out, (n, m), dtype or x.dtype, dev)
-    work = _workspace(workspace, _lib.qblk_linear_f8_workspace(m, k, n), dev)
+    out = _out(out, (n, m), dtype or x.dtype, dev, stream)
+    work = _workspace(workspace, _lib.qblk_linear_f8_workspace(m, k, n), dev, stream)
     cur = _need_current(dev)
     _check(_lib.qblk_linear_f8(_ptr(wq), _ptr(ws), m, k, _ptr(x), _dtype(x), n, _ptr(out), _dtype(out), _ptr(work),
                                _nbytes(work), _stream(stream, cur)), "qblk_linear_f8")
@@ -453,8 +462,8 @@ def ffn_f8(x, w13, s13, w2, s2, dtype=None, out=None, workspace=None, stream=Non
         raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not make a gated layer")
     _need(x, "x", _FLOAT_IN, ndim=2, dim1=hidden, device=dev)
     n = x.shape[0]
-    out = _out(out, (n, hidden), dtype or x.dtype, dev)
-    work = _workspace(workspace, _lib.qblk_ffn_f8_workspace(hidden, inter, n), dev)
+    out = _out(out, (n, hidden), dtype or x.dtype, dev, stream)
+    work = _workspace(workspace, _lib.qblk_ffn_f8_workspace(hidden, inter, n), dev, stream)
     cur = _need_current(dev)
     _check(_lib.qblk_ffn_f8(_ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), hidden, inter, _ptr(x), _dtype(x), n, _ptr(out),
                             _dtype(out), _ptr(work), _nbytes(work), _stream(stream, cur)), "qblk_ffn_f8")
@@ -497,18 +506,18 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
     else:
         _need_dims(experts=experts)
     if ids is None:
-        ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
+        ids = _empty((n, top_k), torch.int32, dev, stream)
     else:
         _need(ids, "ids", (torch.int32,), numel=n * top_k, device=dev)
     if weights is None:
-        weights = torch.empty((n, top_k), dtype=torch.float32, device=dev)
+        weights = _empty((n, top_k), torch.float32, dev, stream)
     else:
         _need(weights, "weights", (torch.float32,), numel=n * top_k, device=dev)
     _need(gate_up, "gate_up", (torch.uint8,), min_numel=_packed(fmt, experts * 2 * inter, hidden), device=dev)
     _need(down, "down", (torch.uint8,), min_numel=_packed(fmt, experts * hidden, inter), device=dev)
-    out = _out(out, (n, hidden), dtype or x.dtype, dev)
+    out = _out(out, (n, hidden), dtype or x.dtype, dev, stream)
     a = _Moe(fmt, n, hidden, inter, experts, top_k)  # the sizes decide the workspace
-    work = _workspace(workspace, _lib.qblk_moe_workspace(C.byref(a)), dev)
+    work = _workspace(workspace, _lib.qblk_moe_workspace(C.byref(a)), dev, stream)
     a.x, a.xt, a.logits, a.renorm, a.weight_scale = _ptr(x), _DT[x.dtype], _ptr(logits), int(renorm), weight_scale
     a.gate_up, a.down, a.ids, a.weights = _ptr(gate_up), _ptr(down), _ptr(ids), _ptr(weights)
     a.y, a.yt, a.workspace, a.workspace_bytes = _ptr(out), _dtype(out), _ptr(work), _nbytes(work)

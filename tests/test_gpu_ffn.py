@@ -546,6 +546,40 @@ def calls(q):
     return out
 
 
+def test_new_memory_belongs_to_the_calls_stream(q, monkeypatch):
+    """Results and workspaces that a call allocates come from the pool of the stream it
+    runs on: from the current stream's they might be in use there, or be given away
+    while the call still runs."""
+    side = torch.cuda.Stream()
+    made = []
+    empty = torch.empty
+
+    def record(*a, **kw):
+        made.append(empty(*a, **kw))
+        return made[-1]
+
+    wq, ws, xq, xs, x = f8_operands(q, 300, 2048, 70, 1)
+    w13, s13, _, _, _ = f8_operands(q, 512, 2048, 1, 1)
+    w2, s2, _, _, _ = f8_operands(q, 2048, 256, 1, 1)
+    layer = Layer(q, "sb4", 6, 256, 256, 4)
+    h, logits = torch.randn(5, 256, device="cuda").half(), torch.randn(5, 6, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    monkeypatch.setattr(q.torch, "empty", record)
+    q.quantize_f8(x, stream=side)
+    q.quantize_act_f8(x, stream=side)
+    q.gemm_f8(wq, ws, xq, xs, stream=side)
+    q.linear_f8(x, wq, ws, stream=side)
+    q.ffn_f8(x, w13, s13, w2, s2, stream=side)
+    q.moe(layer.fmt, h, logits, layer.gate_up, layer.down, 256, 2, stream=side)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert len(made) >= 12
+    segments = torch.cuda.memory_snapshot()
+    for t in made:
+        (seg,) = [g for g in segments if g["address"] <= t.data_ptr() < g["address"] + g["total_size"]]
+        assert seg["stream"] == side.cuda_stream
+
+
 def test_other_stream_and_graph(q):
     """The same bits on a stream of the caller's, and from a captured graph at every replay."""
     for name, (call, outs) in calls(q).items():
