@@ -397,8 +397,10 @@ def quantize_f8(w, out=None, scale=None, stream=None):
         out = _empty((rows, k), F8, dev, stream)
     if scale is None:
         scale = _empty((-(-rows // 128), k // 128), torch.float32, dev, stream)
-    _need_f8(out, scale, "out", dev)
     _need(out, "out", numel=rows * k)
+    if tuple(out.shape) != (rows, k):  # the scales that are written are those of w's shape
+        raise ValueError(f"out: expected shape {(rows, k)}, got {tuple(out.shape)}")
+    _need_f8(out, scale, "out", dev)
     cur = _need_current(dev)
     _check(_lib.qblk_quantize_f8(_ptr(w), _dtype(w), rows, k, _ptr(out), _ptr(scale), _stream(stream, cur)),
            "qblk_quantize_f8")

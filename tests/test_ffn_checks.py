@@ -113,3 +113,14 @@ def test_moe(q):
     bad(ValueError, "out: expected 768", out=T((N, h + 256), F16))
     bad(ValueError, "workspace: holds", workspace=T((100,), U8))
     bad(ValueError, "other arguments", logits=T((N, e), F32, index=1))
+
+
+def test_quantize_f8_out_of_another_shape(q):
+    """The kernel writes the scales of w's shape, ceil(130/128) * 2 = 4 here; an `out` of as many
+    elements in 260 rows of 128 has only 3, and the fourth would land behind them."""
+    with pytest.raises(ValueError, match="out: expected shape"):
+        q.quantize_f8(T((130, 256), F32), out=T((260, 128), F8), scale=T((3, 1), F32))
+    with pytest.raises(ValueError, match="out: expected shape"):
+        q.quantize_f8(T((128, 256), F32), out=T((256, 128), U8), scale=T((1, 2), F32))
+    with pytest.raises(ValueError):
+        q.quantize_f8(T((130, 256), F32), out=T((130 * 256,), F8), scale=T((2, 2), F32))
