@@ -181,6 +181,14 @@ def _need_dims(**dims):
             raise ValueError(f"{name} must be a non-negative integer, got {v!r}")
 
 
+def _need_int32(**values):
+    """For what the library takes as a 32-bit int: ctypes passes the low 32 bits of a
+    larger number, and the call would be another one than the one checked."""
+    for name, v in values.items():
+        if v >= 1 << 31:
+            raise ValueError(f"{name}: {v} is past the range of a 32-bit integer")
+
+
 def _packed(fmt, rows, k):
     """Bytes of a packed rows x k matrix; 0 for a shape the format cannot
     hold (the library itself rejects those with QBLK_ERR_SHAPE/FORMAT before
@@ -494,6 +502,7 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
     of a router of your own (an id outside [0, experts) counts for nothing).
     Returns (y (n, hidden) of x's type unless said, ids, weights)."""
     _need_dims(inter=inter, top_k=top_k)
+    _need_int32(top_k=top_k)
     dev = _need(x, "x", (torch.float16, torch.bfloat16), ndim=2)
     n, hidden = x.shape
     if logits is not None:
@@ -507,6 +516,7 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
         raise ValueError("without logits, experts, ids and weights are needed")
     else:
         _need_dims(experts=experts)
+    _need_int32(experts=experts)
     if ids is None:
         ids = _empty((n, top_k), torch.int32, dev, stream)
     else:

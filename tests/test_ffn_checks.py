@@ -124,3 +124,15 @@ def test_quantize_f8_out_of_another_shape(q):
         q.quantize_f8(T((128, 256), F32), out=T((256, 128), U8), scale=T((1, 2), F32))
     with pytest.raises(ValueError):
         q.quantize_f8(T((130, 256), F32), out=T((130 * 256,), F8), scale=T((2, 2), F32))
+
+
+def test_moe_counts_past_32_bits(q):
+    """experts and top_k cross the C boundary as 32-bit ints.  2^32 + 4 experts are more rows than
+    any packed matrix holds, for which the byte count is 0, so a tensor of any size passed that
+    check, and the library saw 4 experts."""
+    tiny, big = T((16,), U8), 2 ** 32
+    out = dict(ids=T((N, 2), I32), weights=T((N, 2), F32), out=T((N, 256), F16), workspace=T((1 << 20,), U8))
+    with pytest.raises(ValueError, match="experts: 4294967300 is past"):
+        q.moe(q.SB4, T((N, 256), F16), None, tiny, tiny, 512, 2, experts=big + 4, **out)
+    with pytest.raises(ValueError, match="top_k: 4294967298 is past"):
+        q.moe(q.SB4, T((N, 256), F16), T((N, 4), F32), tiny, tiny, 512, big + 2, **out)
