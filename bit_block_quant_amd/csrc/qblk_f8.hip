@@ -1095,8 +1095,18 @@ hipError_t tile_product(const uint8_t* w, const float* ws, int64_t m, int64_t k,
   auto whole = [&](int nt, int64_t first, int64_t rows) {
     a.first_row_tile = static_cast<int>(first);
     a.row_tiles = static_cast<int>(rows);
-    a.tok_tiles = static_cast<int>((n + 64 * nt - 1) / (64 * nt));
-    return up > 0 ? tile_nt<true, false>(nt, exact, a, 1, s) : tile_nt<false, false>(nt, exact, a, 1, s);
+    // in pieces of the tokens: a launch of 2^23 tiles would pass 32 bits of threads
+    return in_pieces((n + 64 * nt - 1) / (64 * nt), 1, 512 * rows, [&](int64_t tt, int64_t count) {
+      const int64_t t0 = tt * 64 * nt, left = n - t0;
+      TileArgs b = a;
+      b.xq += t0 * k;
+      b.xs += t0 * (k / kGroup);
+      b.y = static_cast<uint8_t*>(y) + t0 * (up > 0 ? up : m * (yt == QBLK_F32 ? 4 : 2));
+      if (up > 0) b.hs += t0 * (up / kGroup);
+      b.n = static_cast<int>(left < count * 64 * nt ? left : count * 64 * nt);
+      b.tok_tiles = static_cast<int>(count);
+      return up > 0 ? tile_nt<true, false>(nt, exact, b, 1, s) : tile_nt<false, false>(nt, exact, b, 1, s);
+    });
   };
   if (!split) {
     const int64_t rt = a.row_tiles;

@@ -128,3 +128,26 @@ def test_quantize_act_i8_rows_in_pieces(q):
     xq_ref, s_ref = O.quantize_act_i8(host(x[ri]))
     assert np.array_equal(host(xq[ri]), xq_ref)
     assert np.array_equal(host(s[ri]).view(np.uint32), s_ref.view(np.uint32))
+
+
+def test_gemm_f8_tokens_in_pieces(q):
+    """2^30 tokens of 128 columns: one launch of 128-token tiles would have 2^32 threads.  The codes
+    repeat every 2^20 tokens, and so must the results (one group of columns: no sum depends on the tiling)."""
+    unit, k, n = 1 << 20, 128, (1 << 30) + 77
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < n * (k + 8) + (4 << 30):
+        pytest.skip("not enough GPU memory for 2^30 tokens")
+    g = torch.Generator(device="cuda").manual_seed(341)
+    xq1, xs1 = q.quantize_act_f8(torch.randn(unit, k, device="cuda", generator=g))
+    wq, ws = q.quantize_f8(torch.randn(1, k, device="cuda", generator=g))
+    want = q.gemm_f8(wq, ws, xq1, xs1)
+    w64 = wq.float().double() * ws.double()
+    x64 = xq1[:5000].float().double() * xs1[:5000].double()
+    check(host(want)[:5000], host(x64 @ w64.T), host(x64.abs() @ w64.abs().T), "gemm_f8 of the repeated tokens")
+    xq, xs = torch.empty(n, k, dtype=torch.uint8, device="cuda"), torch.empty(n, 1, device="cuda")
+    for t, one in ((xq, xq1.view(torch.uint8)), (xs, xs1)):
+        t[:1 << 30].view(-1, unit, t.shape[1]).copy_(one)
+        t[1 << 30:] = one[:77]
+    y = q.gemm_f8(wq, ws, xq, xs)
+    assert torch.equal(y[:1 << 30].view(-1, unit), want.view(1, unit).expand(1 << 10, unit))
+    assert torch.equal(y[1 << 30:], want[:77])
