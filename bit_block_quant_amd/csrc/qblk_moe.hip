@@ -712,6 +712,13 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   } while (!done);
 }
 
+// The same value, unknown to the compiler: what is derived from it is formed where
+// it is used, by an instruction or two, and not kept in registers across the loop.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // -------------------------------------------------------------------- down
 // A workgroup owns rows of y for every token.  Its waves take the pairs of
 // (expert, slice of the columns); each writes its fp32 sums per pair to a
@@ -735,7 +742,7 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
   __shared__ float share[kMoeMaxPairs];  // a pair's weight
   __shared__ bool valid[kMoeMaxPairs];   // and whether it has an expert
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4, wrow = lane >> 2, wu = lane & 3;
+  const int r = lane & 15, q = lane >> 4, wu = lane & 3;
   Stage& stage = stages[wave];
   const int pairs = a.n * a.top_k;
   {
@@ -775,7 +782,7 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
     return s < active ? s : active - 1;
   };
   auto row = [&](int group) {
-    const int e = table.expert[slot_of(group, wrow >> 3)];
+    const int wrow = fresh(lane) >> 2, e = table.expert[slot_of(group, wrow >> 3)];
     return a.down + (static_cast<int64_t>(e) * a.hidden + row0 + (wrow & (ROWS - 1))) * a.down_row_bytes;
   };
   // h of an expert's pairs is stored as operands: per unit of 32 columns the hi
@@ -873,13 +880,14 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_moe_down(MoeArgs a, int m
       if (p.hf < halves) return;
       // lane (column r, quarter q): pairs 4q .. 4q+3 of the tile; of two experts
       // the first has the tile's first 8 pairs and columns
-      if (!done && (SPAN == 1 || ((q >> 1) == (r >> 3) && 2 * p.group + (r >> 3) < active))) {
-        const int slot = slot_of(p.group, r >> 3);
+      const int l = fresh(lane), col = l & 15, quarter = l >> 4;
+      if (!done && (SPAN == 1 || ((quarter >> 1) == (col >> 3) && 2 * p.group + (col >> 3) < active))) {
+        const int slot = slot_of(p.group, col >> 3);
         const int first = table.off[slot], count = table.off[slot + 1] - first;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const int at = p.c0 + ((4 * q + i) & (ROWS - 1));
-          if (at < count) slots[(p.slice * pairs + table.pair[first + at]) * ROWS + (r & (ROWS - 1))] = acc[i];
+          const int at = p.c0 + ((4 * quarter + i) & (ROWS - 1));
+          if (at < count) slots[(p.slice * pairs + table.pair[first + at]) * ROWS + (col & (ROWS - 1))] = acc[i];
         }
       }
       acc = float4_t{0, 0, 0, 0};
@@ -945,9 +953,11 @@ hipError_t run(const MoeArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // 8 rows of two experts a workgroup where 16 rows leave compute units idle
-  // (hidden 2048, us, whole call: 64 experts, 8 of them a token: 16 tokens 86
-  // against 112 with 16 rows, 2 tokens 27.7 and 30.9, one 20.6 and 23.1; 16
-  // experts, 2 of them, one token: 16.8 and 16.7).  Where they do not, half of
+  // (hidden 2048, inter 1024, us, whole call in a graph, 8 rows and 16; 64 experts,
+  // 8 of them a token: one token Type 0 20.8 and 23.2, Type 1 21.2 and 23.0, Q4_K
+  // 20.9 and 22.6, Q4_0 22.8 and 25.3; 16 tokens 78 and 103, 78 and 101, 77 and 98,
+  // 87 and 115; 64 tokens 128 and 135, 129 and 136, 124 and 131, 135 and 142; 16
+  // experts, 2 of them, one token, Type 0: 13.5 and 15.6).  Where they do not, half of
   // the tile's products are for nothing (hidden 4096: 64 tokens 253 and 184, one
   // token 31.5 and 26.4).
   return a.hidden / 16 < cu_count() ? down<FMT, 2>(a, s) : down<FMT, 1>(a, s);
