@@ -499,7 +499,8 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
     of hidden weights (per expert the gate rows, then the up rows) and down:
     experts x hidden rows of inter weights, packed as quantize() does.  With
     logits=None, give experts, ids (n, top_k) int32 and weights (n, top_k) fp32
-    of a router of your own (an id outside [0, experts) counts for nothing).
+    of a router of your own (an id outside [0, experts) counts for nothing); the
+    weights are taken as they are: renorm is not looked at, a weight_scale refused.
     Returns (y (n, hidden) of x's type unless said, ids, weights)."""
     _need_dims(inter=inter, top_k=top_k)
     _need_int32(top_k=top_k)
@@ -514,6 +515,8 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
         experts = logits.shape[1]
     elif experts is None or ids is None or weights is None:
         raise ValueError("without logits, experts, ids and weights are needed")
+    elif weight_scale != 1:
+        raise ValueError(f"weight_scale {weight_scale!r}: weights that are given are not scaled")
     else:
         _need_dims(experts=experts)
     _need_int32(experts=experts)

@@ -354,7 +354,8 @@ qblk_status_t qblk_ffn_f8(const uint8_t* w13, const float* s13,
  * expert out; where fewer than top_k are left the remaining ids are -1 with
  * weight 0, and a token with none gets Y = 0.  (+infinity counts as the
  * largest finite value.)  With logits = NULL, ids and weights are inputs from
- * a router of the caller's; ids outside [0, experts) contribute nothing.
+ * a router of the caller's, taken as they are (renorm and weight_scale are not
+ * looked at); ids outside [0, experts) contribute nothing.
  *
  * Products are formed from the exact codes and 16-bit activations, sums are
  * fp32, the intermediate keeps 16 mantissa bits; the order of the sums is fixed,

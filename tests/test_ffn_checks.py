@@ -136,3 +136,12 @@ def test_moe_counts_past_32_bits(q):
         q.moe(q.SB4, T((N, 256), F16), None, tiny, tiny, 512, 2, experts=big + 4, **out)
     with pytest.raises(ValueError, match="top_k: 4294967298 is past"):
         q.moe(q.SB4, T((N, 256), F16), T((N, 4), F32), tiny, tiny, 512, big + 2, **out)
+
+
+def test_moe_scale_of_given_weights(q):
+    """Weights of the caller's router are taken as they are: a scale for them is not dropped silently."""
+    up, down = T((q.packed_bytes(q.SB4, 4 * 1024, 256),), U8), T((q.packed_bytes(q.SB4, 4 * 256, 512),), U8)
+    out = dict(ids=T((N, 2), I32), weights=T((N, 2), F32), out=T((N, 256), F16), workspace=T((1 << 20,), U8))
+    for scale in (2.0, 0.0, float("nan")):
+        with pytest.raises(ValueError, match="weight_scale"):
+            q.moe(q.SB4, T((N, 256), F16), None, up, down, 512, 2, experts=4, weight_scale=scale, **out)
