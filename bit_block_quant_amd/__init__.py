@@ -501,6 +501,7 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
     logits=None, give experts, ids (n, top_k) int32 and weights (n, top_k) fp32
     of a router of your own (an id outside [0, experts) counts for nothing); the
     weights are taken as they are: renorm is not looked at, a weight_scale refused.
+    Where hidden or inter is 0 nothing is routed: ids -1, weights 0.
     Returns (y (n, hidden) of x's type unless said, ids, weights)."""
     _need_dims(inter=inter, top_k=top_k)
     _need_int32(top_k=top_k)
@@ -538,4 +539,8 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
     a.y, a.yt, a.workspace, a.workspace_bytes = _ptr(out), _dtype(out), _ptr(work), _nbytes(work)
     cur = _need_current(dev)
     _check(_lib.qblk_moe(C.byref(a), _stream(stream, cur)), "qblk_moe")
+    if logits is not None and not (hidden and inter):  # the call leaves them as they are
+        with torch.cuda.stream(stream):  # (None: the current one)
+            ids.fill_(-1)
+            weights.zero_()
     return out, ids, weights

@@ -686,3 +686,25 @@ def test_empty_calls(q):
     layer = Layer(q, "sb4", 3, 256, 256, 1)
     y, ids, w = q.moe(layer.fmt, f(0, 256).half(), f(0, 3), layer.gate_up, layer.down, 256, 2)
     assert y.shape == (0, 256) and ids.shape == (0, 2) and w.shape == (0, 2)
+
+
+@pytest.mark.parametrize("hidden,inter", [(256, 0), (0, 256)])
+@pytest.mark.parametrize("other", [False, True])
+def test_moe_without_columns(q, hidden, inter, other):
+    """Nothing is routed: the ids and weights that come back say so, and are not what the memory held."""
+    stream = torch.cuda.Stream() if other else None
+    x, logits = torch.ones(3, hidden, device="cuda").half(), torch.randn(3, 4, device="cuda")
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    ids, w = torch.full((3, 2), 7, dtype=torch.int32, device="cuda"), torch.full((3, 2), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    for given in (dict(ids=ids, weights=w), {}):
+        for _ in range(3):  # new memory that held something
+            junk = torch.full((3, 2), 5, dtype=torch.int32, device="cuda"), torch.full((3, 2), 5.0, device="cuda")
+            del junk
+        y, i, v = q.moe(q.SB4, x, logits, none, none, inter, 2, stream=stream, **given)
+        torch.cuda.synchronize()
+        assert y.shape == (3, hidden) and torch.all(y == 0) and torch.all(i == -1) and torch.all(v == 0)
+    ids.fill_(1)
+    w.fill_(2.0)
+    _, i, v = q.moe(q.SB4, x, None, none, none, inter, 2, experts=4, ids=ids, weights=w)
+    assert torch.all(i == 1) and torch.all(v == 2.0)  # a router of the caller's keeps its own
