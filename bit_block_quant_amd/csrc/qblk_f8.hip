@@ -218,8 +218,8 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int yt) {
     static_cast<uint16_t*>(y)[at] = yt == QBLK_F16 ? f32_to_f16_bits(v) : f32_to_bf16_bits(v);
 }
 
-// Up to 16 T tokens, bound by the weight bytes.  A workgroup owns NR tiles of
-// 16 rows for all its tokens and splits the columns over its waves (wave w
+// n <= 16 T tokens, bound by the weight bytes.  A workgroup owns NR tiles of
+// 16 rows for all tokens and splits the columns over its waves (wave w
 // takes groups w, w + WAVES, ...); the waves' fp32 partial sums meet in LDS in
 // a fixed order.  The codes are widened to bf16 and multiplied on the bf16
 // matrix cores, whose fp32 sums of such products are exact to fp32 rounding
@@ -270,10 +270,8 @@ __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restri
   using Set = FewSet<T, NR, CODES ? T : 1>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = k / kGroup;
-  const int t0 = blockIdx.y * 16 * T;
   const int row0 = blockIdx.x * (GATE ? 16 : 16 * NR);
   const int r = lane & 15, q = lane >> 4;
-  n -= t0;
   uint8_t* const region = lds + wave * kRegion;
 
   // Rows and tokens past the last repeat it; their results are not stored.
@@ -297,8 +295,6 @@ __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restri
   }
   const uint8_t* xb = static_cast<const uint8_t*>(xv);
   if constexpr (CODES) {
-    xb += static_cast<int64_t>(t0) * k;
-    xs += static_cast<int64_t>(t0) * xs_tok;
 #pragma unroll
     for (int t = 0; t < T; t++) {
 #pragma unroll
@@ -352,12 +348,11 @@ __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restri
   const float* sl = nullptr;
   const int xstride = k + 16;
   if constexpr (!CODES) {
-    const int nt = n < 16 * T ? n : 16 * T;
     float* const scales = reinterpret_cast<float*>(lds + WAVES * kRegion);
-    uint8_t* const codes = lds + WAVES * kRegion + (nt * G * 4 + 15) / 16 * 16;
+    uint8_t* const codes = lds + WAVES * kRegion + (n * G * 4 + 15) / 16 * 16;
     xq = codes;
     sl = scales;
-    const int units = nt * G;
+    const int units = n * G;
     for (int u0 = 0; u0 < units; u0 += WAVES * 8) {  // two groups a row of 16 lanes
       float v[2][8];
       int unit[2];
@@ -365,7 +360,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restri
       for (int i = 0; i < 2; i++) {
         unit[i] = u0 + i * WAVES * 4 + (threadIdx.x >> 4);
         const int uu = unit[i] < units ? unit[i] : units - 1;
-        load8<XSRC>(xv, (static_cast<int64_t>(t0) * G + uu) * kGroup + 8 * r, v[i]);
+        load8<XSRC>(xv, uu * kGroup + 8 * r, v[i]);
       }
       __builtin_amdgcn_sched_barrier(0);
       if (u0 == 0) {
@@ -471,9 +466,9 @@ __global__ __launch_bounds__(WAVES* kWave) void k_f8_few(const uint8_t* __restri
     if (tok >= n) continue;
     const int row = row0 + 16 * a + rr;
     if constexpr (GATE)
-      static_cast<float*>(y)[static_cast<int64_t>(t0 + tok) * up_row + row] = silu_mul(sum, up);
+      static_cast<float*>(y)[tok * up_row + row] = silu_mul(sum, up);
     else if (row < m)
-      store_y(y, static_cast<int64_t>(t0 + tok) * m + row, sum, yt);
+      store_y(y, static_cast<int64_t>(tok) * m + row, sum, yt);
   }
 }
 
@@ -947,10 +942,10 @@ hipError_t few(const uint8_t* w, const float* ws, int64_t m, int64_t k, const Fe
                int64_t up_row, hipStream_t s) {
   const int per = GATE ? 16 : 16 * NR;
   const int64_t rows = GATE ? up_row : m;
-  const dim3 grid(static_cast<unsigned>((rows + per - 1) / per), static_cast<unsigned>((n + 16 * T - 1) / (16 * T)));
-  const size_t nt = static_cast<size_t>(n < 16 * T ? n : 16 * T), G = static_cast<size_t>(k / kGroup);
+  const dim3 grid(static_cast<unsigned>((rows + per - 1) / per));
+  const size_t G = static_cast<size_t>(k / kGroup);
   const size_t lds = static_cast<size_t>(WAVES) * few_region(T, NR) +
-                     (XSRC == kCodes ? 0 : (nt * G * 4 + 15) / 16 * 16 + nt * (static_cast<size_t>(k) + 16));
+                     (XSRC == kCodes ? 0 : (n * G * 4 + 15) / 16 * 16 + n * (static_cast<size_t>(k) + 16));
   static const hipError_t allowed =
       hipFuncSetAttribute(reinterpret_cast<const void*>(k_f8_few<T, NR, WAVES, GATE, XSRC>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
