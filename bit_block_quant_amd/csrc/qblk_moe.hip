@@ -525,7 +525,7 @@ __global__ __launch_bounds__(kUpWaves* kWave, 4) void k_moe_up(MoeArgs a) {
   }
 
   const int tiles = a.inter / 16, units = a.hidden / 32, halves = (units + 3) / 4;
-  // tiles of all experts in a row; at most 2^31 (512 experts, 2^26 rows)
+  // tiles of all experts in a row; at most 2^24 (512 experts, 2^19 rows)
   const uint32_t tasks = static_cast<uint32_t>(table.active) * static_cast<uint32_t>(tiles);
   if (blockIdx.x >= tasks) return;
   const int slot_step = gridDim.x / tiles, tile_step = gridDim.x % tiles;
@@ -958,8 +958,9 @@ hipError_t run(const MoeArgs& a, hipStream_t s) {
   // 20.9 and 22.6, Q4_0 22.8 and 25.3; 16 tokens 78 and 103, 78 and 101, 77 and 98,
   // 87 and 115; 64 tokens 128 and 135, 129 and 136, 124 and 131, 135 and 142; 16
   // experts, 2 of them, one token, Type 0: 13.5 and 15.6).  Where they do not, half of
-  // the tile's products are for nothing (hidden 4096: 64 tokens 253 and 184, one
-  // token 31.5 and 26.4).
+  // the tile's products are for nothing (hidden 4096, inter 2048, 4 of 32 experts:
+  // one token Type 0 31.7 and 26.6, Type 1 31.2 and 25.9; 16 tokens 144 and 136, 145
+  // and 135; 64 tokens 238 and 180, 242 and 183).
   return a.hidden / 16 < cu_count() ? down<FMT, 2>(a, s) : down<FMT, 1>(a, s);
 }
 
