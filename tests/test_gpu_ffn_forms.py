@@ -278,3 +278,36 @@ def test_moe_16_rows_bounds_and_graph(q, layers, fmt, n):  # noqa: F811
         assert all(torch.equal(p.t, w) for p, w in zip((py, pi, pw), want))
         torch.randn(1000, device="cuda").sum().item()
     assert all(p.intact() for p in (px, pl, pg, pd, py, pi, pw, work))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hidden", [512, HIDDEN])
+def test_moe_small_activations(q, fmt, hidden):  # noqa: F811
+    """x among the subnormal numbers of f16: its operands keep them."""
+    layer = Layer(q, fmt, 3, hidden, 256, 15)
+    rng = np.random.default_rng(16)
+    x = torch.from_numpy((rng.standard_normal((5, hidden)) * 1e-5).astype(np.float32)).half().cuda()
+    logits = rng.standard_normal((5, 3)).astype(np.float32)
+    y, ids, weights = q.moe(layer.fmt, x, torch.from_numpy(logits).cuda(), layer.gate_up, layer.down, 256, 2, dtype=torch.float32)
+    assert torch.any(y != 0)
+    check_moe(layer, x, y, route_ref(logits, 2, True)[0], f64(weights))
+
+
+def test_moe_largest_intermediate(q):  # noqa: F811
+    """1023 pairs of the largest inter, 2^19: their intermediate takes 2 GB, addressed by 32-bit offsets."""
+    n, hidden, inter = 1023, 32, 1 << 19
+    gen = torch.Generator("cuda").manual_seed(17)
+    up, down = [torch.randn(r, c, device="cuda", generator=gen) * s for r, c, s in ((2 * inter, hidden, 0.2), (hidden, inter, 0.01))]
+    gate_up, down = q.quantize(up, q.Q4_0), q.quantize(down, q.Q4_0)
+    x = torch.randn(n, hidden, device="cuda", generator=gen).half()
+    y, _, _ = q.moe(q.Q4_0, x, torch.zeros(n, 1, device="cuda"), gate_up, down, inter, 1, dtype=torch.float32)
+    up, down = q.dequant(gate_up, q.Q4_0, 2 * inter, hidden).double(), q.dequant(down, q.Q4_0, hidden, inter).double()
+    for t in (0, 1, 500, 1007, 1008, 1022):  # the same formula and bound as above, a token at a time
+        v = x[t].double()
+        gu, mag = up @ v, up.abs() @ v.abs()
+        g, u, dg, du = gu[:inter], gu[inter:], TOL * mag[:inter], TOL * mag[inter:]
+        s = g / (1 + torch.exp(-g))
+        h = s * u
+        dh = 1.1 * dg * (u.abs() + du) + s.abs() * du + 2.0 ** -16 * h.abs()
+        tol = down.abs() @ (dh + TOL * h.abs())
+        assert torch.all((y[t].double() - down @ h).abs() <= tol + 2.0 ** -23 * (down @ h).abs()), t

@@ -151,3 +151,26 @@ def test_gemm_f8_tokens_in_pieces(q):
     y = q.gemm_f8(wq, ws, xq, xs)
     assert torch.equal(y[:1 << 30].view(-1, unit), want.view(1, unit).expand(1 << 10, unit))
     assert torch.equal(y[1 << 30:], want[:77])
+
+
+def test_moe_experts_past_4_gb(q):
+    """512 experts of 9 and 5 MB: the last ones lie past 2^32 bytes.  A token that takes them has the
+    bits of a call that is given those experts alone."""
+    experts, hidden, inter, n = 512, 4096, 2048, 3
+    g = torch.Generator(device="cuda").manual_seed(351)
+
+    def packed(rows, k):
+        b = torch.randint(0, 256, (rows * k // 32, 18), dtype=torch.uint8, device="cuda", generator=g)
+        b[:, 0], b[:, 1] = 0, 0x18 + (b[:, 1] & 3)  # scales 2^-9 .. 2^-8.2
+        return b.view(-1)
+    gate_up, down = packed(experts * 2 * inter, hidden), packed(experts * hidden, inter)
+    assert gate_up.numel() > 1 << 32
+    x = torch.randn(n, hidden, device="cuda", generator=g).half()
+    ids = torch.tensor([[511, 500], [256, 511], [3, 509]], dtype=torch.int32, device="cuda")
+    w = torch.rand(n, 2, device="cuda", generator=g)
+    y, _, _ = q.moe(q.Q4_0, x, None, gate_up, down, inter, 2, experts=experts, ids=ids, weights=w, dtype=torch.float32)
+    few = [3, 256, 500, 509, 511]
+    pick = lambda b: b.view(experts, -1)[few].reshape(-1).contiguous()  # noqa: E731
+    own = torch.tensor([[few.index(i) for i in row] for row in ids.tolist()], dtype=torch.int32, device="cuda")
+    z, _, _ = q.moe(q.Q4_0, x, None, pick(gate_up), pick(down), inter, 2, experts=len(few), ids=own, weights=w, dtype=torch.float32)
+    assert torch.isfinite(y).all() and torch.any(y != 0) and torch.equal(y, z)
