@@ -18,7 +18,12 @@ fallback.  Build with ``python bit_block_quant_amd/build.py`` (or ``__graft_entr
     Y      = qblk.linear_f8(X, wq, ws)            # X: (n, k) f32/f16/bf16 -> (n, m) of X's type
     Y      = qblk.ffn_f8(X, w13, s13, w2, s2)     # gated feed-forward layer
     Y, ids, weights = qblk.moe(qblk.SB4, X, logits, gate_up, down, inter, top_k)
+    wq, ws = qblk.quantize_mxfp4(w)               # 4-bit floats, a power of two per 32 columns
+    Y      = qblk.linear_mxfp4(X, wq, ws)         # X quantized to MXFP8 (or MXFP4) on the way
+    r      = qblk.rmsnorm(X, weight, residual)    # t = X + residual, its norm in codes with scales
+    Y      = qblk.gemm_mxfp4(wq, ws, r.codes, r.scale)
 """
+import collections
 import ctypes as C
 import os
 
@@ -30,6 +35,10 @@ LIB_PATH = os.path.join(_HERE, "libqblk.so")
 Q4_0, SB4, SB4_AFFINE, Q4_K, W4G128 = 0, 1, 2, 3, 4
 F32, F16, BF16 = 0, 1, 2
 FORMATS = {"q4_0": Q4_0, "sb4": SB4, "sb4_affine": SB4_AFFINE, "q4_k": Q4_K, "w4g128": W4G128}
+# what activations are quantized to: e4m3 with an fp32 scale per 128 columns, int8 with one per
+# token, and the two microscaling formats
+ACT_F8, ACT_I8, ACT_MXFP8, ACT_MXFP4 = 0, 1, 2, 3
+ACTS = {"f8": ACT_F8, "i8": ACT_I8, "mxfp8": ACT_MXFP8, "mxfp4": ACT_MXFP4}
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 STATUS = {
@@ -46,6 +55,8 @@ EXPORTS = (
     "qblk_set_deterministic", "qblk_deterministic", "qblk_status_string", "qblk_version",
     "qblk_quantize_f8", "qblk_quantize_act_f8", "qblk_gemm_f8", "qblk_gemm_f8_workspace", "qblk_linear_f8",
     "qblk_linear_f8_workspace", "qblk_ffn_f8", "qblk_ffn_f8_workspace", "qblk_moe", "qblk_moe_workspace",
+    "qblk_quantize_mx", "qblk_dequant_mx", "qblk_gemm_mxfp4", "qblk_gemm_mxfp4_workspace", "qblk_linear_mxfp4",
+    "qblk_linear_mxfp4_workspace", "qblk_rmsnorm",
 )
 
 
@@ -91,6 +102,15 @@ def _load():
         getattr(L, f).restype = i32
     for f in ("qblk_gemm_f8_workspace", "qblk_linear_f8_workspace", "qblk_ffn_f8_workspace", "qblk_moe_workspace"):
         getattr(L, f).restype = sz
+    L.qblk_quantize_mx.argtypes = [p, i32, i64, i64, i32, p, p, p]
+    L.qblk_dequant_mx.argtypes = [p, p, i32, i64, i64, p, i32, p]
+    L.qblk_gemm_mxfp4.argtypes = [p, p, i64, i64, p, p, i32, i64, p, i32, p, sz, p]
+    L.qblk_linear_mxfp4.argtypes = [p, p, i64, i64, p, i32, i32, i64, p, i32, p, sz, p]
+    L.qblk_gemm_mxfp4_workspace.argtypes = L.qblk_linear_mxfp4_workspace.argtypes = [i64, i64, i64, i32]
+    L.qblk_gemm_mxfp4_workspace.restype = L.qblk_linear_mxfp4_workspace.restype = sz
+    L.qblk_rmsnorm.argtypes = [p, p]
+    for f in ("qblk_quantize_mx", "qblk_dequant_mx", "qblk_gemm_mxfp4", "qblk_linear_mxfp4", "qblk_rmsnorm"):
+        getattr(L, f).restype = i32
     L.qblk_status_string.argtypes, L.qblk_status_string.restype = [i32], C.c_char_p
     L.qblk_version.argtypes, L.qblk_version.restype = [], C.c_char_p
     L.qblk_set_deterministic.argtypes, L.qblk_set_deterministic.restype = [i32], i32
@@ -544,3 +564,186 @@ def moe(fmt, x, logits, gate_up, down, inter, top_k, renorm=True, weight_scale=1
             ids.fill_(-1)
             weights.zero_()
     return out, ids, weights
+
+
+# ------------------------------------------------- microscaling (MX) formats
+E8M0 = torch.float8_e8m0fnu
+_E8M0_IN = (E8M0, torch.uint8)
+
+
+def _mx_act(act, name="act"):
+    if act not in (ACT_MXFP8, ACT_MXFP4):
+        raise ValueError(f"{name}: expected ACT_MXFP8 or ACT_MXFP4, got {act!r}")
+    return act
+
+
+def _mx_cols(k, name):
+    if k % 32:
+        raise ValueError(f"{name}: the number of columns must be a multiple of 32, got {k}")
+
+
+def _need_mxfp4(codes, scale, name, device=None):
+    """A matrix of MXFP4 codes (rows, k/2) with its scales; returns (device, rows, k)."""
+    dev = _need(codes, name, (torch.uint8,), ndim=2, device=device)
+    rows, k = codes.shape[0], 2 * codes.shape[1]
+    _mx_cols(k, name)
+    _need(scale, f"{name} scale", _E8M0_IN, numel=rows * (k // 32), device=dev)
+    return dev, rows, k
+
+
+def _need_mx(codes, scale, name, device=None):
+    """MX codes of either kind with their scales; returns (device, rows, k, kind).  Bytes
+    (uint8) are MXFP4 pairs, float8_e4m3fn MXFP8."""
+    if getattr(codes, "dtype", None) == torch.uint8:
+        return _need_mxfp4(codes, scale, name, device) + (ACT_MXFP4,)
+    dev = _need(codes, name, (torch.uint8, F8), ndim=2, device=device)
+    rows, k = codes.shape
+    _mx_cols(k, name)
+    _need(scale, f"{name} scale", _E8M0_IN, numel=rows * (k // 32), device=dev)
+    return dev, rows, k, ACT_MXFP8
+
+
+def _codes_like(act, n, k):
+    """Shapes and types of the codes and scales of n rows of k values."""
+    if act == ACT_MXFP4:
+        return (n, k // 2), torch.uint8, (n, k // 32), E8M0
+    if act == ACT_MXFP8:
+        return (n, k), F8, (n, k // 32), E8M0
+    if act == ACT_F8:
+        return (n, k), F8, (n, k // 128), torch.float32
+    return (n, k), torch.int8, (n,), torch.float32
+
+
+def _act_out(act, n, k, out, scale, dev, stream):
+    """The caller's codes and scales, checked, or new ones."""
+    shape, dtype, sshape, sdtype = _codes_like(act, n, k)
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+    else:
+        _need(out, "out", _F8_IN if dtype == F8 else (dtype,), device=dev)
+        if tuple(out.shape) != shape:
+            raise ValueError(f"out: expected shape {shape}, got {tuple(out.shape)}")
+    if scale is None:
+        scale = _empty(sshape, sdtype, dev, stream)
+    else:
+        _need(scale, "scale", _E8M0_IN if sdtype == E8M0 else (sdtype,), numel=sshape[0] * (sshape[1] if len(sshape) > 1 else 1),
+              device=dev)
+    return out, scale
+
+
+def _quantize_mx(v, act, out, scale, stream):
+    dev = _need(v, "v", _FLOAT_IN, ndim=2)
+    rows, k = v.shape
+    _mx_cols(k, "v")
+    out, scale = _act_out(act, rows, k, out, scale, dev, stream)
+    cur = _need_current(dev)
+    _check(_lib.qblk_quantize_mx(_ptr(v), _dtype(v), rows, k, act, _ptr(out), _ptr(scale), _stream(stream, cur)),
+           "qblk_quantize_mx")
+    return out, scale
+
+
+def quantize_mxfp4(v, out=None, scale=None, stream=None):
+    """(rows, k) f32/f16/bf16 -> (MXFP4 codes (rows, k/2) uint8, e8m0 scales (rows, k/32)): weights, or
+    activations in 4 bits."""
+    return _quantize_mx(v, ACT_MXFP4, out, scale, stream)
+
+
+def quantize_mxfp8(v, out=None, scale=None, stream=None):
+    """(rows, k) f32/f16/bf16 -> (MXFP8 codes (rows, k) e4m3, e8m0 scales (rows, k/32))."""
+    return _quantize_mx(v, ACT_MXFP8, out, scale, stream)
+
+
+def dequant_mx(codes, scale, dtype=torch.float32, out=None, stream=None):
+    """The values (rows, k) of MXFP4 (uint8) or MXFP8 (e4m3) codes."""
+    dev, rows, k, act = _need_mx(codes, scale, "codes")
+    out = _out(out, (rows, k), dtype, dev, stream)
+    cur = _need_current(dev)
+    _check(_lib.qblk_dequant_mx(_ptr(codes), _ptr(scale), act, rows, k, _ptr(out), _dtype(out), _stream(stream, cur)),
+           "qblk_dequant_mx")
+    return out
+
+
+def gemm_mxfp4(wq, ws, xq, xs, dtype=torch.float32, out=None, workspace=None, stream=None):
+    """Y (n, m) = X W^T from codes and scales: W as quantize_mxfp4 gives it, X as quantize_mxfp4 (uint8
+    codes) or quantize_mxfp8 (e4m3) does."""
+    dev, m, k = _need_mxfp4(wq, ws, "wq")
+    _, n, xk, act = _need_mx(xq, xs, "xq", dev)
+    if xk != k:
+        raise ValueError(f"xq: {xk} columns, wq has {k}")
+    out = _out(out, (n, m), dtype, dev, stream)
+    work = _workspace(workspace, _lib.qblk_gemm_mxfp4_workspace(m, k, n, act), dev, stream)
+    cur = _need_current(dev)
+    _check(_lib.qblk_gemm_mxfp4(_ptr(wq), _ptr(ws), m, k, _ptr(xq), _ptr(xs), act, n, _ptr(out), _dtype(out), _ptr(work),
+                                _nbytes(work), _stream(stream, cur)), "qblk_gemm_mxfp4")
+    return out
+
+
+def linear_mxfp4(x, wq, ws, act=ACT_MXFP8, dtype=None, out=None, workspace=None, stream=None):
+    """Y (n, m) = X W^T with X (n, k) f32/f16/bf16, quantized to `act` on the way, and W as
+    quantize_mxfp4 gives it; Y of X's type unless said."""
+    _mx_act(act)
+    dev, m, k = _need_mxfp4(wq, ws, "wq")
+    _need(x, "x", _FLOAT_IN, ndim=2, dim1=k, device=dev)
+    n = x.shape[0]
+    out = _out(out, (n, m), dtype or x.dtype, dev, stream)
+    work = _workspace(workspace, _lib.qblk_linear_mxfp4_workspace(m, k, n, act), dev, stream)
+    cur = _need_current(dev)
+    _check(_lib.qblk_linear_mxfp4(_ptr(wq), _ptr(ws), m, k, _ptr(x), _dtype(x), act, n, _ptr(out), _dtype(out), _ptr(work),
+                                  _nbytes(work), _stream(stream, cur)), "qblk_linear_mxfp4")
+    return out
+
+
+# ------------------------------------------------------------------- norm
+class _RmsNorm(C.Structure):
+    """qblk_rmsnorm_t"""
+    _fields_ = [("n", C.c_int64), ("hidden", C.c_int64), ("x", C.c_void_p), ("residual", C.c_void_p), ("xt", C.c_int),
+                ("weight", C.c_void_p), ("wt", C.c_int), ("eps", C.c_float), ("act", C.c_int), ("codes", C.c_void_p),
+                ("scale", C.c_void_p), ("total", C.c_void_p), ("y", C.c_void_p)]
+
+
+Norm = collections.namedtuple("Norm", ["codes", "scale", "total", "y"])
+
+
+def rmsnorm(x, weight, residual=None, eps=1e-6, quant=ACT_F8, out=None, scale=None, total=None, y=None, stream=None):
+    """Root-mean-square norm with the residual's addition and the codes that a product reads.
+
+    t = x + residual (of x's type), y = t / sqrt(mean(t^2) + eps) * weight over the rows of x
+    (n, hidden) f32/f16/bf16.  quant: ACT_F8 (for gemm_f8), ACT_I8 (for gemm_w4a8), ACT_MXFP8
+    or ACT_MXFP4 (for gemm_mxfp4), or None for the normed values alone.  Returns
+    Norm(codes, scale, total, y): total is t (None without a residual; give `total`, which may
+    be x or residual, to place it), y the normed values in x's type (always with quant=None, else
+    where `y` is a tensor, or True for a new one)."""
+    if quant not in (None, ACT_F8, ACT_I8, ACT_MXFP8, ACT_MXFP4):
+        raise ValueError(f"quant: expected one of ACTS' values or None, got {quant!r}")
+    dev = _need(x, "x", _FLOAT_IN, ndim=2)
+    n, hidden = x.shape
+    step = 128 if quant == ACT_F8 else 32 if quant in (ACT_MXFP8, ACT_MXFP4) else 8
+    if hidden % step:
+        raise ValueError(f"x: the number of columns must be a multiple of {step}, got {hidden}")
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps!r}")
+    _need(weight, "weight", _FLOAT_IN, numel=hidden, device=dev)
+    if residual is not None:
+        _need(residual, "residual", (x.dtype,), numel=n * hidden, device=dev)
+        if total is None:
+            total = _empty((n, hidden), x.dtype, dev, stream)
+        else:
+            _need(total, "total", (x.dtype,), numel=n * hidden, device=dev)
+    elif total is not None:
+        raise ValueError("total: there is no residual to add")
+    if quant is None:
+        if out is not None or scale is not None:
+            raise ValueError("out, scale: nothing is quantized")
+    else:
+        out, scale = _act_out(quant, n, hidden, out, scale, dev, stream)
+    if y is True or (y is None and quant is None):
+        y = _empty((n, hidden), x.dtype, dev, stream)
+    elif y is False:
+        y = None
+    if y is not None:
+        _need(y, "y", (x.dtype,), numel=n * hidden, device=dev)
+    a = _RmsNorm(n, hidden, _ptr(x), _ptr(residual), _dtype(x), _ptr(weight), _dtype(weight), eps, -1 if quant is None else quant,
+                 _ptr(out), _ptr(scale), _ptr(total), _ptr(y))
+    cur = _need_current(dev)
+    _check(_lib.qblk_rmsnorm(C.byref(a), _stream(stream, cur)), "qblk_rmsnorm")
+    return Norm(out, scale, total, y)

@@ -53,6 +53,18 @@ hipError_t launch_ffn_f8(const uint8_t* w13, const float* s13, const uint8_t* w2
                          hipStream_t s);
 hipError_t launch_zero_bytes(void* y, int64_t bytes, hipStream_t s);
 
+// Microscaling formats: `f8` for e4m3 elements, else e2m1; sizes positive
+hipError_t launch_quantize_mx(const void* v, int vt, int64_t rows, int64_t k, bool f8, uint8_t* codes, uint8_t* scale,
+                              hipStream_t s);
+hipError_t launch_dequant_mx(const uint8_t* codes, const uint8_t* scale, int64_t rows, int64_t k, bool f8, void* out,
+                             int ot, hipStream_t s);
+int64_t gemm_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8);
+hipError_t launch_gemm_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const uint8_t* xq,
+                             const uint8_t* xs, bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s);
+int64_t linear_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8);
+hipError_t launch_linear_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const void* x, int xt,
+                               bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s);
+
 // A dispatch packet counts its work-items in 32 bits per grid dimension, so
 // one launch covers at most 2^32 - 1 threads along x.  Launchers whose grid
 // grows with the data run it in pieces of whole workgroups:

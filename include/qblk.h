@@ -391,6 +391,104 @@ typedef struct {
 size_t qblk_moe_workspace(const qblk_moe_t* args); /* reads the sizes and fmt only */
 qblk_status_t qblk_moe(const qblk_moe_t* args, qblk_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * OCP microscaling (MX): 32 neighbouring values of a row under one power of two,
+ * kept as the byte e + 127 (e8m0; 255: every value of the block is NaN).  Rows
+ * of k values, k a multiple of 32: codes row-major, scales rows x k/32 bytes.
+ *
+ *   QBLK_ACT_MXFP4   e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives), two
+ *                    to a byte: column 2j in the low half of byte j, k/2 bytes a row
+ *   QBLK_ACT_MXFP8   e4m3, a byte each
+ *
+ * Rule: e = floor(log2(max|v|)) - 2 (MXFP4) or - 8 (MXFP8), at least -127 (a block
+ * of zeros: -127); code = the element nearest to v / 2^e, halves to the even code,
+ * beyond the largest element (6 or 448) that one; all exact, so equal inputs give
+ * equal bytes everywhere.  A NaN or an infinity in a block makes its scale 255
+ * and its codes 0.
+ *
+ * The products: Y[t,r] = sum_c W[r,c] X[t,c] with W (m x k) in MXFP4 and X
+ * (n x k) in either, an element being code * 2^e; Y n x m row-major of type yt in
+ * {F32, F16, BF16}, one rounding at the end, sums in fp32 in a fixed order (equal
+ * inputs, equal bits).  With MXFP4 activations, and with MXFP8 ones and F32
+ * results, sums are exact to fp32 rounding.  F16 and BF16 results of MXFP8
+ * activations are formed by the 8-bit matrix instructions, which drop of the
+ * products of 8 neighbouring columns what lies below 2^-13 of the largest.  A token
+ * with a NaN block has NaN results, and so has a row of W with one.  With MXFP8
+ * and F32 an element has to be a bf16 number (2^-133 to 2^128; what is smaller
+ * counts as 0).
+ * m at most 2^26, k at most 2^23 (QBLK_ERR_SHAPE).
+ *
+ * Codes are 16-byte aligned, the scales' bytes at any address; workspaces as for
+ * the 8-bit products above. */
+typedef enum {
+  QBLK_ACT_NONE = -1, /* qblk_rmsnorm only: no codes */
+  QBLK_ACT_F8 = 0,    /* e4m3, fp32 scale per 128 columns (qblk_quantize_act_f8) */
+  QBLK_ACT_I8 = 1,    /* int8, fp32 scale per row (qblk_quantize_act_i8) */
+  QBLK_ACT_MXFP8 = 2,
+  QBLK_ACT_MXFP4 = 3
+} qblk_act_t;
+
+/* Quantize v (rows x k, type vt in {F32, F16, BF16}); elem is one of the two MX
+ * formats (QBLK_ERR_FORMAT otherwise, as everywhere below). */
+qblk_status_t qblk_quantize_mx(const void* v, qblk_dtype_t vt, int64_t rows,
+                               int64_t k, qblk_act_t elem, void* codes,
+                               uint8_t* scale, qblk_stream_t stream);
+
+/* The values that codes and scales stand for, rounded once to type ot. */
+qblk_status_t qblk_dequant_mx(const void* codes, const uint8_t* scale,
+                              qblk_act_t elem, int64_t rows, int64_t k,
+                              void* out, qblk_dtype_t ot, qblk_stream_t stream);
+
+/* Y = X W^T from the codes and scales of both. */
+size_t qblk_gemm_mxfp4_workspace(int64_t m, int64_t k, int64_t n,
+                                 qblk_act_t act);
+qblk_status_t qblk_gemm_mxfp4(const uint8_t* w, const uint8_t* wscale,
+                              int64_t m, int64_t k, const void* xq,
+                              const uint8_t* xscale, qblk_act_t act, int64_t n,
+                              void* y, qblk_dtype_t yt, void* workspace,
+                              size_t workspace_bytes, qblk_stream_t stream);
+
+/* The same with X given as values of type xt, quantized to `act` by the call. */
+size_t qblk_linear_mxfp4_workspace(int64_t m, int64_t k, int64_t n,
+                                   qblk_act_t act);
+qblk_status_t qblk_linear_mxfp4(const uint8_t* w, const uint8_t* wscale,
+                                int64_t m, int64_t k, const void* x,
+                                qblk_dtype_t xt, qblk_act_t act, int64_t n,
+                                void* y, qblk_dtype_t yt, void* workspace,
+                                size_t workspace_bytes, qblk_stream_t stream);
+
+/* Root-mean-square norm of n rows (tokens) of `hidden` values, with the codes that
+ * a product reads:
+ *
+ *   t = x + residual, rounded to the type xt (t = x where residual is NULL)
+ *   y = t * (1 / sqrt(mean(t^2) + eps)) * weight     in fp32
+ *
+ * total: t (n x hidden of type xt), written where residual is given; it may be the
+ * same memory as x or as residual.  y: the normed values rounded to xt, or NULL.
+ * codes and scale: y quantized by the rule and in the layout of `act` (hidden a
+ * multiple of 128 for QBLK_ACT_F8, of 32 for the MX formats, of 8 for
+ * QBLK_ACT_I8 and QBLK_ACT_NONE), from the fp32 values.  Other outputs must not
+ * overlap any input or one another.  weight has `hidden` values of type wt in
+ * {F32, F16, BF16}; eps >= 0 (QBLK_ERR_SHAPE); sums of squares are fp32 (a row
+ * whose sum passes 3.4e38 gives zeros, a row of zeros with eps = 0 NaN).  hidden
+ * at most 2^24. */
+typedef struct {
+  int64_t n, hidden;
+  const void* x;
+  const void* residual; /* or NULL */
+  int xt;               /* a qblk_dtype_t; plain ints, so that any value can be refused */
+  const void* weight;
+  int wt; /* a qblk_dtype_t */
+  float eps;
+  int act; /* a qblk_act_t */
+  void* codes;
+  void* scale;
+  void* total;
+  void* y;
+} qblk_rmsnorm_t;
+
+qblk_status_t qblk_rmsnorm(const qblk_rmsnorm_t* args, qblk_stream_t stream);
+
 /* Static English text for a status code (never NULL). */
 const char* qblk_status_string(qblk_status_t st);
 
