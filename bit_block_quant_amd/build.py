@@ -30,7 +30,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqblk.so")
 HBMREF_LIB = os.path.join(HERE, "libqblk_hbmref.so")
 SOURCES = ["qblk_abi.hip", "qblk_quant.hip", "qblk_gemv.hip", "qblk_gemm.hip", "qblk_w4a8.hip",
-           "qblk_ffn_abi.hip", "qblk_f8.hip", "qblk_moe.hip", "qblk_mx_abi.hip", "qblk_mx.hip",
+           "qblk_ffn_abi.hip", "qblk_f8.hip", "qblk_moe.hip", "qblk_mx_abi.hip", "qblk_mx.hip", "qblk_mx_tile.hip",
            "qblk_norm.hip"]
 HBMREF_SOURCES = ["hbm_read.hip"]
 ARCH = "gfx950"

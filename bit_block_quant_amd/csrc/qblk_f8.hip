@@ -1014,12 +1014,7 @@ hipError_t tile_product(const uint8_t* w, const float* ws, int64_t m, int64_t k,
         a.part, m * n, plan.splits, static_cast<int>(up), groups, static_cast<uint8_t*>(y), hs, at.tok, at.group);
     return hipGetLastError();
   }
-  const int64_t pitch = part_pitch(m);
-  return in_pieces(n * pitch / 4, 256, 256, [&](int64_t first, int64_t c) {
-    k_f8_join<<<dim3(static_cast<unsigned>((c + 255) / 256)), 256, 0, s>>>(a.part, first, c, static_cast<int>(m), n * pitch,
-                                                                         plan.splits, y, yt);
-    return hipGetLastError();
-  });
+  return launch_join(a.part, m, n, plan.splits, y, yt, s);
 }
 
 // Products of up to this many tokens are exact to fp32 rounding.
@@ -1078,6 +1073,14 @@ hipError_t code_product(const uint8_t* w, const float* ws, int64_t m, int64_t k,
 }
 
 }  // namespace
+
+hipError_t launch_join(const float* part, int64_t m, int64_t n, int splits, void* y, int yt, hipStream_t s) {
+  const int64_t pitch = part_pitch(m);
+  return in_pieces(n * pitch / 4, 256, 256, [&](int64_t first, int64_t c) {
+    k_f8_join<<<dim3(static_cast<unsigned>((c + 255) / 256)), 256, 0, s>>>(part, first, c, static_cast<int>(m), n * pitch, splits, y, yt);
+    return hipGetLastError();
+  });
+}
 
 hipError_t launch_quantize_act_f8(const void* x, int xt, int64_t n, int64_t k, uint8_t* xq, float* scale,
                                   hipStream_t s) {

@@ -51,6 +51,8 @@ int64_t ffn_f8_workspace(int64_t hidden, int64_t inter, int64_t n);
 hipError_t launch_ffn_f8(const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2, int64_t hidden,
                          int64_t inter, const void* x, int xt, int64_t n, void* y, int yt, void* work,
                          hipStream_t s);
+// y (n x m of type yt) = the sum of `splits` partial products [split][n][m rounded up to 4], in their order
+hipError_t launch_join(const float* part, int64_t m, int64_t n, int splits, void* y, int yt, hipStream_t s);
 hipError_t launch_zero_bytes(void* y, int64_t bytes, hipStream_t s);
 
 // Microscaling formats: `f8` for e4m3 elements, else e2m1; sizes positive

@@ -8,6 +8,7 @@
 // The matrix cores take both scales with the codes: in a K = 128 instruction a
 // lane holds 32 columns, which is one block, and its scales.
 #include "qblk_mx_device.h"
+#include "qblk_mx_tile.h"
 
 namespace qblk {
 namespace {
@@ -23,8 +24,9 @@ constexpr int kQuantUnits = 4;
 
 template <int XT, bool F8>
 __global__ __launch_bounds__(256) void k_quant_mx(const void* __restrict__ x, int64_t first, int64_t units,
-                                                  uint8_t* __restrict__ codes, uint8_t* __restrict__ scale) {
-  // unit = 8 values; whole quads are on or off together
+                                                  uint8_t* __restrict__ codes, uint8_t* __restrict__ scale, int per, int padded) {
+  // unit = 8 values; whole quads are on or off together.  padded > 0: rows of `per`
+  // units go to rows of `padded` bytes, zeros behind them.
   const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (256 * kQuantUnits) + threadIdx.x;
   float v[kQuantUnits][8];
 #pragma unroll
@@ -44,10 +46,22 @@ __global__ __launch_bounds__(256) void k_quant_mx(const void* __restrict__ x, in
     uint32_t c[2];
     mx_codes<F8, 8>(v[i], b, c);
     if (u >= units) continue;
+    constexpr int kBytes = F8 ? 8 : 4;
+    int64_t at = (first + u) * kBytes;
+    if (padded > 0) {
+      const int64_t t = (first + u) / per;
+      const int in = static_cast<int>(first + u - t * per);
+      at = t * padded + in * kBytes;
+      if (in < 4)  // the row's first block clears what is behind its last: fewer than 4 blocks
+        for (int b = per * kBytes + in * 4 * kBytes; b < padded; b += 16 * kBytes) {
+#pragma unroll
+          for (int o = 0; o < 4 * kBytes; o += 16) *reinterpret_cast<u32x4*>(codes + t * padded + b + o) = u32x4{0, 0, 0, 0};
+        }
+    }
     if constexpr (F8)
-      *reinterpret_cast<u32x2*>(codes + (first + u) * 8) = u32x2{c[0], c[1]};
+      *reinterpret_cast<u32x2*>(codes + at) = u32x2{c[0], c[1]};
     else
-      *reinterpret_cast<uint32_t*>(codes + (first + u) * 4) = c[0];
+      *reinterpret_cast<uint32_t*>(codes + at) = c[0];
     if ((threadIdx.x & 3) == 0) scale[(first + u) / 4] = static_cast<uint8_t>(b);
   }
 }
@@ -179,6 +193,7 @@ struct FewArgs {
   const uint8_t* xq;
   const uint8_t* xs;
   void* y;
+  int64_t xrow;  // bytes from one token's codes to the next one's
   int m, k, n, yt;
 };
 
@@ -192,7 +207,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_mx_few(FewArgs p) {
   const int row0 = blockIdx.x * 16 * NR, tok0 = blockIdx.y * 16 * T;
   const int r = lane & 15, q = lane >> 4;
   uint8_t* const region = lds + wave * kRegion;
-  const int64_t wrow = static_cast<int64_t>(nb) * 16, xrow = static_cast<int64_t>(nb) * (F8 ? 32 : 16);
+  const int64_t wrow = static_cast<int64_t>(nb) * 16;
 
   // Rows and tokens past the last repeat it; their results are not stored.
   auto row_at = [&](int row) { return row < p.m ? row : p.m - 1; };
@@ -215,11 +230,11 @@ __global__ __launch_bounds__(WAVES* kWave) void k_mx_few(FewArgs p) {
         const int at = g * kCols + 16 * (lane & 15) < p.k ? g * kCols + 16 * (lane & 15) : p.k - 16;
 #pragma unroll
         for (int u = 0; u < 4; u++)
-          s.x[t][u] = *reinterpret_cast<const u32x4*>(p.xq + tok_at(tok0 + 16 * t + 4 * u + (lane >> 4)) * xrow + at);
+          s.x[t][u] = *reinterpret_cast<const u32x4*>(p.xq + tok_at(tok0 + 16 * t + 4 * u + (lane >> 4)) * p.xrow + at);
       } else {
 #pragma unroll
         for (int u = 0; u < 2; u++)
-          s.x[t][u] = *reinterpret_cast<const u32x4*>(p.xq + tok_at(tok0 + 16 * t + 8 * u + (lane >> 3)) * xrow + block * 16);
+          s.x[t][u] = *reinterpret_cast<const u32x4*>(p.xq + tok_at(tok0 + 16 * t + 8 * u + (lane >> 3)) * p.xrow + block * 16);
       }
       s.sx[t] = scales8(p.xs + static_cast<int64_t>(tok_at(tok0 + 16 * t + r)) * nb, g, nb);
     }
@@ -364,10 +379,9 @@ hipError_t few_kind(const FewArgs& a, bool f8, hipStream_t s) {
 
 // in pieces of tokens: at most 65535 workgroups in the grid's second dimension
 hipError_t few_product(const FewArgs& all, int64_t n, bool f8, hipStream_t s) {
-  const int64_t xrow = f8 ? all.k : all.k / 2;
   return in_pieces(n, 64, 1, [&](int64_t t0, int64_t c) {
     FewArgs a = all;
-    a.xq += t0 * xrow;
+    a.xq += t0 * all.xrow;
     a.xs += t0 * (all.k / kMxBlock);
     a.y = static_cast<uint8_t*>(a.y) + t0 * a.m * (a.yt == QBLK_F32 ? 4 : 2);
     a.n = static_cast<int>(c);
@@ -376,19 +390,110 @@ hipError_t few_product(const FewArgs& all, int64_t n, bool f8, hipStream_t s) {
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
-int64_t code_bytes(int64_t n, int64_t k, bool f8) { return align256(f8 ? n * k : n * (k / 2)); }
+
+// ------------------------------------------------------------- many tokens
+constexpr int kTileCols = 128;  // columns of a stage of the tile kernel
+int64_t padded_row(int64_t k, bool f8) { return (k + kTileCols - 1) / kTileCols * (f8 ? kTileCols : kTileCols / 2); }
+
+struct Plan {
+  int tokens, splits, per;  // tokens of a tile; stages per split, a multiple of 4
+  double us;
+};
+Plan tile_plan(int64_t m, int64_t k, int64_t n, bool f8) {
+  const int64_t rt = (m + kMxTileRows - 1) / kMxTileRows, G = (k + kTileCols - 1) / kTileCols;
+  Plan best{64, 1, static_cast<int>((G + 3) / 4 * 4), 1e30};
+  for (int i = 0; i < 3; i++) {
+    const int tokens = 64 << i;
+    for (int sp = 1; sp <= 16; sp *= 2) {
+      const int64_t per = ((G + sp - 1) / sp + 3) / 4 * 4, real = (G + per - 1) / per;
+      if (sp > 1 && real < sp) break;
+      const int64_t rounds = (rt * ((n + tokens - 1) / tokens) * real + cu_count() - 1) / cu_count();
+      constexpr double stage[2][3] = {{0.3, 0.4, 0.6}, {0.4, 0.6, 1.0}};
+      const double us = rounds * (per * stage[f8][i] + 4 + i) + (real > 1 ? 2.0 + 0.35e-6 * real * n * m * 4 : 0.0);
+      if (us < best.us) best = Plan{tokens, static_cast<int>(real), static_cast<int>(per), us};
+    }
+  }
+  return best;
+}
+
+bool use_few(int64_t m, int64_t k, int64_t n, bool f8) { return n <= 32; }
+
+// Rows of x's codes copied into rows of whole stages, zeros behind them: 16 bytes a thread.
+__global__ __launch_bounds__(256) void k_mx_pad(const uint8_t* __restrict__ x, int64_t first, int64_t count, int row, int padded,
+                                                uint8_t* __restrict__ out) {
+  int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= count) return;
+  i += first;
+  const int per = padded / 16;
+  const int64_t t = i / per;
+  const int c = 16 * static_cast<int>(i - t * per);
+  *reinterpret_cast<u32x4*>(out + 16 * i) = c < row ? *reinterpret_cast<const u32x4*>(x + t * row + c) : u32x4{0, 0, 0, 0};
+}
+
+hipError_t pad(const uint8_t* x, int64_t n, int64_t row, int64_t padded, uint8_t* out, hipStream_t s) {
+  return in_pieces(n * (padded / 16), 256, 256, [&](int64_t first, int64_t c) {
+    k_mx_pad<<<dim3(static_cast<unsigned>((c + 255) / 256)), 256, 0, s>>>(x, first, c, static_cast<int>(row), static_cast<int>(padded), out);
+    return hipGetLastError();
+  });
+}
+
+hipError_t tile_product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const uint8_t* xq, int64_t xrow,
+                        const uint8_t* xs, bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
+  const Plan plan = tile_plan(m, k, n, f8);
+  uint8_t* rest = static_cast<uint8_t*>(work);
+  const int64_t row = padded_row(k, f8);
+  if (xrow != row) {
+    const hipError_t e = pad(xq, n, xrow, row, rest, s);
+    if (e != hipSuccess) return e;
+    xq = rest;
+    rest += align256(n * row);
+  }
+  const int64_t rt = (m + kMxTileRows - 1) / kMxTileRows;
+  MxTileArgs a{w, ws, xq, xs, y, reinterpret_cast<float*>(rest), row, static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt,
+               static_cast<int>(rt), static_cast<int>((n + plan.tokens - 1) / plan.tokens), 0, plan.per};
+  log_launch("mx tile f%d m=%lld k=%lld n=%lld tokens=%d splits=%d", f8 ? 8 : 4, (long long)m, (long long)k, (long long)n, plan.tokens, plan.splits);
+  if (plan.splits > 1) {
+    const hipError_t e = mx_tile(plan.tokens, f8, a, plan.splits, s);
+    return e == hipSuccess ? launch_join(a.part, m, n, plan.splits, y, yt, s) : e;
+  }
+  // in pieces of the tokens: a launch of 2^23 tiles would pass 32 bits of threads
+  return in_pieces((n + plan.tokens - 1) / plan.tokens, 1, 512 * rt, [&](int64_t tt, int64_t count) {
+    const int64_t t0 = tt * plan.tokens, left = n - t0;
+    MxTileArgs b = a;
+    b.xq += t0 * row;
+    b.xs += t0 * (k / kMxBlock);
+    b.y = static_cast<uint8_t*>(y) + t0 * m * (yt == QBLK_F32 ? 4 : 2);
+    b.n = static_cast<int>(left < count * plan.tokens ? left : count * plan.tokens);
+    b.tok_tiles = static_cast<int>(count);
+    return mx_tile(plan.tokens, f8, b, 1, s);
+  });
+}
+
+// Y from codes in rows of xrow bytes, by one kernel or the other
+hipError_t product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const uint8_t* xq, int64_t xrow,
+                   const uint8_t* xs, bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
+  if (use_few(m, k, n, f8) || (f8 && yt == QBLK_F32))
+    return few_product(FewArgs{w, ws, xq, xs, y, xrow, static_cast<int>(m), static_cast<int>(k), 0, yt}, n, f8, s);
+  return tile_product(w, ws, m, k, xq, xrow, xs, f8, n, y, yt, work, s);
+}
 
 template <bool F8>
-hipError_t quantize(const void* x, int xt, int64_t units, uint8_t* codes, uint8_t* scale, hipStream_t s) {
+hipError_t quantize(const void* x, int xt, int64_t units, uint8_t* codes, uint8_t* scale, int per, int padded, hipStream_t s) {
   return in_pieces(units, 256 * kQuantUnits, 256, [&](int64_t u0, int64_t c) {
     const dim3 grid(static_cast<unsigned>((c + 256 * kQuantUnits - 1) / (256 * kQuantUnits)));
     switch (xt) {
-      case QBLK_F32: k_quant_mx<QBLK_F32, F8><<<grid, 256, 0, s>>>(x, u0, c, codes, scale); break;
-      case QBLK_F16: k_quant_mx<QBLK_F16, F8><<<grid, 256, 0, s>>>(x, u0, c, codes, scale); break;
-      default: k_quant_mx<QBLK_BF16, F8><<<grid, 256, 0, s>>>(x, u0, c, codes, scale); break;
+      case QBLK_F32: k_quant_mx<QBLK_F32, F8><<<grid, 256, 0, s>>>(x, u0, c, codes, scale, per, padded); break;
+      case QBLK_F16: k_quant_mx<QBLK_F16, F8><<<grid, 256, 0, s>>>(x, u0, c, codes, scale, per, padded); break;
+      default: k_quant_mx<QBLK_BF16, F8><<<grid, 256, 0, s>>>(x, u0, c, codes, scale, per, padded); break;
     }
     return hipGetLastError();
   });
+}
+
+hipError_t quantize_rows(const void* v, int vt, int64_t rows, int64_t k, bool f8, int64_t row_bytes, uint8_t* codes, uint8_t* scale,
+                         hipStream_t s) {
+  const int per = static_cast<int>(k / 8), padded = row_bytes == (f8 ? k : k / 2) ? 0 : static_cast<int>(row_bytes);
+  return f8 ? quantize<true>(v, vt, rows * per, codes, scale, per, padded, s) : quantize<false>(v, vt, rows * per, codes, scale, per, padded, s);
 }
 
 template <bool F8>
@@ -409,7 +514,7 @@ hipError_t dequant(const uint8_t* codes, const uint8_t* scale, int64_t units, vo
 hipError_t launch_quantize_mx(const void* v, int vt, int64_t rows, int64_t k, bool f8, uint8_t* codes, uint8_t* scale,
                               hipStream_t s) {
   log_launch("quantize_mx%d rows=%lld k=%lld", f8 ? 8 : 4, (long long)rows, (long long)k);
-  return f8 ? quantize<true>(v, vt, rows * (k / 8), codes, scale, s) : quantize<false>(v, vt, rows * (k / 8), codes, scale, s);
+  return quantize_rows(v, vt, rows, k, f8, f8 ? k : k / 2, codes, scale, s);
 }
 
 hipError_t launch_dequant_mx(const uint8_t* codes, const uint8_t* scale, int64_t rows, int64_t k, bool f8, void* out,
@@ -418,24 +523,34 @@ hipError_t launch_dequant_mx(const uint8_t* codes, const uint8_t* scale, int64_t
   return f8 ? dequant<true>(codes, scale, rows * (k / 8), out, ot, s) : dequant<false>(codes, scale, rows * (k / 8), out, ot, s);
 }
 
-int64_t gemm_mxfp4_workspace(int64_t, int64_t, int64_t, bool) { return 0; }
+int64_t gemm_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
+  if (use_few(m, k, n, f8)) return 0;
+  const int splits = tile_plan(m, k, n, f8).splits;
+  return (k % kTileCols != 0 ? align256(n * padded_row(k, f8)) : 0) + (splits > 1 ? align256(splits * n * part_pitch(m) * 4) : 0);
+}
 
 hipError_t launch_gemm_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const uint8_t* xq,
                              const uint8_t* xs, bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
-  return few_product(FewArgs{w, ws, xq, xs, y, static_cast<int>(m), static_cast<int>(k), 0, yt}, n, f8, s);
+  return product(w, ws, m, k, xq, f8 ? k : k / 2, xs, f8, n, y, yt, work, s);
 }
 
+// Codes of x in rows of whole stages where the tile kernel reads them.
 int64_t linear_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
-  return code_bytes(n, k, f8) + align256(n * (k / kMxBlock)) + gemm_mxfp4_workspace(m, k, n, f8);
+  const bool few = use_few(m, k, n, f8);
+  const int splits = few ? 1 : tile_plan(m, k, n, f8).splits;
+  return align256(n * (few ? (f8 ? k : k / 2) : padded_row(k, f8))) + align256(n * (k / kMxBlock)) +
+         (splits > 1 ? align256(splits * n * part_pitch(m) * 4) : 0);
 }
 
 hipError_t launch_linear_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const void* x, int xt,
                                bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
+  const bool few = use_few(m, k, n, f8);
+  const int64_t row = few ? (f8 ? k : k / 2) : padded_row(k, f8);
   uint8_t* xq = static_cast<uint8_t*>(work);
-  uint8_t* xs = xq + code_bytes(n, k, f8);
-  const hipError_t e = launch_quantize_mx(x, xt, n, k, f8, xq, xs, s);
+  uint8_t* xs = xq + align256(n * row);
+  const hipError_t e = quantize_rows(x, xt, n, k, f8, row, xq, xs, s);
   if (e != hipSuccess) return e;
-  return launch_gemm_mxfp4(w, ws, m, k, xq, xs, f8, n, y, yt, xs + align256(n * (k / kMxBlock)), s);
+  return product(w, ws, m, k, xq, row, xs, f8, n, y, yt, xs + align256(n * (k / kMxBlock)), s);
 }
 
 }  // namespace qblk
