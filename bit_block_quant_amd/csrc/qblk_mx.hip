@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void k_quant_mx(const void* __restrict__ x, in
       const int64_t t = (first + u) / per;
       const int in = static_cast<int>(first + u - t * per);
       at = t * padded + in * kBytes;
-      if (in < 4)  // the row's first block clears what is behind its last: fewer than 4 blocks
+      if (in < 4)  // the row's first block clears what is behind its last
         for (int b = per * kBytes + in * 4 * kBytes; b < padded; b += 16 * kBytes) {
 #pragma unroll
           for (int o = 0; o < 4 * kBytes; o += 16) *reinterpret_cast<u32x4*>(codes + t * padded + b + o) = u32x4{0, 0, 0, 0};
@@ -392,15 +392,15 @@ hipError_t few_product(const FewArgs& all, int64_t n, bool f8, hipStream_t s) {
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // ------------------------------------------------------------- many tokens
-constexpr int kTileCols = 128;  // columns of a stage of the tile kernel
-int64_t padded_row(int64_t k, bool f8) { return (k + kTileCols - 1) / kTileCols * (f8 ? kTileCols : kTileCols / 2); }
+// Bytes of a token's codes in whole stages of the tile kernel: 128 each.
+int64_t padded_row(int64_t k, bool f8) { return ((f8 ? k : k / 2) + 127) / 128 * 128; }
 
 struct Plan {
   int tokens, splits, per;  // tokens of a tile; stages per split, a multiple of 4
   double us;
 };
 Plan tile_plan(int64_t m, int64_t k, int64_t n, bool f8) {
-  const int64_t rt = (m + kMxTileRows - 1) / kMxTileRows, G = (k + kTileCols - 1) / kTileCols;
+  const int64_t rt = (m + kMxTileRows - 1) / kMxTileRows, G = padded_row(k, f8) / 128;
   Plan best{64, 1, static_cast<int>((G + 3) / 4 * 4), 1e30};
   for (int i = 0; i < 3; i++) {
     const int tokens = 64 << i;
@@ -408,7 +408,7 @@ Plan tile_plan(int64_t m, int64_t k, int64_t n, bool f8) {
       const int64_t per = ((G + sp - 1) / sp + 3) / 4 * 4, real = (G + per - 1) / per;
       if (sp > 1 && real < sp) break;
       const int64_t rounds = (rt * ((n + tokens - 1) / tokens) * real + cu_count() - 1) / cu_count();
-      constexpr double stage[2][3] = {{0.3, 0.4, 0.6}, {0.4, 0.6, 1.0}};
+      constexpr double stage[2][3] = {{0.6, 0.8, 1.2}, {0.4, 0.6, 1.0}};
       const double us = rounds * (per * stage[f8][i] + 4 + i) + (real > 1 ? 2.0 + 0.35e-6 * real * n * m * 4 : 0.0);
       if (us < best.us) best = Plan{tokens, static_cast<int>(real), static_cast<int>(per), us};
     }
@@ -526,7 +526,7 @@ hipError_t launch_dequant_mx(const uint8_t* codes, const uint8_t* scale, int64_t
 int64_t gemm_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
   if (use_few(m, k, n, f8)) return 0;
   const int splits = tile_plan(m, k, n, f8).splits;
-  return (k % kTileCols != 0 ? align256(n * padded_row(k, f8)) : 0) + (splits > 1 ? align256(splits * n * part_pitch(m) * 4) : 0);
+  return (padded_row(k, f8) != (f8 ? k : k / 2) ? align256(n * padded_row(k, f8)) : 0) + (splits > 1 ? align256(splits * n * part_pitch(m) * 4) : 0);
 }
 
 hipError_t launch_gemm_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const uint8_t* xq,

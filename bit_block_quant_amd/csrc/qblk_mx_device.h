@@ -84,6 +84,19 @@ __device__ __forceinline__ uint32_t mx_codes4(const float v[4], uint32_t b) {
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[2], q[3], 1.0f, 1);
 }
 
+// Four values in 16 bits each, rounded to nearest even by the conversions (v_cvt_pk_bf16_f32
+// for bf16: one operation for two values).
+template <int YT>
+__device__ __forceinline__ u32x2 pack16(const float4_t& v) {
+  if constexpr (YT == QBLK_F16) {
+    const half2_t a = {static_cast<half_t>(v.x), static_cast<half_t>(v.y)}, b = {static_cast<half_t>(v.z), static_cast<half_t>(v.w)};
+    return u32x2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+  } else {
+    const bf16x2_n a = {static_cast<__bf16>(v.x), static_cast<__bf16>(v.y)}, b = {static_cast<__bf16>(v.z), static_cast<__bf16>(v.w)};
+    return u32x2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+  }
+}
+
 // The value of a scale's byte.
 __device__ __forceinline__ float mx_scale_value(uint32_t b) {
   return b == 255u ? __builtin_nanf("") : b == 0u ? 0x1p-127f : __builtin_bit_cast(float, b << 23);

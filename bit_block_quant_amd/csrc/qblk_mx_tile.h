@@ -9,7 +9,7 @@ namespace qblk {
 struct MxTileArgs {
   const uint8_t* w;
   const uint8_t* ws;
-  const uint8_t* xq;  // rows of x_pitch bytes: whole stages of 128 columns, zeros past k
+  const uint8_t* xq;  // rows of x_pitch bytes: whole stages of 128 bytes, zeros past k
   const uint8_t* xs;
   void* y;
   float* part;  // split K: partial sums, [split][n][part_pitch(m)]
