@@ -118,12 +118,14 @@ __global__ __launch_bounds__(256) void k_dequant_mx(const uint8_t* __restrict__ 
 }
 
 // ------------------------------------------------------------- few tokens
-// A workgroup owns NR tiles of 16 rows for 16 T tokens and splits the columns
-// over its waves, 256 columns (a group: 128 bytes of a row of W) at a time: wave w
-// takes groups w, w + WAVES, ...; the waves' fp32 sums meet in LDS in a fixed
-// order.  A load takes 8 rows' 128 bytes, 8 neighbouring lanes a row, and the rows
-// change lanes through LDS of the wave's own.  A wave has its next two groups in
-// flight, in registers.
+// Bound by the weight bytes.  A workgroup of 8 or 16 waves owns a run of rows, 16 at a
+// time, for all tokens, and splits the columns over its waves, 256 (a group: 128 bytes
+// of a row of W) at a time: wave w takes groups w, w + WAVES, ...; the waves' fp32 sums
+// meet in LDS in a fixed order.  x stays in LDS: each wave holds the columns it works on,
+// so no wave waits for another before the sums.  The loads of W run on over the ends of
+// the 16 rows, in registers: a load takes 8 rows' 128 bytes, 8 neighbouring lanes a row,
+// and the rows change lanes through LDS of the wave's own.  A wave has one group in
+// flight where 24 waves share a compute unit, two where 16 do (few_shape).
 //
 // EXACT: e4m3 activations with fp32 results.  The e4m3 instructions bring 8
 // neighbouring columns' products to the largest one's exponent and drop what is
@@ -132,17 +134,16 @@ __global__ __launch_bounds__(256) void k_dequant_mx(const uint8_t* __restrict__ 
 // multiplied there, where sums are exact to fp32 rounding.  (e2m1 by e2m1: the
 // products of a block are whole multiples of 1/4 up to 36 of one scale, and the
 // scaled instructions' sums were found equal to fp32 sums of them.)
+// XSRC: kCodes, x as codes and scales; else the element type of x, which every
+// workgroup quantizes itself (one launch less; for few values, see fused_quant).
+constexpr int kCodes = 3;
 constexpr int kCols = 256;                  // of a group
 constexpr int kGroupBlocks = kCols / kMxBlock;
+constexpr int64_t kFewLds = 160 * 1024;
 
-constexpr int few_region(int T, int NR, bool F8) {
-  return T * NR * 1024 > (F8 ? 4096 : 2048) ? T * NR * 1024 : (F8 ? 4096 : 2048);
-}
-
-template <int T, int NR, bool F8>
 struct FewSet {
-  u32x4 w[NR][2], x[T][F8 ? 4 : 2];
-  uint64_t sw[NR], sx[T];
+  u32x4 w[2];
+  uint64_t s;
 };
 
 // 8 bytes of a row's scales from block 8 g on; past the row's end zeros (2^-127)
@@ -190,203 +191,324 @@ __device__ __forceinline__ bf16x8_n wide8(uint32_t a, uint32_t b, float s) {
 struct FewArgs {
   const uint8_t* w;
   const uint8_t* ws;
-  const uint8_t* xq;
+  const void* x;  // codes, or values
   const uint8_t* xs;
   void* y;
   int64_t xrow;  // bytes from one token's codes to the next one's
   int m, k, n, yt;
+  int rows;  // of a workgroup
 };
 
-template <int T, int NR, int WAVES, bool F8, bool EXACT>
+// What a workgroup keeps in LDS: partial sums of two turns, tiles of W changing lanes, and
+// x with its scales.
+constexpr int few_sums(int T, int waves) { return 2 * waves * T * 1024; }
+constexpr int few_steps(int k, int waves) { return ((k + kCols - 1) / kCols + waves - 1) / waves; }  // groups of a wave
+constexpr int few_xrow(bool f8) { return f8 ? kCols : kCols / 2; }
+constexpr int64_t few_lds(int T, int waves, int k, int64_t n, bool f8) {
+  return few_sums(T, waves) + waves * 2048 + int64_t(waves) * few_steps(k, waves) * n * (few_xrow(f8) + kGroupBlocks);
+}
+
+template <int T, int WAVES, bool F8, bool EXACT, int XSRC>
 __global__ __launch_bounds__(WAVES* kWave) void k_mx_few(FewArgs p) {
   extern __shared__ __align__(16) uint8_t lds[];
-  constexpr int kRegion = few_region(T, NR, F8);
-  using Set = FewSet<T, NR, F8>;
+  constexpr int kXRow = few_xrow(F8), kSets = WAVES == 16 ? 2 : 1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nb = p.k / kMxBlock, G = (nb + kGroupBlocks - 1) / kGroupBlocks;
-  const int row0 = blockIdx.x * 16 * NR, tok0 = blockIdx.y * 16 * T;
+  const int steps = few_steps(p.k, WAVES);
+  const int begin = blockIdx.x * p.rows, end = p.m - begin < p.rows ? p.m : begin + p.rows;
+  const int tiles = (end - begin + 15) / 16;
   const int r = lane & 15, q = lane >> 4;
-  uint8_t* const region = lds + wave * kRegion;
-  const int64_t wrow = static_cast<int64_t>(nb) * 16;
+  constexpr int kSums = few_sums(T, WAVES);
+  uint8_t* const turn_at = lds + kSums + wave * 2048;
+  uint8_t* const xl = lds + kSums + WAVES * 2048 + wave * steps * p.n * kXRow;
+  uint8_t* const xsl = lds + kSums + WAVES * 2048 + WAVES * steps * p.n * kXRow + wave * steps * p.n * kGroupBlocks;
+  const uint32_t wrow = static_cast<uint32_t>(nb) * 16;
 
-  // Rows and tokens past the last repeat it; their results are not stored.
-  auto row_at = [&](int row) { return row < p.m ? row : p.m - 1; };
-  auto tok_at = [&](int tok) { return tok < p.n ? tok : p.n - 1; };
-  auto load = [&](Set& s, int step) {
-    int g = wave + step * WAVES;
+  // The next group of this wave, `lstep` of the 16 rows `ltile`.  Rows past the last
+  // repeat it (their results are not stored), blocks past the row's end its last (x is
+  // zero there), and so does a wave without a group.
+  const int total = tiles * steps;
+  int ltile = 0, lstep = 0, loaded = 0;
+  const uint32_t whole = static_cast<uint32_t>(lane >> 3) * wrow + 16 * (lane & 7), whole_s = static_cast<uint32_t>(r * nb);
+  auto next_load = [&](FewSet& s) {
+    if (loaded++ >= total) return;
+    int g = wave + lstep * WAVES;
     if (g > G - 1) g = G - 1;
-    // blocks past the row's end repeat its last; x is cleared there
-    const int block = g * kGroupBlocks + (lane & 7) < nb ? g * kGroupBlocks + (lane & 7) : nb - 1;
+    const int row0 = begin + 16 * ltile, last = end - 1 - row0 < 15 ? end - 1 - row0 : 15, left = nb - g * kGroupBlocks;
+    const uint8_t* base = p.w + static_cast<int64_t>(row0) * wrow + static_cast<int64_t>(g) * (kCols / 2);
+    uint32_t at[2] = {whole, whole + 8 * wrow}, at_s = whole_s;
+    if (last < 15 || left < kGroupBlocks) {
+      const int chunk = (lane & 7) < left ? lane & 7 : left - 1;
 #pragma unroll
-    for (int a = 0; a < NR; a++) {
-#pragma unroll
-      for (int u = 0; u < 2; u++)
-        s.w[a][u] = *reinterpret_cast<const u32x4*>(p.w + row_at(row0 + 16 * a + 8 * u + (lane >> 3)) * wrow + block * 16);
-      s.sw[a] = scales8(p.ws + static_cast<int64_t>(row_at(row0 + 16 * a + r)) * nb, g, nb);
-    }
-#pragma unroll
-    for (int t = 0; t < T; t++) {
-      if constexpr (F8) {
-        const int at = g * kCols + 16 * (lane & 15) < p.k ? g * kCols + 16 * (lane & 15) : p.k - 16;
-#pragma unroll
-        for (int u = 0; u < 4; u++)
-          s.x[t][u] = *reinterpret_cast<const u32x4*>(p.xq + tok_at(tok0 + 16 * t + 4 * u + (lane >> 4)) * p.xrow + at);
-      } else {
-#pragma unroll
-        for (int u = 0; u < 2; u++)
-          s.x[t][u] = *reinterpret_cast<const u32x4*>(p.xq + tok_at(tok0 + 16 * t + 8 * u + (lane >> 3)) * p.xrow + block * 16);
+      for (int u = 0; u < 2; u++) {
+        const int row = 8 * u + (lane >> 3) < last ? 8 * u + (lane >> 3) : last;
+        at[u] = static_cast<uint32_t>(row) * wrow + 16 * chunk;
       }
-      s.sx[t] = scales8(p.xs + static_cast<int64_t>(tok_at(tok0 + 16 * t + r)) * nb, g, nb);
+      at_s = static_cast<uint32_t>((r < last ? r : last) * nb);
     }
+#pragma unroll
+    for (int u = 0; u < 2; u++) s.w[u] = *reinterpret_cast<const u32x4*>(base + at[u]);
+    s.s = scales8(p.ws + static_cast<int64_t>(row0) * nb + at_s, g, nb);
+    if (++lstep == steps) {
+      lstep = 0;
+      ltile++;
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  // rows of 128 bytes, by 8 lanes each -> row r, chunks q and q + 4
-  auto turn = [&](const u32x4 v[2], u32x4 out[2]) {
+  FewSet S[kSets];
+  auto first_loads = [&]() {
+#pragma unroll
+    for (int i = 0; i < kSets; i++) next_load(S[i]);
+  };
+
+  // x: chunk c of token t's group lies at chunk c ^ t & 15 (of 8: c ^ t >> 1 & 7) of its row.
+  auto x_place = [&](int step, int t, int c) {
+    return xl + (step * p.n + t) * kXRow + ((F8 ? c ^ (t & 15) : c ^ ((t >> 1) & 7)) << 4);
+  };
+  // Some tokens' part of this wave's group `step` at a time, several in flight; the first
+  // of W behind the first of x.
+  int xstep = 0, xtok = 0;
+  if constexpr (XSRC == kCodes) {
+    constexpr int lanes = kXRow / 16, per = 64 / lanes, kAtOnce = 4;  // lanes of a token, tokens of a load
+    const uint8_t* xq = static_cast<const uint8_t*>(p.x);
+    const int c = lane % lanes;
+    for (bool first = true; xstep < steps; first = false) {
+      u32x4 v[kAtOnce];
+      uint64_t sc[kAtOnce];
+      int st[kAtOnce], tk[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; i++) {
+        st[i] = xstep;
+        tk[i] = xtok + lane / lanes;
+        const int g = wave + xstep * WAVES, left = p.k - g * kCols;  // columns of this group
+        const bool here = xstep < steps && tk[i] < p.n;
+        v[i] = here && c * (F8 ? 16 : 32) < left ? *reinterpret_cast<const u32x4*>(xq + tk[i] * p.xrow + static_cast<int64_t>(g) * kXRow + 16 * c)
+                                                 : u32x4{0, 0, 0, 0};
+        sc[i] = here && c == 0 && left > 0 ? scales8(p.xs + static_cast<int64_t>(tk[i]) * nb, g, nb) : 0;
+        xtok += per;
+        if (xtok >= p.n) {
+          xtok = 0;
+          xstep++;
+        }
+      }
+      if (first) first_loads();
+#pragma unroll
+      for (int i = 0; i < kAtOnce; i++) {
+        if (st[i] >= steps || tk[i] >= p.n) continue;
+        *reinterpret_cast<u32x4*>(x_place(st[i], tk[i], c)) = v[i];
+        if (c == 0) *reinterpret_cast<uint64_t*>(xsl + (st[i] * p.n + tk[i]) * kGroupBlocks) = sc[i];
+      }
+    }
+  } else {
+    constexpr int kAtOnce = 2;  // a token's group by 32 lanes, 8 values each
+    const int l = lane & 31;
+    for (bool first = true; xstep < steps; first = false) {
+      float v[kAtOnce][8];
+      int st[kAtOnce], tk[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; i++) {
+        int s2[2], t2[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          s2[h] = xstep;
+          t2[h] = xtok;
+          if (++xtok == p.n) {
+            xtok = 0;
+            xstep++;
+          }
+        }
+        st[i] = lane < 32 ? s2[0] : s2[1];
+        tk[i] = lane < 32 ? t2[0] : t2[1];
+        const int col = (wave + st[i] * WAVES) * kCols + 8 * l;
+        if (col < p.k) {  // (a group past the steps lies past the columns too)
+          load8<XSRC>(p.x, static_cast<int64_t>(tk[i]) * p.k + col, v[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; e++) v[i][e] = 0.0f;
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (first) first_loads();
+#pragma unroll
+      for (int i = 0; i < kAtOnce; i++) {
+        const uint32_t b = mx_scale<F8>(quad_max(top_bits<8>(v[i])));
+        uint32_t c[2];
+        mx_codes<F8, 8>(v[i], b, c);
+        if (st[i] >= steps) continue;
+        if constexpr (F8)
+          *reinterpret_cast<u32x2*>(x_place(st[i], tk[i], l >> 1) + 8 * (l & 1)) = u32x2{c[0], c[1]};
+        else
+          *reinterpret_cast<uint32_t*>(x_place(st[i], tk[i], l >> 2) + 4 * (l & 3)) = c[0];
+        if ((l & 3) == 0) xsl[(st[i] * p.n + tk[i]) * kGroupBlocks + (l >> 2)] = static_cast<uint8_t>(b);
+      }
+    }
+  }
+  wave_fence();
+
+  float4_t acc[T];
+#pragma unroll
+  for (int t = 0; t < T; t++) acc[t] = float4_t{0, 0, 0, 0};
+  int tile = 0, step = 0;
+
+  auto use = [&](const FewSet& s) {
+    const int g = wave + step * WAVES;
+    // rows of 128 bytes, by 8 lanes each -> row r, chunks q and q + 4
 #pragma unroll
     for (int u = 0; u < 2; u++) {
       const int row = 8 * u + (lane >> 3);
-      *reinterpret_cast<u32x4*>(region + row * 128 + (((lane & 7) ^ ((row >> 1) & 7)) << 4)) = v[u];
+      *reinterpret_cast<u32x4*>(turn_at + row * 128 + (((lane & 7) ^ ((row >> 1) & 7)) << 4)) = s.w[u];
     }
     wave_fence();
-    const int key = (r >> 1) & 7;
-    out[0] = *reinterpret_cast<const u32x4*>(region + r * 128 + ((q ^ key) << 4));
-    out[1] = *reinterpret_cast<const u32x4*>(region + r * 128 + (((q + 4) ^ key) << 4));
-    wave_fence();
-  };
-  // rows of 256 bytes, by 16 lanes each -> row r, of either 128 bytes what a lane's
-  // operand holds: chunks q and q + 4 (the instruction's order), or its block (EXACT)
-  auto turn8 = [&](const u32x4 v[4], u32x4 out[2][2]) {
+    u32x4 wv[2];
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-      const int row = 4 * u + (lane >> 4);
-      *reinterpret_cast<u32x4*>(region + row * 256 + (((lane & 15) ^ row) << 4)) = v[u];
-    }
-    wave_fence();
+    for (int j = 0; j < 2; j++) wv[j] = *reinterpret_cast<const u32x4*>(turn_at + r * 128 + (((q + 4 * j) ^ ((r >> 1) & 7)) << 4));
+    const uint32_t sw[2] = {static_cast<uint32_t>(s.s) >> (8 * q), static_cast<uint32_t>(s.s >> 32) >> (8 * q)};
+    if (g < G) {
 #pragma unroll
-    for (int j = 0; j < 2; j++)
+      for (int t = 0; t < T; t++) {
+        const int tok = 16 * t + r < p.n ? 16 * t + r : p.n - 1;
+        const u32x2 sc = *reinterpret_cast<const u32x2*>(xsl + (step * p.n + tok) * kGroupBlocks);
+        const uint32_t sx[2] = {sc.x >> (8 * q), sc.y >> (8 * q)};
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int c = 8 * j + (EXACT ? 2 * q + h : q + 4 * h);
-        out[j][h] = *reinterpret_cast<const u32x4*>(region + r * 256 + ((c ^ r) << 4));
-      }
-    wave_fence();
-  };
-
-  Set A, B;
-  load(A, 0);
-  load(B, 1);
-  float4_t acc[NR][T];
-#pragma unroll
-  for (int a = 0; a < NR; a++)
-#pragma unroll
-    for (int t = 0; t < T; t++) acc[a][t] = float4_t{0, 0, 0, 0};
-
-  auto use = [&](const Set& s, int step) {
-    const int g = wave + step * WAVES;
-    if (g >= G) return;
-    u32x4 wv[NR][2];
-    uint32_t sw[NR][2];
-#pragma unroll
-    for (int a = 0; a < NR; a++) {
-      turn(s.w[a], wv[a]);
-      sw[a][0] = static_cast<uint32_t>(s.sw[a]) >> (8 * q);
-      sw[a][1] = static_cast<uint32_t>(s.sw[a] >> 32) >> (8 * q);
-    }
-    const int left = nb - g * kGroupBlocks;  // blocks of this group
-#pragma unroll
-    for (int t = 0; t < T; t++) {
-      u32x4 xv[2][2];
-      if constexpr (F8) {
-        turn8(s.x[t], xv);
-      } else {
-        u32x4 c[2];
-        turn(s.x[t], c);
-        xv[0][0] = c[0];
-        xv[1][0] = c[1];
-      }
-      if (left < kGroupBlocks) {
-#pragma unroll
-        for (int j = 0; j < 2; j++)
-#pragma unroll
-          for (int h = 0; h < (F8 ? 2 : 1); h++) {
-            const int b = 4 * j + (F8 && !EXACT ? (q >> 1) + 2 * h : q);
-            if (b >= left) xv[j][h] = u32x4{0, 0, 0, 0};
-          }
-      }
-      const uint32_t sx[2] = {static_cast<uint32_t>(s.sx[t]) >> (8 * q), static_cast<uint32_t>(s.sx[t] >> 32) >> (8 * q)};
-#pragma unroll
-      for (int j = 0; j < 2; j++)
-#pragma unroll
-        for (int a = 0; a < NR; a++) {
+        for (int j = 0; j < 2; j++) {
           if constexpr (EXACT) {
-            const float fw = __builtin_bit_cast(float, (sw[a][j] & 255u) << 23), fx = __builtin_bit_cast(float, (sx[j] & 255u) << 23);
+            const float fw = __builtin_bit_cast(float, (sw[j] & 255u) << 23), fx = __builtin_bit_cast(float, (sx[j] & 255u) << 23);
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-              acc[a][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide4(wv[a][j][2 * h], fw), wide8(xv[j][h].x, xv[j][h].y, fx), acc[a][t], 0, 0, 0);
-              acc[a][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide4(wv[a][j][2 * h + 1], fw), wide8(xv[j][h].z, xv[j][h].w, fx), acc[a][t], 0, 0, 0);
+              const u32x4 x = *reinterpret_cast<const u32x4*>(x_place(step, tok, 8 * j + 2 * q + h));
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide4(wv[j][2 * h], fw), wide8(x.x, x.y, fx), acc[t], 0, 0, 0);
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide4(wv[j][2 * h + 1], fw), wide8(x.z, x.w, fx), acc[t], 0, 0, 0);
             }
-          } else if constexpr (F8) {
-            acc[a][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(regs4(wv[a][j]), regs8(xv[j][0], xv[j][1]), acc[a][t], 4, 0, 0,
-                                                                         static_cast<int>(sw[a][j]), 0, static_cast<int>(sx[j]));
+          } else if constexpr (F8) {  // the instruction's order of e4m3: 16 columns of each half of the 128
+            const u32x4 x0 = *reinterpret_cast<const u32x4*>(x_place(step, tok, 8 * j + q));
+            const u32x4 x1 = *reinterpret_cast<const u32x4*>(x_place(step, tok, 8 * j + q + 4));
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(regs4(wv[j]), regs8(x0, x1), acc[t], 4, 0, 0,
+                                                                     static_cast<int>(sw[j]), 0, static_cast<int>(sx[j]));
           } else {
-            acc[a][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(regs4(wv[a][j]), regs4(xv[j][0]), acc[a][t], 4, 4, 0,
-                                                                         static_cast<int>(sw[a][j]), 0, static_cast<int>(sx[j]));
+            const u32x4 x = *reinterpret_cast<const u32x4*>(x_place(step, tok, 4 * j + q));
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(regs4(wv[j]), regs4(x), acc[t], 4, 4, 0,
+                                                                     static_cast<int>(sw[j]), 0, static_cast<int>(sx[j]));
           }
         }
+      }
     }
+    wave_fence();  // (the tile's place is written again)
+    if (++step < steps) return;
+    // The waves' sums, in turns of two places: one barrier a tile.  Lane (r, q) holds rows
+    // 4 q .. 4 q + 3 for token r of each 16.
+    step = 0;
+    uint8_t* const sums = lds + (tile & 1) * (kSums / 2);
+#pragma unroll
+    for (int t = 0; t < T; t++) {
+      *reinterpret_cast<float4_t*>(sums + ((wave * T + t) * 64 + lane) * 16) = acc[t];
+      acc[t] = float4_t{0, 0, 0, 0};
+    }
+    // as __syncthreads, but the loads stay under way
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const float* rf = reinterpret_cast<const float*>(sums);
+    for (int o = threadIdx.x; o < T * 256; o += WAVES * kWave) {
+      const int rr = o & 15, tok = o >> 4;
+      const int at = ((tok >> 4) * 64 + (rr >> 2) * 16 + (tok & 15)) * 4 + (rr & 3);
+      float sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < WAVES; v++) sum += rf[v * (T * 256) + at];
+      const int row = begin + 16 * tile + rr;
+      if (tok < p.n && row < end) store_y(p.y, static_cast<int64_t>(tok) * p.m + row, sum, p.yt);
+    }
+    tile++;
   };
 
-  const int steps = (G + WAVES - 1) / WAVES;
-  for (int step = 0; step < steps; step += 2) {
-    use(A, step);
-    load(A, step + 2);
-    use(B, step + 1);
-    load(B, step + 3);
-  }
-
-  // lane (r, q) holds rows 4q..4q+3 of each tile for token r of each 16
-  float4_t* red = reinterpret_cast<float4_t*>(region);
+  for (int it = 0; it < total; it += kSets) {
 #pragma unroll
-  for (int a = 0; a < NR; a++)
-#pragma unroll
-    for (int t = 0; t < T; t++) red[(a * T + t) * 64 + lane] = acc[a][t];
-  __syncthreads();
-  const float* rf = reinterpret_cast<const float*>(lds);
-  for (int o = threadIdx.x; o < NR * T * 256; o += WAVES * kWave) {
-    const int rr = o & 15, tok = (o >> 4) % (16 * T), a = o / (256 * T);
-    const int at = ((a * T + (tok >> 4)) * 64 + (rr >> 2) * 16 + (tok & 15)) * 4 + (rr & 3);
-    float sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < WAVES; v++) sum += rf[v * (kRegion / 4) + at];
-    const int row = row0 + 16 * a + rr;
-    if (tok0 + tok < p.n && row < p.m) store_y(p.y, static_cast<int64_t>(tok0 + tok) * p.m + row, sum, p.yt);
+    for (int i = 0; i < kSets; i++) {
+      if (it + i >= total) break;
+      use(S[i]);
+      next_load(S[i]);
+    }
   }
 }
 
-template <int T, int NR, int WAVES, bool F8, bool EXACT>
-hipError_t few(const FewArgs& a, hipStream_t s) {
-  const size_t lds = static_cast<size_t>(WAVES) * few_region(T, NR, F8);
-  log_launch("mx few%s m=%d k=%d n=%d T=%d NR=%d waves=%d%s", F8 ? " f8" : " f4", a.m, a.k, a.n, T, NR, WAVES, EXACT ? " exact" : "");
-  k_mx_few<T, NR, WAVES, F8, EXACT>
-      <<<dim3(static_cast<unsigned>((a.m + 16 * NR - 1) / (16 * NR)), static_cast<unsigned>((a.n + 16 * T - 1) / (16 * T))), WAVES * kWave, lds, s>>>(a);
+// Waves of a workgroup, and workgroups that share a compute unit.  16 waves and two
+// groups in flight each where there is one workgroup for a unit (x leaves no room for
+// another, or the row tiles do not suffice) and groups for as many waves; else 8 waves,
+// up to three workgroups.  Us, 8 and 16 waves, weights from memory: 4096 x 14336, one
+// token 13.6, 10.6; 22016 x 4096, 16 tokens 21.6, 17.6; but 22016 x 4096, one token 12.3,
+// 15.5; 11008 x 4096, one token 8.5, 9.4; 700 x 1024 3.0, 3.8.
+struct FewShape {
+  int waves, per_cu;
+};
+template <int T>
+FewShape few_shape(int64_t m, int k, int64_t n, bool f8) {
+  const int64_t lds = few_lds(T, 8, k, n, f8), tiles = (m + 15) / 16;
+  const int per_cu = T == 1 && lds <= 53 * 1024 ? 3 : lds <= 80 * 1024 ? 2 : 1;
+  const bool room = few_lds(T, 16, k, n, f8) <= kFewLds, one = tiles <= cu_count() || per_cu == 1 || (per_cu == 2 && tiles <= 3 * cu_count());
+  return room && one && k > 8 * kCols ? FewShape{16, 1} : FewShape{8, per_cu};
+}
+
+template <int T, int WAVES, bool F8, bool EXACT, int XSRC>
+hipError_t few_go(FewArgs a, int per_cu, hipStream_t s) {
+  const size_t lds = static_cast<size_t>(few_lds(T, WAVES, a.k, a.n, F8));
+  static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx_few<T, WAVES, F8, EXACT, XSRC>),
+                                                        hipFuncAttributeMaxDynamicSharedMemorySize, kFewLds);
+  if (allowed != hipSuccess) return allowed;
+  const int64_t most = static_cast<int64_t>(cu_count()) * per_cu, tiles = (static_cast<int64_t>(a.m) + 15) / 16;
+  a.rows = static_cast<int>(tiles <= most ? 16 : (a.m + most - 1) / most);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.m) + a.rows - 1) / a.rows);
+  log_launch("mx few%s m=%d k=%d n=%d T=%d waves=%d rows=%d x=%d%s lds=%zu", F8 ? " f8" : " f4", a.m, a.k, a.n, T, WAVES, a.rows, XSRC,
+             EXACT ? " exact" : "", lds);
+  k_mx_few<T, WAVES, F8, EXACT, XSRC><<<dim3(grid), WAVES * kWave, lds, s>>>(a);
   return hipGetLastError();
 }
 
-template <int T>
-hipError_t few_kind(const FewArgs& a, bool f8, hipStream_t s) {
-  if (!f8) return few<T, 1, 8, false, false>(a, s);
-  return a.yt == QBLK_F32 ? few<T, 1, 8, true, true>(a, s) : few<T, 1, 8, true, false>(a, s);
+template <int T, bool F8, bool EXACT, int XSRC>
+hipError_t few(const FewArgs& a, hipStream_t s) {
+  const FewShape f = few_shape<T>(a.m, a.k, a.n, F8);
+  return f.waves == 16 ? few_go<T, 16, F8, EXACT, XSRC>(a, f.per_cu, s) : few_go<T, 8, F8, EXACT, XSRC>(a, f.per_cu, s);
 }
 
-// in pieces of tokens: at most 65535 workgroups in the grid's second dimension
+template <int T, int XSRC>
+hipError_t few_kind(const FewArgs& a, bool f8, hipStream_t s) {
+  if (!f8) return few<T, false, false, XSRC>(a, s);
+  return a.yt == QBLK_F32 ? few<T, true, true, XSRC>(a, s) : few<T, true, false, XSRC>(a, s);
+}
+
+// Tokens of one launch: what fits into LDS with x.
+int64_t few_tokens(int64_t k, bool f8) {
+  for (int T = 2; T >= 1; T /= 2)
+    if (few_lds(T, 8, static_cast<int>(k), 16 * T, f8) <= kFewLds) return 16 * T;
+  int64_t n = 15;
+  while (n > 0 && few_lds(1, 8, static_cast<int>(k), n, f8) > kFewLds) n--;
+  return n;
+}
+
+// x as codes: as many tokens a launch as fit.
 hipError_t few_product(const FewArgs& all, int64_t n, bool f8, hipStream_t s) {
-  return in_pieces(n, 64, 1, [&](int64_t t0, int64_t c) {
+  const int64_t most = few_tokens(all.k, f8);
+  for (int64_t t0 = 0; t0 < n; t0 += most) {
     FewArgs a = all;
-    a.xq += t0 * all.xrow;
+    a.x = static_cast<const uint8_t*>(a.x) + t0 * all.xrow;
     a.xs += t0 * (all.k / kMxBlock);
     a.y = static_cast<uint8_t*>(a.y) + t0 * a.m * (a.yt == QBLK_F32 ? 4 : 2);
-    a.n = static_cast<int>(c);
-    return c <= 16 ? few_kind<1>(a, f8, s) : c <= 32 ? few_kind<2>(a, f8, s) : few_kind<4>(a, f8, s);
-  }, 65535);
+    a.n = static_cast<int>(n - t0 < most ? n - t0 : most);
+    const hipError_t e = a.n <= 16 ? few_kind<1, kCodes>(a, f8, s) : few_kind<2, kCodes>(a, f8, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// Whether a product quantizes its x inside every workgroup: that saves a launch, but each
+// of them does it again.
+bool fused_quant(int64_t n, int64_t k) { return n <= 4 && n * k <= 32768; }  // (always fits into LDS)
+
+hipError_t fused_product(const FewArgs& a, int xt, bool f8, hipStream_t s) {
+  switch (xt) {
+    case QBLK_F32: return few_kind<1, QBLK_F32>(a, f8, s);
+    case QBLK_F16: return few_kind<1, QBLK_F16>(a, f8, s);
+    default: return few_kind<1, QBLK_BF16>(a, f8, s);
+  }
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -416,7 +538,7 @@ Plan tile_plan(int64_t m, int64_t k, int64_t n, bool f8) {
   return best;
 }
 
-bool use_few(int64_t m, int64_t k, int64_t n, bool f8) { return n <= 32; }
+bool use_few(int64_t m, int64_t k, int64_t n, bool f8) { return n <= 16 && n <= few_tokens(k, f8); }
 
 // Rows of x's codes copied into rows of whole stages, zeros behind them: 16 bytes a thread.
 __global__ __launch_bounds__(256) void k_mx_pad(const uint8_t* __restrict__ x, int64_t first, int64_t count, int row, int padded,
@@ -473,7 +595,7 @@ hipError_t tile_product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t 
 hipError_t product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const uint8_t* xq, int64_t xrow,
                    const uint8_t* xs, bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
   if (use_few(m, k, n, f8) || (f8 && yt == QBLK_F32))
-    return few_product(FewArgs{w, ws, xq, xs, y, xrow, static_cast<int>(m), static_cast<int>(k), 0, yt}, n, f8, s);
+    return few_product(FewArgs{w, ws, xq, xs, y, xrow, static_cast<int>(m), static_cast<int>(k), 0, yt, 0}, n, f8, s);
   return tile_product(w, ws, m, k, xq, xrow, xs, f8, n, y, yt, work, s);
 }
 
@@ -536,6 +658,7 @@ hipError_t launch_gemm_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int
 
 // Codes of x in rows of whole stages where the tile kernel reads them.
 int64_t linear_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
+  if (fused_quant(n, k)) return 0;
   const bool few = use_few(m, k, n, f8);
   const int splits = few ? 1 : tile_plan(m, k, n, f8).splits;
   return align256(n * (few ? (f8 ? k : k / 2) : padded_row(k, f8))) + align256(n * (k / kMxBlock)) +
@@ -544,6 +667,8 @@ int64_t linear_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
 
 hipError_t launch_linear_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const void* x, int xt,
                                bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
+  if (fused_quant(n, k))
+    return fused_product(FewArgs{w, ws, x, nullptr, y, 0, static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt, 0}, xt, f8, s);
   const bool few = use_few(m, k, n, f8);
   const int64_t row = few ? (f8 ? k : k / 2) : padded_row(k, f8);
   uint8_t* xq = static_cast<uint8_t*>(work);

@@ -109,7 +109,7 @@ __device__ __forceinline__ u32x4 few_scales(const uint8_t* row, int b, int nb) {
 template <int I, int ALL, int READS, int COPIES>
 __device__ __forceinline__ void order() {
   if constexpr (I < ALL) {
-    constexpr int left = READS - 2 * I, reads = left > 2 ? 2 : left > 0 ? left : 0, copies = (I + 1) * COPIES / ALL - I * COPIES / ALL;
+    constexpr int left = READS - 3 * I, reads = left > 3 ? 3 : left > 0 ? left : 0, copies = (I + 1) * COPIES / ALL - I * COPIES / ALL;
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
     if constexpr (copies > 0) __builtin_amdgcn_sched_group_barrier(0x020, copies, 0);
