@@ -518,27 +518,80 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 int64_t padded_row(int64_t k, bool f8) { return ((f8 ? k : k / 2) + 127) / 128 * 128; }
 
 struct Plan {
-  int tokens, splits, per;  // tokens of a tile; stages per split, a multiple of 4
+  int shape, splits, per;  // of kMxTiles; stages per split, a multiple of 4
   double us;
 };
+
+// The time of a shape is estimated from what was measured for it, us: a stage of a
+// workgroup that has a compute unit to itself or (tiles of 128 rows, `both`) shares it,
+// the rest of a workgroup's time, and of a split its join.  Fitted to 1500 times of 96
+// products of either kind (8 matrices, 20 to 4096 tokens, every shape, 1 to 16
+// splits, weights from memory): the choice is 0.6% (e2m1) and 1.1% (e4m3) behind the best
+// form on average, at worst 24% (4096 x 4096, 100 tokens: 11.8 us for 9.5).
+double tile_us(int64_t tiles, int shape, int64_t per, int64_t splits, int64_t out, bool f8, int64_t cus) {
+  constexpr double both[2][5] = {{1.73, 1.40, 0.74, 1.20, 0.96}, {1.31, 0.82, 0.61, 0.91, 0.65}};
+  constexpr double alone[2][2] = {{0.62, 0.52}, {0.52, 0.365}};
+  constexpr double ends[2][5] = {{3.2, 2.0, 3.6, 2.9, 2.1}, {0.1, 0.5, 1.5, 0.6, 0.5}};
+  constexpr double launch[2] = {1.2, 2.7}, join[2] = {3.6, 3.3}, join_byte[2] = {0.355e-6, 0.414e-6};
+  const int64_t rounds = (tiles * splits + cus - 1) / cus;
+  const double one = per * (shape >= 3 ? alone[f8][shape - 3] : both[f8][shape]) + ends[f8][shape], two = per * both[f8][shape] + ends[f8][shape];
+  const double work = shape >= 3 ? (rounds / 2) * two + (rounds % 2) * one : rounds * one;
+  return launch[f8] + work + (splits > 1 ? join[f8] + join_byte[f8] * splits * out * 4 : 0.0);
+}
+int64_t tiles_of(int64_t m, int64_t n, int shape) {
+  return ((m + kMxTiles[shape].rows - 1) / kMxTiles[shape].rows) * ((n + kMxTiles[shape].tokens - 1) / kMxTiles[shape].tokens);
+}
 Plan tile_plan(int64_t m, int64_t k, int64_t n, bool f8) {
-  const int64_t rt = (m + kMxTileRows - 1) / kMxTileRows, G = padded_row(k, f8) / 128;
-  Plan best{64, 1, static_cast<int>((G + 3) / 4 * 4), 1e30};
-  for (int i = 0; i < 3; i++) {
-    const int tokens = 64 << i;
-    for (int sp = 1; sp <= 16; sp *= 2) {
-      const int64_t per = ((G + sp - 1) / sp + 3) / 4 * 4, real = (G + per - 1) / per;
-      if (sp > 1 && real < sp) break;
-      const int64_t rounds = (rt * ((n + tokens - 1) / tokens) * real + cu_count() - 1) / cu_count();
-      constexpr double stage[2][3] = {{0.6, 0.8, 1.2}, {0.4, 0.6, 1.0}};
-      const double us = rounds * (per * stage[f8][i] + 4 + i) + (real > 1 ? 2.0 + 0.35e-6 * real * n * m * 4 : 0.0);
-      if (us < best.us) best = Plan{tokens, static_cast<int>(real), static_cast<int>(per), us};
+  const int64_t G = padded_row(k, f8) / 128, cus = cu_count();
+  Plan best{0, 1, static_cast<int>((G + 3) / 4 * 4), 1e30};
+  for (int i = 0; i < 5; i++) {
+    const int64_t tiles = tiles_of(m, n, i);
+    for (int want = 1; want <= 16; want++) {
+      if (want > 1 && (tiles * want > 2 * cus || 4 * want >= G + 4)) break;  // (splits are for tiles that leave units idle)
+      const int64_t per = ((G + want - 1) / want + 3) / 4 * 4;
+      if ((want - 1) * per >= G) continue;  // as many as fewer splits
+      const double us = tile_us(tiles, i, want == 1 ? G : per, want, n * m, f8, cus);
+      if (us < best.us) best = Plan{i, want, static_cast<int>(per), us};
     }
   }
   return best;
 }
 
-bool use_few(int64_t m, int64_t k, int64_t n, bool f8) { return n <= 16 && n <= few_tokens(k, f8); }
+// Where an unsplit product's tiles leave much of their last round of compute units
+// empty: the row tiles that fill whole rounds with one shape, and a second launch of the
+// other rows with another.
+struct Cut {
+  int64_t rows;  // of the first launch; 0: do not cut
+  int shape, rest;
+};
+Cut tile_cut(const Plan& plan, int64_t m, int64_t k, int64_t n, bool f8) {
+  Cut best{0, 0, 0};
+  if (plan.splits > 1) return best;
+  const int64_t G = padded_row(k, f8) / 128, cus = cu_count();
+  double us = plan.us;
+  for (int i = 0; i < 2; i++) {
+    const int64_t rt = (m + 255) / 256, wide = (n + kMxTiles[i].tokens - 1) / kMxTiles[i].tokens;
+    const int64_t rows = rt * wide / cus * cus / wide;
+    if (rows <= 0 || rows >= rt) continue;
+    for (int rest = i; rest < 5; rest++) {
+      const double c = tile_us(rows * wide, i, G, 1, 0, f8, cus) + tile_us(tiles_of(m - rows * 256, n, rest), rest, G, 1, 0, f8, cus);
+      if (c < us) {
+        us = c;
+        best = Cut{rows * 256, i, rest};
+      }
+    }
+  }
+  return best;
+}
+
+// Whether a product runs k_mx_few: up to 16 tokens wherever their codes fit into LDS; up
+// to 32 with few rows (us, few and tiles: 4096 x 4096, 24 tokens, e2m1 7.1, 9.3, e4m3 12.2, 9.3; 32:
+// 9.3, 9.4; 11008 x 4096, 24 tokens, e2m1 12.1, 12.0).
+bool use_few(int64_t m, int64_t k, int64_t n, bool f8) {
+  if (n > few_tokens(k, f8)) return false;
+  return n <= 16 || (!f8 && n <= 32 && (m + 15) / 16 <= cu_count());
+}
+
 
 // Rows of x's codes copied into rows of whole stages, zeros behind them: 16 bytes a thread.
 __global__ __launch_bounds__(256) void k_mx_pad(const uint8_t* __restrict__ x, int64_t first, int64_t count, int row, int padded,
@@ -570,25 +623,39 @@ hipError_t tile_product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t 
     xq = rest;
     rest += align256(n * row);
   }
-  const int64_t rt = (m + kMxTileRows - 1) / kMxTileRows;
   MxTileArgs a{w, ws, xq, xs, y, reinterpret_cast<float*>(rest), row, static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt,
-               static_cast<int>(rt), static_cast<int>((n + plan.tokens - 1) / plan.tokens), 0, plan.per};
-  log_launch("mx tile f%d m=%lld k=%lld n=%lld tokens=%d splits=%d", f8 ? 8 : 4, (long long)m, (long long)k, (long long)n, plan.tokens, plan.splits);
-  if (plan.splits > 1) {
-    const hipError_t e = mx_tile(plan.tokens, f8, a, plan.splits, s);
-    return e == hipSuccess ? launch_join(a.part, m, n, plan.splits, y, yt, s) : e;
+               0, 0, 0, plan.per};
+  // the rows [first, first + rows), `first` a multiple of the shape's
+  auto whole = [&](int shape, int64_t first, int64_t rows) {
+    const MxTile tile = kMxTiles[shape];
+    a.first_row_tile = static_cast<int>(first / tile.rows);
+    a.row_tiles = static_cast<int>((rows + tile.rows - 1) / tile.rows);
+    log_launch("mx tile f%d m=%lld k=%lld n=%lld rows=%lld+%lld tile=%dx%d", f8 ? 8 : 4, (long long)m, (long long)k, (long long)n,
+               (long long)first, (long long)rows, tile.rows, tile.tokens);
+    // in pieces of the tokens: a launch of 2^23 tiles would pass 32 bits of threads
+    return in_pieces((n + tile.tokens - 1) / tile.tokens, 1, 512 * static_cast<int64_t>(a.row_tiles), [&](int64_t tt, int64_t count) {
+      const int64_t t0 = tt * tile.tokens, left = n - t0;
+      MxTileArgs b = a;
+      b.xq += t0 * row;
+      b.xs += t0 * (k / kMxBlock);
+      b.y = static_cast<uint8_t*>(y) + t0 * m * (yt == QBLK_F32 ? 4 : 2);
+      b.n = static_cast<int>(left < count * tile.tokens ? left : count * tile.tokens);
+      b.tok_tiles = static_cast<int>(count);
+      return mx_tile(shape, f8, b, 1, s);
+    });
+  };
+  if (plan.splits == 1) {
+    const Cut cut = tile_cut(plan, m, k, n, f8);
+    if (cut.rows == 0) return whole(plan.shape, 0, m);
+    const hipError_t e = whole(cut.shape, 0, cut.rows);
+    return e == hipSuccess ? whole(cut.rest, cut.rows, m - cut.rows) : e;
   }
-  // in pieces of the tokens: a launch of 2^23 tiles would pass 32 bits of threads
-  return in_pieces((n + plan.tokens - 1) / plan.tokens, 1, 512 * rt, [&](int64_t tt, int64_t count) {
-    const int64_t t0 = tt * plan.tokens, left = n - t0;
-    MxTileArgs b = a;
-    b.xq += t0 * row;
-    b.xs += t0 * (k / kMxBlock);
-    b.y = static_cast<uint8_t*>(y) + t0 * m * (yt == QBLK_F32 ? 4 : 2);
-    b.n = static_cast<int>(left < count * plan.tokens ? left : count * plan.tokens);
-    b.tok_tiles = static_cast<int>(count);
-    return mx_tile(plan.tokens, f8, b, 1, s);
-  });
+  const MxTile tile = kMxTiles[plan.shape];
+  a.row_tiles = static_cast<int>((m + tile.rows - 1) / tile.rows);
+  a.tok_tiles = static_cast<int>((n + tile.tokens - 1) / tile.tokens);
+  log_launch("mx tile f%d m=%lld k=%lld n=%lld tile=%dx%d splits=%d", f8 ? 8 : 4, (long long)m, (long long)k, (long long)n, tile.rows, tile.tokens, plan.splits);
+  const hipError_t e = mx_tile(plan.shape, f8, a, plan.splits, s);
+  return e == hipSuccess ? launch_join(a.part, m, n, plan.splits, y, yt, s) : e;
 }
 
 // Y from codes in rows of xrow bytes, by one kernel or the other

@@ -18,8 +18,13 @@ struct MxTileArgs {
   int stages_per_split;  // a multiple of 4
 };
 
-constexpr int kMxTileRows = 256;
-// tokens of a tile: 256, 128 or 64; splits > 1 write partial sums
-hipError_t mx_tile(int tokens, bool f8, const MxTileArgs& a, int splits, hipStream_t s);
+// rows and tokens of each tile shape
+struct MxTile {
+  int rows, tokens;
+};
+constexpr MxTile kMxTiles[] = {{256, 256}, {256, 128}, {256, 64}, {128, 128}, {128, 64}};
+
+// splits > 1 write partial sums
+hipError_t mx_tile(int shape, bool f8, const MxTileArgs& a, int splits, hipStream_t s);
 
 }  // namespace qblk

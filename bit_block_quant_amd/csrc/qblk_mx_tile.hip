@@ -476,21 +476,28 @@ hipError_t go(const MxTileArgs& a, int splits, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tokens of a tile: 256, 128 or 64.
+// kMxTiles.  The tiles of 128 rows leave room for two workgroups a compute unit, which
+// hide each other's ends and barriers.  Of e2m1 activations that takes two stages each;
+// where there is one workgroup a unit anyway it has three (us, two and three stages: 4096 x
+// 4096, 64 tokens, 128 x 64: 12.4, 9.6; 11008 x 4096, 333 tokens, 128 x 128: 21.2, 25.7).
 template <int KIND, bool SPLIT>
-hipError_t by_tokens(int tokens, const MxTileArgs& a, int splits, hipStream_t s) {
-  switch (tokens) {
-    case 64: return go<Shape<4, 1, 2, 2, KIND == kF4 ? 3 : 5, KIND>, SPLIT>(a, splits, s);
-    case 128: return go<Shape<2, 2, 4, 2, KIND == kF4 ? 2 : 4, KIND>, SPLIT>(a, splits, s);
-    default: return go<Shape<4, 2, 2, 4, KIND == kF4 ? 2 : 3, KIND>, SPLIT>(a, splits, s);
+hipError_t by_shape(int shape, const MxTileArgs& a, int splits, hipStream_t s) {
+  constexpr bool f4 = KIND == kF4;
+  const bool many = !f4 || static_cast<int64_t>(a.row_tiles) * a.tok_tiles * splits > cu_count();
+  switch (shape) {
+    case 0: return go<Shape<4, 2, 2, 4, f4 ? 2 : 3, KIND>, SPLIT>(a, splits, s);
+    case 1: return go<Shape<2, 2, 4, 2, f4 ? 2 : 4, KIND>, SPLIT>(a, splits, s);
+    case 2: return go<Shape<4, 1, 2, 2, f4 ? 3 : 5, KIND>, SPLIT>(a, splits, s);
+    case 3: return many ? go<Shape<2, 2, 2, 2, f4 ? 2 : 3, KIND>, SPLIT>(a, splits, s) : go<Shape<2, 2, 2, 2, 3, KIND>, SPLIT>(a, splits, s);
+    default: return many ? go<Shape<2, 1, 2, 2, f4 ? 2 : 4, KIND>, SPLIT>(a, splits, s) : go<Shape<2, 1, 2, 2, f4 ? 3 : 4, KIND>, SPLIT>(a, splits, s);
   }
 }
 
 }  // namespace
 
-hipError_t mx_tile(int tokens, bool f8, const MxTileArgs& a, int splits, hipStream_t s) {
-  if (splits > 1) return f8 ? by_tokens<kF8, true>(tokens, a, splits, s) : by_tokens<kF4, true>(tokens, a, splits, s);
-  return f8 ? by_tokens<kF8, false>(tokens, a, 1, s) : by_tokens<kF4, false>(tokens, a, 1, s);
+hipError_t mx_tile(int shape, bool f8, const MxTileArgs& a, int splits, hipStream_t s) {
+  if (splits > 1) return f8 ? by_shape<kF8, true>(shape, a, splits, s) : by_shape<kF4, true>(shape, a, splits, s);
+  return f8 ? by_shape<kF8, false>(shape, a, 1, s) : by_shape<kF4, false>(shape, a, 1, s);
 }
 
 }  // namespace qblk
