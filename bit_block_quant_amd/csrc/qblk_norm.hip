@@ -6,20 +6,50 @@
 //   codes and scales of y: e4m3 with an fp32 scale per 128 columns, int8 with one
 //   per row, or MXFP8 / MXFP4, each by the rule of its own quantizer
 //
-// The codes are made from the fp32 y: rounding it to 16 bits first would move them.
+// The codes are made from the fp32 y: rounding it to 16 bits first would move them.  For
+// the same reason the squares' partial sums meet in 64 bits and the root's reciprocal is
+// kept as a sum of two fp32 numbers: y is then t * weight, rounded once (16-bit inputs:
+// not at all), times it, rounded once.
+#include <type_traits>
+
 #include "qblk_mx_device.h"
 #include "qblk_norm.h"
 
 namespace qblk {
 namespace {
 
-__device__ __forceinline__ void load_weight(const void* w, int wt, int64_t at, float v[8]) {
-  if (wt == QBLK_F32)
-    load8<QBLK_F32>(w, at, v);
-  else if (wt == QBLK_F16)
-    load8<QBLK_F16>(w, at, v);
-  else
-    load8<QBLK_BF16>(w, at, v);
+// 8 values as they lie in memory: asked for first, made numbers of when they are used
+struct Raw {
+  u32x4 a, b;  // (b: of fp32)
+};
+__device__ __forceinline__ Raw fetch8(const void* x, bool wide, int64_t at) {
+  Raw r;
+  if (wide) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(x) + at);
+    r.a = p[0];
+    r.b = p[1];
+  } else {
+    r.a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + at);
+    r.b = u32x4{0, 0, 0, 0};
+  }
+  return r;
+}
+template <int XT>
+__device__ __forceinline__ void numbers(const Raw& r, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if constexpr (XT == QBLK_F32) {
+      const uint32_t a = r.a[i], b = r.b[i];  // (a bit cast of a vector's element itself takes its first)
+      v[i] = __builtin_bit_cast(float, a);
+      v[4 + i] = __builtin_bit_cast(float, b);
+    } else if constexpr (XT == QBLK_F16) {
+      v[2 * i] = f16_bits_to_f32(r.a[i] & 0xffffu);
+      v[2 * i + 1] = f16_bits_to_f32(r.a[i] >> 16);
+    } else {
+      v[2 * i] = bf16_bits_to_f32(r.a[i]);
+      v[2 * i + 1] = __builtin_bit_cast(float, r.a[i] & 0xffff0000u);
+    }
+  }
 }
 
 // v rounded to the type, and stored there if `to` is given
@@ -33,31 +63,38 @@ __device__ __forceinline__ void round_store(float v[8], void* to, int64_t at) {
   } else {
     uint32_t h[4];
 #pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const u32x2 w = pack16<XT>(float4_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]});
+      h[2 * i] = w.x;
+      h[2 * i + 1] = w.y;
+    }
+#pragma unroll
     for (int i = 0; i < 4; i++) {
-      const uint32_t a = XT == QBLK_F16 ? f32_to_f16_bits(v[2 * i]) : f32_to_bf16_bits(v[2 * i]);
-      const uint32_t b = XT == QBLK_F16 ? f32_to_f16_bits(v[2 * i + 1]) : f32_to_bf16_bits(v[2 * i + 1]);
-      h[i] = a | (b << 16);
-      v[2 * i] = XT == QBLK_F16 ? f16_bits_to_f32(a) : bf16_bits_to_f32(a);
-      v[2 * i + 1] = XT == QBLK_F16 ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
+      v[2 * i] = XT == QBLK_F16 ? f16_bits_to_f32(h[i] & 0xffffu) : bf16_bits_to_f32(h[i]);
+      v[2 * i + 1] = XT == QBLK_F16 ? f16_bits_to_f32(h[i] >> 16) : __builtin_bit_cast(float, h[i] & 0xffff0000u);
     }
     if (to) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(to) + at) = u32x4{h[0], h[1], h[2], h[3]};
   }
 }
 
-// The sum (or, MAX, the largest) over `waves` waves' lanes, in every lane; `part`
-// holds a float for each wave and is free again afterwards.
-template <bool MAX>
-__device__ __forceinline__ float row_total(float v, float* part, int waves, int wave) {
+// The sum (or, MAX, the largest) over `waves` waves' lanes, in every lane; `part` holds
+// a number for each wave and is free again afterwards.
+template <bool MAX, class N>
+__device__ __forceinline__ N row_total(N v, N* part, int waves, int wave) {
+  auto join = [](N a, N b) {
+    if constexpr (MAX)
+      return max_nan(a, b);
+    else
+      return a + b;
+  };
 #pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) {
-    const float o = __shfl_xor(v, m, kWave);
-    v = MAX ? max_nan(v, o) : v + o;
-  }
+  for (int m = 1; m < kWave; m <<= 1) v = join(v, __shfl_xor(v, m, kWave));
   if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) part[wave] = v;
   __syncthreads();
   v = part[0];
-  for (int i = 1; i < waves; i++) v = MAX ? max_nan(v, part[i]) : v + part[i];
+#pragma unroll
+  for (int i = 1; i < waves; i++) v = join(v, part[i]);
   __syncthreads();
   return v;
 }
@@ -67,7 +104,7 @@ __device__ __forceinline__ float row_total(float v, float* part, int waves, int 
 // second time for the output.
 template <int XT, int TH, int V, bool LOOP>
 __global__ __launch_bounds__(TH < 256 ? 256 : TH) void k_rmsnorm(NormArgs p) {
-  __shared__ float part[TH / kWave];
+  __shared__ double part[TH / kWave];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rows = TH < 256 ? 256 / TH : 1;
   const int64_t row = p.row0 + static_cast<int64_t>(blockIdx.x) * rows + (TH < 256 ? wave : 0);
@@ -76,13 +113,16 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void k_rmsnorm(NormArgs p) {
   const int units = p.hidden / 8;
   const int64_t base = row * p.hidden;
 
-  auto fetch = [&](int u, float v[8]) {
-    load8<XT>(p.x, base + 8 * u, v);
-    if (p.residual) {
-      float o[8];
-      load8<XT>(p.residual, base + 8 * u, o);
+  constexpr bool kWide = XT == QBLK_F32;
+  const bool add = p.residual != nullptr;
+  // t of unit u from what was fetched
+  auto total = [&](int u, const Raw& x, const Raw& o, float v[8]) {
+    numbers<XT>(x, v);
+    if (add) {
+      float w[8];
+      numbers<XT>(o, w);
 #pragma unroll
-      for (int i = 0; i < 8; i++) v[i] += o[i];
+      for (int i = 0; i < 8; i++) v[i] += w[i];
       round_store<XT>(v, p.total, base + 8 * u);
     }
   };
@@ -92,115 +132,148 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void k_rmsnorm(NormArgs p) {
     for (int i = 0; i < 8; i++) a = __builtin_fmaf(v[i], v[i], a);
     return a;
   };
+  Raw xr[V], orr[V], wr[V];  // the weights too are asked for before the row's sum is known
+  const Raw none = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+#pragma unroll
+  for (int j = 0; j < V; j++) {
+    const int u = t + j * TH;
+    xr[j] = u < units ? fetch8(p.x, kWide, base + 8 * u) : none;
+  }
+  if (add) {
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+      const int u = t + j * TH;
+      orr[j] = u < units ? fetch8(p.residual, kWide, base + 8 * u) : none;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; j++) {
+    const int u = t + j * TH;
+    wr[j] = u < units ? fetch8(p.weight, p.wt == QBLK_F32, 8 * static_cast<int64_t>(u)) : none;
+  }
   float v[V][8];
-  float sum = 0.0f;
+  float own = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; j++) {
     const int u = t + j * TH;
     if (u < units) {
-      fetch(u, v[j]);
+      total(u, xr[j], orr[j], v[j]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; i++) v[j][i] = 0.0f;
     }
+    own += squares(v[j]);
   }
-#pragma unroll
-  for (int j = 0; j < V; j++) sum += squares(v[j]);
+  double sum = own;
   if constexpr (LOOP) {
     for (int u = t + V * TH; u < units; u += TH) {
       float o[8];
-      fetch(u, o);
+      total(u, fetch8(p.x, kWide, base + 8 * u), add ? fetch8(p.residual, kWide, base + 8 * u) : none, o);
       sum += squares(o);
     }
   }
   sum = row_total<false>(sum, part, TH / kWave, wave);
-  const float r = 1.0f / __builtin_sqrtf(sum / static_cast<float>(p.hidden) + p.eps);
+  const double root = 1.0 / __builtin_sqrt(sum / p.hidden + p.eps);
+  const float r1 = static_cast<float>(root), r2 = static_cast<float>(root - r1);  // (an infinite root: r2 NaN, as 0 * it)
 
-  auto scaled = [&](int u, float a[8]) {
-    float w[8];
-    load_weight(p.weight, p.wt, 8 * static_cast<int64_t>(u), w);
+  // y of N units
+  auto scaled = [&](const Raw* w, float (*a)[8], auto N) {
+    auto by = [&](auto T) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) a[i] = a[i] * r * w[i];
+      for (int j = 0; j < decltype(N)::value; j++) {
+        float f[8];
+        numbers<decltype(T)::value>(w[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const float tw = a[j][i] * f[i];
+          a[j][i] = __builtin_fmaf(tw, r1, tw * r2);
+        }
+      }
+    };
+    if (p.wt == QBLK_F32)
+      by(std::integral_constant<int, QBLK_F32>());
+    else if (p.wt == QBLK_F16)
+      by(std::integral_constant<int, QBLK_F16>());
+    else
+      by(std::integral_constant<int, QBLK_BF16>());
   };
-  const void* const again = p.residual ? p.total : p.x;  // LOOP: this thread's own stores, or x
+  auto largest = [](const float a[8], float top) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) top = max_nan(top, __builtin_fabsf(a[i]));
+    return top;
+  };
+  scaled(wr, v, std::integral_constant<int, V>());
+  // LOOP: unit u again, from this thread's own stores, or x
+  auto again = [&](int u, float a[1][8]) {
+    numbers<XT>(fetch8(add ? p.total : p.x, kWide, base + 8 * u), a[0]);
+    const Raw w = fetch8(p.weight, p.wt == QBLK_F32, 8 * static_cast<int64_t>(u));
+    scaled(&w, a, std::integral_constant<int, 1>());
+  };
   float top = 0.0f;
   if (p.act == QBLK_ACT_I8) {
 #pragma unroll
-    for (int j = 0; j < V; j++) {
-      if (t + j * TH >= units) continue;
-      float a[8];
-#pragma unroll
-      for (int i = 0; i < 8; i++) a[i] = v[j][i];
-      scaled(t + j * TH, a);
-#pragma unroll
-      for (int i = 0; i < 8; i++) top = max_nan(top, __builtin_fabsf(a[i]));
-    }
+    for (int j = 0; j < V; j++) top = t + j * TH < units ? largest(v[j], top) : top;
     if constexpr (LOOP) {
       for (int u = t + V * TH; u < units; u += TH) {
-        float a[8];
-        load8<XT>(again, base + 8 * u, a);
-        scaled(u, a);
-#pragma unroll
-        for (int i = 0; i < 8; i++) top = max_nan(top, __builtin_fabsf(a[i]));
+        float a[1][8];
+        again(u, a);
+        top = largest(a[0], top);
       }
     }
-    top = row_total<true>(top, part, TH / kWave, wave) / 127.0f;
+    top = row_total<true>(top, reinterpret_cast<float*>(part), TH / kWave, wave) / 127.0f;
     if (t == 0) static_cast<float*>(p.scale)[row] = top;
   }
-  // whole waves take part: groups of 16 lanes and quads are on or off together
-  auto emit = [&](int u, float a[8], bool on) {
-    if (on) {
-      scaled(u, a);
-    }
+  // The codes of unit u.  Whole waves take part: groups of 16 lanes and quads are on or off together.
+  auto codes = [&](auto A, int u, float a[8], bool on) {
+    constexpr int act = decltype(A)::value;
     uint32_t c[2];
     const int64_t at = base + 8 * u;
-    switch (p.act) {
-      case QBLK_ACT_F8: {
-        const float s = quant_group(a, c);
-        if (on) {
-          *reinterpret_cast<u32x2*>(p.codes + at) = u32x2{c[0], c[1]};
-          if ((t & 15) == 0) static_cast<float*>(p.scale)[at / kGroup] = s;
-        }
-        break;
-      }
-      case QBLK_ACT_MXFP8: {
-        const uint32_t b = mx_scale<true>(quad_max(top_bits<8>(a)));
-        mx_codes<true, 8>(a, b, c);
-        if (on) {
-          *reinterpret_cast<u32x2*>(p.codes + at) = u32x2{c[0], c[1]};
-          if ((t & 3) == 0) static_cast<uint8_t*>(p.scale)[at / kMxBlock] = static_cast<uint8_t>(b);
-        }
-        break;
-      }
-      case QBLK_ACT_MXFP4: {
-        const uint32_t b = mx_scale<false>(quad_max(top_bits<8>(a)));
-        mx_codes<false, 8>(a, b, c);
-        if (on) {
-          *reinterpret_cast<uint32_t*>(p.codes + at / 2) = c[0];
-          if ((t & 3) == 0) static_cast<uint8_t*>(p.scale)[at / kMxBlock] = static_cast<uint8_t>(b);
-        }
-        break;
-      }
-      case QBLK_ACT_I8: {
-        int n[8];
-        codes8(a, top, -127.0f, 127.0f, n);
+    if constexpr (act == QBLK_ACT_F8) {
+      const float s = quant_group(a, c);
+      if (on && (t & 15) == 0) static_cast<float*>(p.scale)[at / kGroup] = s;
+    } else if constexpr (act == QBLK_ACT_I8) {
+      int n[8];
+      codes8(a, top, -127.0f, 127.0f, n);
 #pragma unroll
-        for (int i = 0; i < 2; i++)
-          c[i] = (n[4 * i] & 255) | ((n[4 * i + 1] & 255) << 8) | ((n[4 * i + 2] & 255) << 16) | (static_cast<uint32_t>(n[4 * i + 3]) << 24);
-        if (on) *reinterpret_cast<u32x2*>(p.codes + at) = u32x2{c[0], c[1]};
-        break;
+      for (int i = 0; i < 2; i++)
+        c[i] = (n[4 * i] & 255) | ((n[4 * i + 1] & 255) << 8) | ((n[4 * i + 2] & 255) << 16) | (static_cast<uint32_t>(n[4 * i + 3]) << 24);
+    } else {
+      const uint32_t b = mx_scale<act == QBLK_ACT_MXFP8>(quad_max(top_bits<8>(a)));
+      mx_codes<act == QBLK_ACT_MXFP8, 8>(a, b, c);
+      if (on && (t & 3) == 0) static_cast<uint8_t*>(p.scale)[at / kMxBlock] = static_cast<uint8_t>(b);
+    }
+    if (!on) return;
+    if constexpr (act == QBLK_ACT_MXFP4)
+      *reinterpret_cast<uint32_t*>(p.codes + at / 2) = c[0];
+    else
+      *reinterpret_cast<u32x2*>(p.codes + at) = u32x2{c[0], c[1]};
+  };
+  auto emit = [&](auto A) {
+#pragma unroll
+    for (int j = 0; j < V; j++) codes(A, t + j * TH, v[j], t + j * TH < units);
+    if constexpr (LOOP) {
+      for (int u0 = V * TH; u0 < units; u0 += TH) {
+        float a[1][8] = {{0, 0, 0, 0, 0, 0, 0, 0}};
+        if (u0 + t < units) again(u0 + t, a);
+        codes(A, u0 + t, a[0], u0 + t < units);
       }
     }
-    if (on && p.y) round_store<XT>(a, p.y, at);
   };
+  switch (p.act) {
+    case QBLK_ACT_F8: emit(std::integral_constant<int, QBLK_ACT_F8>()); break;
+    case QBLK_ACT_I8: emit(std::integral_constant<int, QBLK_ACT_I8>()); break;
+    case QBLK_ACT_MXFP8: emit(std::integral_constant<int, QBLK_ACT_MXFP8>()); break;
+    case QBLK_ACT_MXFP4: emit(std::integral_constant<int, QBLK_ACT_MXFP4>()); break;
+  }
+  if (!p.y) return;
 #pragma unroll
-  for (int j = 0; j < V; j++) emit(t + j * TH, v[j], t + j * TH < units);
+  for (int j = 0; j < V; j++)
+    if (t + j * TH < units) round_store<XT>(v[j], p.y, base + 8 * (t + j * TH));
   if constexpr (LOOP) {
-    for (int u0 = V * TH; u0 < units; u0 += TH) {
-      const int u = u0 + t;
-      float a[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (u < units) load8<XT>(again, base + 8 * u, a);
-      emit(u, a, u < units);
+    for (int u = t + V * TH; u < units; u += TH) {
+      float a[1][8];
+      again(u, a);
+      round_store<XT>(a[0], p.y, base + 8 * u);
     }
   }
 }
@@ -217,14 +290,19 @@ hipError_t norm(const NormArgs& all, int64_t n, hipStream_t s) {
   });
 }
 
+// Few rows: as many threads a row as it has work for; with more rows than fill the card
+// fewer, which wait for each other less (us, rows of 4096 bf16 with a residual, 256 and
+// 512 threads: 1 row 4.8, 3.6; 333 6.9, 5.9; 4096 26.9, 28.4; 1501 rows of 11008, 512 and
+// 1024 threads: 35.5, 42.5).
 template <int XT>
 hipError_t norm_width(const NormArgs& a, int64_t n, hipStream_t s) {
   const int units = a.hidden / 8;
+  const bool few = n <= 4 * cu_count();
   if (units <= 64) return norm<XT, 64, 1, false>(a, n, s);
   if (units <= 256) return norm<XT, 256, 1, false>(a, n, s);
-  if (units <= 512) return norm<XT, 256, 2, false>(a, n, s);
-  if (units <= 1024) return norm<XT, 256, 4, false>(a, n, s);
-  if (units <= 2048) return norm<XT, 1024, 2, false>(a, n, s);
+  if (units <= 512) return few ? norm<XT, 512, 1, false>(a, n, s) : norm<XT, 256, 2, false>(a, n, s);
+  if (units <= 1024) return few ? norm<XT, 512, 2, false>(a, n, s) : norm<XT, 256, 4, false>(a, n, s);
+  if (units <= 2048) return n <= cu_count() ? norm<XT, 1024, 2, false>(a, n, s) : norm<XT, 512, 4, false>(a, n, s);
   return norm<XT, 1024, 4, true>(a, n, s);
 }
 
