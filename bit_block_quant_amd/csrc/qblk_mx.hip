@@ -172,22 +172,6 @@ __device__ __forceinline__ int8v regs8(const u32x4& a, const u32x4& b) {
                static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
 }
 
-// 8 elements with their scale as bf16
-__device__ __forceinline__ bf16x8_n wide4(uint32_t c, float s) {
-  const bf16x2_n p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0);
-  const bf16x2_n p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1);
-  const bf16x2_n p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2);
-  const bf16x2_n p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3);
-  return bf16x8_n{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
-}
-__device__ __forceinline__ bf16x8_n wide8(uint32_t a, uint32_t b, float s) {
-  const bf16x2_n p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, false);
-  const bf16x2_n p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, true);
-  const bf16x2_n p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, false);
-  const bf16x2_n p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, true);
-  return bf16x8_n{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
-}
-
 struct FewArgs {
   const uint8_t* w;
   const uint8_t* ws;
@@ -484,19 +468,9 @@ int64_t few_tokens(int64_t k, bool f8) {
   return n;
 }
 
-// x as codes: as many tokens a launch as fit.
-hipError_t few_product(const FewArgs& all, int64_t n, bool f8, hipStream_t s) {
-  const int64_t most = few_tokens(all.k, f8);
-  for (int64_t t0 = 0; t0 < n; t0 += most) {
-    FewArgs a = all;
-    a.x = static_cast<const uint8_t*>(a.x) + t0 * all.xrow;
-    a.xs += t0 * (all.k / kMxBlock);
-    a.y = static_cast<uint8_t*>(a.y) + t0 * a.m * (a.yt == QBLK_F32 ? 4 : 2);
-    a.n = static_cast<int>(n - t0 < most ? n - t0 : most);
-    const hipError_t e = a.n <= 16 ? few_kind<1, kCodes>(a, f8, s) : few_kind<2, kCodes>(a, f8, s);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+// x as codes; at most few_tokens of them
+hipError_t few_product(const FewArgs& a, bool f8, hipStream_t s) {
+  return a.n <= 16 ? few_kind<1, kCodes>(a, f8, s) : few_kind<2, kCodes>(a, f8, s);
 }
 
 // Whether a product quantizes its x inside every workgroup: that saves a launch, but each
@@ -557,6 +531,27 @@ Plan tile_plan(int64_t m, int64_t k, int64_t n, bool f8) {
   return best;
 }
 
+// Exact sums of e4m3 activations: two shapes, whose stages take twice the time.
+Plan exact_plan(int64_t m, int64_t k, int64_t n) {
+  const int64_t G = padded_row(k, true) / 128, cus = cu_count();
+  Plan best{1, 1, static_cast<int>((G + 3) / 4 * 4), 1e30};
+  for (int i = 1; i < 5; i += 3)
+    for (int want = 1; want <= 16; want++) {
+      const int64_t tiles = tiles_of(m, n, i);
+      if (want > 1 && (tiles * want > 2 * cus || 4 * want >= G + 4)) break;
+      const int64_t per = ((G + want - 1) / want + 3) / 4 * 4;
+      if ((want - 1) * per >= G) continue;
+      const double us = tile_us(tiles, i, 2 * (want == 1 ? G : per), want, n * m, true, cus);
+      if (us < best.us) best = Plan{i, want, static_cast<int>(per), us};
+    }
+  return best;
+}
+// The splits that room is kept for: of either kind of result.
+int most_splits(int64_t m, int64_t k, int64_t n, bool f8) {
+  const int a = tile_plan(m, k, n, f8).splits, b = f8 ? exact_plan(m, k, n).splits : 1;
+  return a > b ? a : b;
+}
+
 // Where an unsplit product's tiles leave much of their last round of compute units
 // empty: the row tiles that fill whole rounds with one shape, and a second launch of the
 // other rows with another.
@@ -614,7 +609,8 @@ hipError_t pad(const uint8_t* x, int64_t n, int64_t row, int64_t padded, uint8_t
 
 hipError_t tile_product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const uint8_t* xq, int64_t xrow,
                         const uint8_t* xs, bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
-  const Plan plan = tile_plan(m, k, n, f8);
+  const bool exact = f8 && yt == QBLK_F32;
+  const Plan plan = exact ? exact_plan(m, k, n) : tile_plan(m, k, n, f8);
   uint8_t* rest = static_cast<uint8_t*>(work);
   const int64_t row = padded_row(k, f8);
   if (xrow != row) {
@@ -641,11 +637,11 @@ hipError_t tile_product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t 
       b.y = static_cast<uint8_t*>(y) + t0 * m * (yt == QBLK_F32 ? 4 : 2);
       b.n = static_cast<int>(left < count * tile.tokens ? left : count * tile.tokens);
       b.tok_tiles = static_cast<int>(count);
-      return mx_tile(shape, f8, b, 1, s);
+      return exact ? mx_tile_exact(shape, b, 1, s) : mx_tile(shape, f8, b, 1, s);
     });
   };
   if (plan.splits == 1) {
-    const Cut cut = tile_cut(plan, m, k, n, f8);
+    const Cut cut = exact ? Cut{0, 0, 0} : tile_cut(plan, m, k, n, f8);
     if (cut.rows == 0) return whole(plan.shape, 0, m);
     const hipError_t e = whole(cut.shape, 0, cut.rows);
     return e == hipSuccess ? whole(cut.rest, cut.rows, m - cut.rows) : e;
@@ -654,15 +650,15 @@ hipError_t tile_product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t 
   a.row_tiles = static_cast<int>((m + tile.rows - 1) / tile.rows);
   a.tok_tiles = static_cast<int>((n + tile.tokens - 1) / tile.tokens);
   log_launch("mx tile f%d m=%lld k=%lld n=%lld tile=%dx%d splits=%d", f8 ? 8 : 4, (long long)m, (long long)k, (long long)n, tile.rows, tile.tokens, plan.splits);
-  const hipError_t e = mx_tile(plan.shape, f8, a, plan.splits, s);
+  const hipError_t e = exact ? mx_tile_exact(plan.shape, a, plan.splits, s) : mx_tile(plan.shape, f8, a, plan.splits, s);
   return e == hipSuccess ? launch_join(a.part, m, n, plan.splits, y, yt, s) : e;
 }
 
 // Y from codes in rows of xrow bytes, by one kernel or the other
 hipError_t product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const uint8_t* xq, int64_t xrow,
                    const uint8_t* xs, bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
-  if (use_few(m, k, n, f8) || (f8 && yt == QBLK_F32))
-    return few_product(FewArgs{w, ws, xq, xs, y, xrow, static_cast<int>(m), static_cast<int>(k), 0, yt, 0}, n, f8, s);
+  if (use_few(m, k, n, f8))
+    return few_product(FewArgs{w, ws, xq, xs, y, xrow, static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt, 0}, f8, s);
   return tile_product(w, ws, m, k, xq, xrow, xs, f8, n, y, yt, work, s);
 }
 
@@ -714,7 +710,7 @@ hipError_t launch_dequant_mx(const uint8_t* codes, const uint8_t* scale, int64_t
 
 int64_t gemm_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
   if (use_few(m, k, n, f8)) return 0;
-  const int splits = tile_plan(m, k, n, f8).splits;
+  const int splits = most_splits(m, k, n, f8);
   return (padded_row(k, f8) != (f8 ? k : k / 2) ? align256(n * padded_row(k, f8)) : 0) + (splits > 1 ? align256(splits * n * part_pitch(m) * 4) : 0);
 }
 
@@ -727,7 +723,7 @@ hipError_t launch_gemm_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int
 int64_t linear_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
   if (fused_quant(n, k)) return 0;
   const bool few = use_few(m, k, n, f8);
-  const int splits = few ? 1 : tile_plan(m, k, n, f8).splits;
+  const int splits = few ? 1 : most_splits(m, k, n, f8);
   return align256(n * (few ? (f8 ? k : k / 2) : padded_row(k, f8))) + align256(n * (k / kMxBlock)) +
          (splits > 1 ? align256(splits * n * part_pitch(m) * 4) : 0);
 }

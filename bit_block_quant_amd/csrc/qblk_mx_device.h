@@ -84,6 +84,22 @@ __device__ __forceinline__ uint32_t mx_codes4(const float v[4], uint32_t b) {
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[2], q[3], 1.0f, 1);
 }
 
+// 8 elements with their scale as bf16
+__device__ __forceinline__ bf16x8_n wide4(uint32_t c, float s) {
+  const bf16x2_n p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0);
+  const bf16x2_n p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1);
+  const bf16x2_n p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2);
+  const bf16x2_n p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3);
+  return bf16x8_n{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+}
+__device__ __forceinline__ bf16x8_n wide8(uint32_t a, uint32_t b, float s) {
+  const bf16x2_n p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, false);
+  const bf16x2_n p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, true);
+  const bf16x2_n p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, false);
+  const bf16x2_n p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, true);
+  return bf16x8_n{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+}
+
 // Four values in 16 bits each, rounded to nearest even by the conversions (v_cvt_pk_bf16_f32
 // for bf16: one operation for two values).
 template <int YT>

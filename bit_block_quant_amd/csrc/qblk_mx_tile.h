@@ -25,6 +25,8 @@ struct MxTile {
 constexpr MxTile kMxTiles[] = {{256, 256}, {256, 128}, {256, 64}, {128, 128}, {128, 64}};
 
 // splits > 1 write partial sums
+// (sums of e4m3 activations exact to fp32 rounding: shapes 1 and 4)
+hipError_t mx_tile_exact(int shape, const MxTileArgs& a, int splits, hipStream_t s);
 hipError_t mx_tile(int shape, bool f8, const MxTileArgs& a, int splits, hipStream_t s);
 
 }  // namespace qblk

@@ -22,8 +22,9 @@ typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
-// What the activations are.
-constexpr int kF4 = 0, kF8 = 1;
+// What the activations are.  kExact: e4m3 with fp32 results, both operands widened to bf16
+// with their scales (k_mx_few says why) and multiplied there, at a quarter of the rate.
+constexpr int kF4 = 0, kF8 = 1, kExact = 2;
 
 // MI x NJ results of 32 x 32 a wave, WM x WN waves, STAGES stages in LDS.
 template <int MI_, int NJ_, int WM_, int WN_, int STAGES_, int KIND_>
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
   // Where this lane's operands lie in a stage: step t's is the first's with 16 t (of
   // e4m3 32 t) exchanged into the address.
   const int wplace = place<S::WRow>(wm * 32 * MI + r, S::Steps * h);
-  const int xplace = S::WBytes + place<S::XRow>(wn * 32 * NJ + r, S::KIND == kF4 ? S::Steps * h : h);
+  const int xplace = S::WBytes + place<S::XRow>(wn * 32 * NJ + r, S::KIND == kF4 ? S::Steps * h : S::KIND == kF8 ? h : 4 * h);
   u32x4 wf[2][MI], xf[2][NJ][S::KIND == kF4 ? 1 : 2];
   auto read = [&](int at, int t, int to) {
 #pragma unroll
@@ -246,9 +247,9 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
     for (int j = 0; j < NJ; j++) {
       if constexpr (S::KIND == kF4) {
         xf[to][j][0] = *reinterpret_cast<const u32x4*>(lds + at + (xplace ^ (16 * t)) + j * 32 * S::XRow);
-      } else {  // the instruction's halves of e4m3: 16 columns of block t, 16 of block 2 + t
+      } else {  // the instruction's halves of e4m3, 16 columns of block t and 16 of block 2 + t; or a whole block
         xf[to][j][0] = *reinterpret_cast<const u32x4*>(lds + at + (xplace ^ (32 * t)) + j * 32 * S::XRow);
-        xf[to][j][1] = *reinterpret_cast<const u32x4*>(lds + at + (xplace ^ (32 * t) ^ 64) + j * 32 * S::XRow);
+        xf[to][j][1] = *reinterpret_cast<const u32x4*>(lds + at + (xplace ^ (32 * t) ^ (S::KIND == kF8 ? 64 : 16)) + j * 32 * S::XRow);
       }
     }
   };
@@ -264,7 +265,7 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
     for (int j = 0; j < NJ; j++) xsc[to][j] = *reinterpret_cast<const uint32_t*>(from + (S::BM + (wn * NJ + j) * 32) * row);
   };
   auto shift_scales = [&](int to) {
-    if constexpr (S::KIND == kF8) {
+    if constexpr (S::KIND != kF4) {
 #pragma unroll
       for (int i = 0; i < MI; i++) wsc[to][i] >>= 16 * h;
 #pragma unroll
@@ -273,6 +274,25 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
   };
   auto multiply = [&](int from, auto T, int sc) {
     constexpr int t = decltype(T)::value;
+    if constexpr (S::KIND == kExact) {
+      auto scale = [](uint32_t v) { return __builtin_bit_cast(float, ((v >> (8 * t)) & 255u) << 23); };
+#pragma unroll
+      for (int g = 0; g < 4; g++) {  // 8 of the block's columns
+        bf16x8_n b[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; j++) {
+          const u32x4 x = xf[from][j][(g >> 1) * (S::KIND == kF4 ? 0 : 1)];
+          b[j] = wide8(x[2 * (g & 1)], x[2 * (g & 1) + 1], scale(xsc[sc][j]));
+        }
+#pragma unroll
+        for (int i = 0; i < MI; i++) {
+          const bf16x8_n a = wide4(wf[from][i][g], scale(wsc[sc][i]));
+#pragma unroll
+          for (int j = 0; j < NJ; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[j], acc[i][j], 0, 0, 0);
+        }
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < MI; i++)
 #pragma unroll
@@ -353,7 +373,7 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
         for (int i = S::Early; i < S::Copies; i++) copy(old, held(g + S::STAGES - 1), i);
       }
       multiply(t & 1, T, set);
-      order<0, MI * NJ, reads, (t == 0 ? S::Copies - S::Early : 0)>();
+      if constexpr (S::KIND != kExact) order<0, MI * NJ, reads, (t == 0 ? S::Copies - S::Early : 0)>();
       pin();
     };
     step(std::integral_constant<int, 0>());
@@ -372,7 +392,7 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
 #pragma unroll
     for (int i = 0; i < S::Early; i++) copy(at, held(g + S::STAGES), i);
     multiply(1, std::integral_constant<int, S::Steps - 1>(), set);
-    order<0, MI * NJ, reads + MI + NJ, S::Early>();
+    if constexpr (S::KIND != kExact) order<0, MI * NJ, reads + MI + NJ, S::Early>();
     pin();
     shift_scales(set ^ 1);
     old = at;
@@ -494,6 +514,13 @@ hipError_t by_shape(int shape, const MxTileArgs& a, int splits, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t mx_tile_exact(int shape, const MxTileArgs& a, int splits, hipStream_t s) {
+  using Wide = Shape<2, 2, 4, 2, 4, kExact>;
+  using Small = Shape<2, 1, 2, 2, 4, kExact>;
+  if (shape == 1) return splits > 1 ? go<Wide, true>(a, splits, s) : go<Wide, false>(a, 1, s);
+  return splits > 1 ? go<Small, true>(a, splits, s) : go<Small, false>(a, 1, s);
+}
 
 hipError_t mx_tile(int shape, bool f8, const MxTileArgs& a, int splits, hipStream_t s) {
   if (splits > 1) return f8 ? by_shape<kF8, true>(shape, a, splits, s) : by_shape<kF4, true>(shape, a, splits, s);
