@@ -326,8 +326,13 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
   // next stage has landed.  Copies past the last stage repeat it.
   auto barrier = [&](auto Newer) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    // those of STAGES - 2 stages stay under way, and the scales' loads behind them
-    __builtin_amdgcn_s_waitcnt(vm_lgkm0((S::STAGES - 2) * S::Copies + decltype(Newer)::value));
+    // those of STAGES - 2 stages stay under way, and the scales' loads behind them (rows
+    // of fewer than 16 blocks have none)
+    constexpr int stay = (S::STAGES - 2) * S::Copies, newer = decltype(Newer)::value;
+    if (newer > 0 && nb < 16)
+      __builtin_amdgcn_s_waitcnt(vm_lgkm0(stay));
+    else
+      __builtin_amdgcn_s_waitcnt(vm_lgkm0(stay + newer));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     __builtin_amdgcn_sched_barrier(0);
