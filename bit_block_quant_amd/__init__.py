@@ -152,7 +152,7 @@ def packed_bytes(fmt, rows, k):
 
 
 def _ptr(t):
-    return t.data_ptr() if t is not None and t.numel() > 0 else None
+    return None if t is None else t.data_ptr()  # (0 of a tensor without elements)
 
 
 # ---------------------------------------------------------------- checks
@@ -187,9 +187,14 @@ def _need(t, name, dtypes=None, min_numel=None, numel=None, ndim=None, dim1=None
     return t.device
 
 
+# 0.1 us; torch.cuda.current_device() takes 0.3, to see first whether there is a GPU (a
+# tensor that passed _need says so)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _need_current(dev):
     """Kernels launch on the current device: the tensors must live there."""
-    cur = torch.cuda.current_device()
+    cur = _current_device()
     if dev.index is not None and dev.index != cur:
         raise ValueError(f"tensors on {dev}, but the current device is cuda:{cur}")
     return cur
