@@ -420,7 +420,8 @@ __global__ __launch_bounds__(WAVES* kWave) void k_mx_few(FewArgs p) {
 // another, or the row tiles do not suffice) and groups for as many waves; else 8 waves,
 // up to three workgroups.  Us, 8 and 16 waves, weights from memory: 4096 x 14336, one
 // token 13.6, 10.6; 22016 x 4096, 16 tokens 21.6, 17.6; but 22016 x 4096, one token 12.3,
-// 15.5; 11008 x 4096, one token 8.5, 9.4; 700 x 1024 3.0, 3.8.
+// 15.5; 11008 x 4096, one token 8.5, 9.4; 700 x 1024 3.0, 3.8.  Three workgroups and two:
+// 14336 x 4096, 4 tokens 11.2, 9.9 (in turns 6 and 4), 22016 x 4096 12.2, 15 (6 and 6).
 struct FewShape {
   int waves, per_cu;
 };
@@ -429,7 +430,10 @@ FewShape few_shape(int64_t m, int k, int64_t n, bool f8) {
   const int64_t lds = few_lds(T, 8, k, n, f8), tiles = (m + 15) / 16;
   const int per_cu = T == 1 && lds <= 53 * 1024 ? 3 : lds <= 80 * 1024 ? 2 : 1;
   const bool room = few_lds(T, 16, k, n, f8) <= kFewLds, one = tiles <= cu_count() || per_cu == 1 || (per_cu == 2 && tiles <= 3 * cu_count());
-  return room && one && k > 8 * kCols ? FewShape{16, 1} : FewShape{8, per_cu};
+  if (room && one && k > 8 * kCols) return FewShape{16, 1};
+  // three workgroups' turns of 16 rows, or two's where those leave much less undone
+  auto turns = [&](int64_t per) { return per * ((tiles + per * cu_count() - 1) / (per * cu_count())); };
+  return FewShape{8, per_cu == 3 && tiles > 3 * cu_count() && 5 * turns(2) < 4 * turns(3) ? 2 : per_cu};
 }
 
 template <int T, int WAVES, bool F8, bool EXACT, int XSRC>
@@ -461,7 +465,7 @@ hipError_t few_kind(const FewArgs& a, bool f8, hipStream_t s) {
 
 // Tokens of one launch: what fits into LDS with x.
 int64_t few_tokens(int64_t k, bool f8) {
-  for (int T = 2; T >= 1; T /= 2)
+  for (int T = f8 ? 1 : 2; T >= 1; T /= 2)
     if (few_lds(T, 8, static_cast<int>(k), 16 * T, f8) <= kFewLds) return 16 * T;
   int64_t n = 15;
   while (n > 0 && few_lds(1, 8, static_cast<int>(k), n, f8) > kFewLds) n--;
@@ -470,7 +474,7 @@ int64_t few_tokens(int64_t k, bool f8) {
 
 // x as codes; at most few_tokens of them
 hipError_t few_product(const FewArgs& a, bool f8, hipStream_t s) {
-  return a.n <= 16 ? few_kind<1, kCodes>(a, f8, s) : few_kind<2, kCodes>(a, f8, s);
+  return a.n <= 16 ? few_kind<1, kCodes>(a, f8, s) : few<2, false, false, kCodes>(a, s);  // (e2m1 only: use_few)
 }
 
 // Whether a product quantizes its x inside every workgroup: that saves a launch, but each
@@ -496,17 +500,21 @@ struct Plan {
   double us;
 };
 
+constexpr int kShapes = sizeof(kMxTiles) / sizeof(kMxTiles[0]);
+// 256 x 128 is e4m3's alone: of e2m1 it was the best at none of the products below.
+constexpr bool has_shape(int shape, bool f8) { return f8 || shape != 1; }
+
 // The time of a shape is estimated from what was measured for it, us: a stage of a
-// workgroup that has a compute unit to itself or (tiles of 128 rows, `both`) shares it,
-// the rest of a workgroup's time, and of a split its join.  Fitted to 1500 times of 96
-// products of either kind (8 matrices, 20 to 4096 tokens, every shape, 1 to 16
-// splits, weights from memory): the choice is 0.6% (e2m1) and 1.1% (e4m3) behind the best
-// form on average, at worst 24% (4096 x 4096, 100 tokens: 11.8 us for 9.5).
+// workgroup that has a compute unit to itself or (the small tiles, `both`) shares it,
+// the rest of a workgroup's time, and of a split its join.  Fitted to 2300 times of 90
+// products of either kind (9 matrices, 20 to 3000 tokens, every shape, 1 to 16
+// splits, weights from memory): the choice is 0.5% (e2m1) and 1.6% (e4m3) behind the best
+// form on average, at worst 18% (11008 x 4096, 160 tokens: 22.5 us for 19.1).
 double tile_us(int64_t tiles, int shape, int64_t per, int64_t splits, int64_t out, bool f8, int64_t cus) {
-  constexpr double both[2][5] = {{1.73, 1.40, 0.74, 1.20, 0.96}, {1.31, 0.82, 0.61, 0.91, 0.65}};
-  constexpr double alone[2][2] = {{0.62, 0.52}, {0.52, 0.365}};
-  constexpr double ends[2][5] = {{3.2, 2.0, 3.6, 2.9, 2.1}, {0.1, 0.5, 1.5, 0.6, 0.5}};
-  constexpr double launch[2] = {1.2, 2.7}, join[2] = {3.6, 3.3}, join_byte[2] = {0.355e-6, 0.414e-6};
+  constexpr double both[2][6] = {{1.68, 1.27, 0.72, 1.16, 0.91, 0.59}, {1.28, 0.76, 0.575, 0.85, 0.60, 0.46}};
+  constexpr double alone[2][3] = {{0.61, 0.505, 0.39}, {0.505, 0.34, 0.29}};
+  constexpr double ends[2][6] = {{2.4, 2.2, 3.45, 2.1, 1.7, 1.0}, {0.8, 1.7, 2.7, 1.1, 1.2, 0.7}};
+  constexpr double launch[2] = {2.1, 2.9}, join[2] = {3.25, 2.9}, join_byte[2] = {0.37e-6, 0.38e-6};
   const int64_t rounds = (tiles * splits + cus - 1) / cus;
   const double one = per * (shape >= 3 ? alone[f8][shape - 3] : both[f8][shape]) + ends[f8][shape], two = per * both[f8][shape] + ends[f8][shape];
   const double work = shape >= 3 ? (rounds / 2) * two + (rounds % 2) * one : rounds * one;
@@ -518,7 +526,8 @@ int64_t tiles_of(int64_t m, int64_t n, int shape) {
 Plan tile_plan(int64_t m, int64_t k, int64_t n, bool f8) {
   const int64_t G = padded_row(k, f8) / 128, cus = cu_count();
   Plan best{0, 1, static_cast<int>((G + 3) / 4 * 4), 1e30};
-  for (int i = 0; i < 5; i++) {
+  for (int i = 0; i < kShapes; i++) {
+    if (!has_shape(i, f8)) continue;
     const int64_t tiles = tiles_of(m, n, i);
     for (int want = 1; want <= 16; want++) {
       if (want > 1 && (tiles * want > 2 * cus || 4 * want >= G + 4)) break;  // (splits are for tiles that leave units idle)
@@ -565,10 +574,12 @@ Cut tile_cut(const Plan& plan, int64_t m, int64_t k, int64_t n, bool f8) {
   const int64_t G = padded_row(k, f8) / 128, cus = cu_count();
   double us = plan.us;
   for (int i = 0; i < 2; i++) {
+    if (!has_shape(i, f8)) continue;
     const int64_t rt = (m + 255) / 256, wide = (n + kMxTiles[i].tokens - 1) / kMxTiles[i].tokens;
     const int64_t rows = rt * wide / cus * cus / wide;
     if (rows <= 0 || rows >= rt) continue;
-    for (int rest = i; rest < 5; rest++) {
+    for (int rest = i; rest < kShapes; rest++) {
+      if (!has_shape(rest, f8)) continue;
       const double c = tile_us(rows * wide, i, G, 1, 0, f8, cus) + tile_us(tiles_of(m - rows * 256, n, rest), rest, G, 1, 0, f8, cus);
       if (c < us) {
         us = c;
@@ -579,14 +590,22 @@ Cut tile_cut(const Plan& plan, int64_t m, int64_t k, int64_t n, bool f8) {
   return best;
 }
 
-// Whether a product runs k_mx_few: up to 16 tokens wherever their codes fit into LDS; up
-// to 32 with few rows (us, few and tiles: 4096 x 4096, 24 tokens, e2m1 7.1, 9.3, e4m3 12.2, 9.3; 32:
-// 9.3, 9.4; 11008 x 4096, 24 tokens, e2m1 12.1, 12.0).
-bool use_few(int64_t m, int64_t k, int64_t n, bool f8) {
+// Whether a product runs k_mx_few: up to 16 tokens, where x leaves room for 16 waves (with
+// 8 alone on a unit the loads in flight are too few) and the rows make few turns of 16 a
+// workgroup; up to 28 tokens where there is one turn.  Us, few and tiles: 8192 x 8192,
+// e4m3, 8 tokens 12.7, 13.9, 12 tokens (no room) 18.9, 14.1; 22016 x 4096, e2m1, 8 tokens
+// 12.5, 13.5, 16 tokens 15.2, 14.0; 11008 x 4096, 16 tokens 9.5, 10.0; 128256 x 4096, 2
+// tokens 55.9, 52.5, e4m3 56.4, 56.4, 8 tokens 62.1, 58.6; 4096 x 4096, e2m1, 28 tokens
+// 6.8, 7.9, 32 8.2, 8.0; e4m3, 20 tokens 8.6, 8.8.  Exact sums, whose tiles take twice the
+// time: wherever the codes fit.
+bool use_few(int64_t m, int64_t k, int64_t n, bool f8, bool exact) {
   if (n > few_tokens(k, f8)) return false;
-  return n <= 16 || (!f8 && n <= 32 && (m + 15) / 16 <= cu_count());
+  if (exact) return n <= 16;
+  const int64_t turns = ((m + 15) / 16 + cu_count() - 1) / cu_count();
+  if (few_lds(n > 16 ? 2 : 1, 16, static_cast<int>(k), n, f8) > kFewLds) return false;
+  if (n > 16) return !f8 && n <= 28 && turns == 1;
+  return turns <= (n > 8 ? 4 : 6) || (f8 && n <= 4);
 }
-
 
 // Rows of x's codes copied into rows of whole stages, zeros behind them: 16 bytes a thread.
 __global__ __launch_bounds__(256) void k_mx_pad(const uint8_t* __restrict__ x, int64_t first, int64_t count, int row, int padded,
@@ -657,7 +676,7 @@ hipError_t tile_product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t 
 // Y from codes in rows of xrow bytes, by one kernel or the other
 hipError_t product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const uint8_t* xq, int64_t xrow,
                    const uint8_t* xs, bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
-  if (use_few(m, k, n, f8))
+  if (use_few(m, k, n, f8, f8 && yt == QBLK_F32))
     return few_product(FewArgs{w, ws, xq, xs, y, xrow, static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt, 0}, f8, s);
   return tile_product(w, ws, m, k, xq, xrow, xs, f8, n, y, yt, work, s);
 }
@@ -708,8 +727,9 @@ hipError_t launch_dequant_mx(const uint8_t* codes, const uint8_t* scale, int64_t
   return f8 ? dequant<true>(codes, scale, rows * (k / 8), out, ot, s) : dequant<false>(codes, scale, rows * (k / 8), out, ot, s);
 }
 
+// Room for either kind of result (what has exact sums runs k_mx_few wherever others do).
 int64_t gemm_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
-  if (use_few(m, k, n, f8)) return 0;
+  if (use_few(m, k, n, f8, false)) return 0;
   const int splits = most_splits(m, k, n, f8);
   return (padded_row(k, f8) != (f8 ? k : k / 2) ? align256(n * padded_row(k, f8)) : 0) + (splits > 1 ? align256(splits * n * part_pitch(m) * 4) : 0);
 }
@@ -722,7 +742,7 @@ hipError_t launch_gemm_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int
 // Codes of x in rows of whole stages where the tile kernel reads them.
 int64_t linear_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
   if (fused_quant(n, k)) return 0;
-  const bool few = use_few(m, k, n, f8);
+  const bool few = use_few(m, k, n, f8, false);
   const int splits = few ? 1 : most_splits(m, k, n, f8);
   return align256(n * (few ? (f8 ? k : k / 2) : padded_row(k, f8))) + align256(n * (k / kMxBlock)) +
          (splits > 1 ? align256(splits * n * part_pitch(m) * 4) : 0);
@@ -732,7 +752,7 @@ hipError_t launch_linear_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, i
                                bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
   if (fused_quant(n, k))
     return fused_product(FewArgs{w, ws, x, nullptr, y, 0, static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt, 0}, xt, f8, s);
-  const bool few = use_few(m, k, n, f8);
+  const bool few = use_few(m, k, n, f8, f8 && yt == QBLK_F32);
   const int64_t row = few ? (f8 ? k : k / 2) : padded_row(k, f8);
   uint8_t* xq = static_cast<uint8_t*>(work);
   uint8_t* xs = xq + align256(n * row);

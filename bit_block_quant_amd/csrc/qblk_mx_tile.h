@@ -22,7 +22,7 @@ struct MxTileArgs {
 struct MxTile {
   int rows, tokens;
 };
-constexpr MxTile kMxTiles[] = {{256, 256}, {256, 128}, {256, 64}, {128, 128}, {128, 64}};
+constexpr MxTile kMxTiles[] = {{256, 256}, {256, 128}, {256, 64}, {128, 128}, {128, 64}, {64, 64}};
 
 // splits > 1 write partial sums
 // (sums of e4m3 activations exact to fp32 rounding: shapes 1 and 4)

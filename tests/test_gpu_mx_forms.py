@@ -74,14 +74,18 @@ def run(q, m, k, n, name, dtype, linear=False):  # noqa: F811
 
 # (m, k, n): rows x tokens of a tile, whole or K split (or rows cut in two launches)
 TILES4 = [(11189, 288, 641), (10993, 14400, 135),  # 256 x 256, split
-          (11029, 288, 321), (11040, 3200, 258), (10991, 11008, 33),  # 256 x 128; 256 x 64, split
-          (258, 1152, 5474), (131, 4128, 1615), (103, 288, 33), (100, 3200, 33),  # one workgroup a unit: 128 x 128, split; 128 x 64, split
-          (1289, 288, 5500), (10916, 14400, 65), (257, 288, 5474), (8526, 6400, 33),  # two: the same
-          (11831, 288, 1540), (3477, 3200, 5400), (4869, 288, 4630), (11992, 288, 1282)]  # cut
-TILES8 = [(11189, 288, 641), (8270, 14400, 129), (11029, 288, 321), (130, 6400, 4175), (11040, 3200, 258), (6438, 11008, 132),
-          (257, 288, 5474), (130, 3200, 2087), (103, 288, 33), (100, 3200, 33),
-          (10414, 1152, 1802), (3477, 3200, 5400), (2845, 1152, 5914), (11177, 416, 1415), (10933, 4128, 662)]
+          (11040, 3200, 258), (10991, 11008, 33),  # 256 x 64, split
+          (10881, 288, 130), (2315, 6400, 65), (11029, 288, 321), (10916, 14400, 65),  # 128 x 128, split; two workgroups a unit
+          (8486, 3200, 65), (4381, 14400, 33), (11354, 288, 259), (5451, 11008, 33),  # 128 x 64, likewise
+          (103, 288, 33), (100, 3200, 33), (258, 1152, 5474), (131, 4128, 1615),  # 64 x 64, split
+          (11831, 288, 1540), (3477, 3200, 5400), (10571, 288, 1564), (6075, 288, 3217), (11992, 288, 1282)]  # cut
+TILES8 = [(11189, 288, 641), (8270, 14400, 129), (11003, 1152, 325), (8277, 6400, 67), (11040, 3200, 258), (6438, 11008, 132),
+          (10881, 288, 130), (2311, 3200, 65), (8416, 1152, 65), (517, 14400, 65), (103, 288, 33), (100, 3200, 33),
+          (11678, 1152, 1685), (3477, 3200, 5400), (7330, 1152, 2327), (10016, 1152, 1552), (7175, 288, 2178), (1421, 4128, 5487),
+          (9369, 3200, 784)]
 EXACT = [(11029, 288, 321), (130, 3200, 2312), (103, 288, 33), (102, 1152, 33)]  # 256 x 128, split; 128 x 64, split
+# few tokens whose codes leave no room, or of many rows
+TILES16 = [(300, 14400, 12), (8200, 8224, 12), (25003, 288, 5), (12805, 1056, 16), (70001, 96, 1)]
 
 
 @pytest.mark.parametrize("m,k,n", TILES4)
@@ -92,6 +96,15 @@ def test_tiles_of_4_bits(q, m, k, n):  # noqa: F811
 @pytest.mark.parametrize("m,k,n", TILES8)
 def test_tiles_of_8_bits(q, m, k, n):  # noqa: F811
     run(q, m, k, n, "mxfp8", ["f16", "bf16"][(m + n) % 2])
+
+
+@pytest.mark.parametrize("name", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("m,k,n", TILES16)
+def test_tiles_of_few_tokens(q, m, k, n, name):  # noqa: F811
+    for dtype in ("f32", "bf16"):
+        run(q, m, k, n, name, dtype)
+        if n > 4:
+            run(q, m, k, n, name, dtype, linear=True)
 
 
 @pytest.mark.parametrize("m,k,n", EXACT)
@@ -110,7 +123,7 @@ def test_tiles_of_every_tail(q, k, name):  # noqa: F811
 
 # (m, k, n): 16 waves or 8, one to three workgroups a compute unit, several turns of 16 rows, 32 tokens
 FEW = [(300, 4096, 1), (4100, 2080, 3), (20003, 1056, 3), (700, 992, 16), (12345, 288, 9), (5003, 8192, 16), (700, 6144, 16),
-       (2000, 1056, 30), (300, 2400, 25), (40001, 512, 2)]
+       (2000, 1056, 28), (300, 2400, 25), (40001, 512, 2), (12805, 288, 4), (12005, 4096, 10), (700, 992, 20)]
 
 
 @pytest.mark.parametrize("name,dtype", [("mxfp4", "f32"), ("mxfp4", "f16"), ("mxfp8", "bf16"), ("mxfp8", "f32")])
