@@ -18,64 +18,51 @@ typedef uint32_t u32x2_a1 __attribute__((ext_vector_type(2), aligned(1)));
 
 // ------------------------------------------------------------ quantizers
 // HBM bound: 2 or 4 bytes read and 17/32 or 33/32 written per value.  A lane takes
-// 8 values, four lanes a block; a workgroup kQuantUnits times 256 lanes' worth,
-// every load before the first use.
-constexpr int kQuantUnits = 4;
-
+// 8 values, four lanes a block, each workgroup 2048 values (us, lanes of 8 and of 32: 64 x 4096 bf16
+// 2.1, 2.8; 4096 x 11008 to e2m1 21.3, 24.4, 5.5 TB/s; 14336 x 4096 fp32 45.9, 49.1, 5.9 TB/s).
 template <int XT, bool F8>
 __global__ __launch_bounds__(256) void k_quant_mx(const void* __restrict__ x, int64_t first, int64_t units,
                                                   uint8_t* __restrict__ codes, uint8_t* __restrict__ scale, int per, int padded) {
   // unit = 8 values; whole quads are on or off together.  padded > 0: rows of `per`
   // units go to rows of `padded` bytes, zeros behind them.
-  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (256 * kQuantUnits) + threadIdx.x;
-  float v[kQuantUnits][8];
+  int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (u >= units) return;
+  u += first;
+  float v[8];
+  load8<XT>(x, u * 8, v);
+  const uint32_t b = mx_scale<F8>(quad_max(top_bits<8>(v)));
+  uint32_t c[2];
+  mx_codes<F8, 8>(v, b, c);
+  constexpr int kBytes = F8 ? 8 : 4;
+  int64_t at = u * kBytes;
+  if (padded > 0) {
+    const int64_t t = u / per;
+    const int in = static_cast<int>(u - t * per);
+    at = t * padded + in * kBytes;
+    if (in < 4)  // the row's first block clears what is behind its last
+      for (int z = per * kBytes + in * 4 * kBytes; z < padded; z += 16 * kBytes) {
 #pragma unroll
-  for (int i = 0; i < kQuantUnits; i++) {
-    const int64_t u = u0 + 256 * i;
-    if (u < units) {
-      load8<XT>(x, (first + u) * 8, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; j++) v[i][j] = 0.0f;
-    }
+        for (int o = 0; o < 4 * kBytes; o += 16) *reinterpret_cast<u32x4*>(codes + t * padded + z + o) = u32x4{0, 0, 0, 0};
+      }
   }
-#pragma unroll
-  for (int i = 0; i < kQuantUnits; i++) {
-    const int64_t u = u0 + 256 * i;
-    const uint32_t b = mx_scale<F8>(quad_max(top_bits<8>(v[i])));
-    uint32_t c[2];
-    mx_codes<F8, 8>(v[i], b, c);
-    if (u >= units) continue;
-    constexpr int kBytes = F8 ? 8 : 4;
-    int64_t at = (first + u) * kBytes;
-    if (padded > 0) {
-      const int64_t t = (first + u) / per;
-      const int in = static_cast<int>(first + u - t * per);
-      at = t * padded + in * kBytes;
-      if (in < 4)  // the row's first block clears what is behind its last
-        for (int b = per * kBytes + in * 4 * kBytes; b < padded; b += 16 * kBytes) {
-#pragma unroll
-          for (int o = 0; o < 4 * kBytes; o += 16) *reinterpret_cast<u32x4*>(codes + t * padded + b + o) = u32x4{0, 0, 0, 0};
-        }
-    }
-    if constexpr (F8)
-      *reinterpret_cast<u32x2*>(codes + at) = u32x2{c[0], c[1]};
-    else
-      *reinterpret_cast<uint32_t*>(codes + at) = c[0];
-    if ((threadIdx.x & 3) == 0) scale[(first + u) / 4] = static_cast<uint8_t>(b);
-  }
+  if constexpr (F8)
+    *reinterpret_cast<u32x2*>(codes + at) = u32x2{c[0], c[1]};
+  else
+    *reinterpret_cast<uint32_t*>(codes + at) = c[0];
+  if ((threadIdx.x & 3) == 0) scale[u / 4] = static_cast<uint8_t>(b);
 }
 
 // ------------------------------------------------------------- the values
 // HBM bound.  A lane takes 8 values: element times scale in fp32 (exact, but for
-// underflow), rounded once to the result's type.
-template <int OT, bool F8>
+// underflow), rounded once to the result's type; UNITS times, every load before the first
+// use (dequant_units).
+template <int OT, bool F8, int UNITS>
 __global__ __launch_bounds__(256) void k_dequant_mx(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scale,
                                                     int64_t first, int64_t units, void* __restrict__ out) {
-  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (256 * kQuantUnits) + threadIdx.x;
-  uint32_t c[kQuantUnits][2], b[kQuantUnits];
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (256 * UNITS) + threadIdx.x;
+  uint32_t c[UNITS][2], b[UNITS];
 #pragma unroll
-  for (int i = 0; i < kQuantUnits; i++) {
+  for (int i = 0; i < UNITS; i++) {
     const int64_t u = first + (u0 + 256 * i < units ? u0 + 256 * i : units - 1);
     if constexpr (F8) {
       const u32x2 w = *reinterpret_cast<const u32x2*>(codes + u * 8);
@@ -87,7 +74,7 @@ __global__ __launch_bounds__(256) void k_dequant_mx(const uint8_t* __restrict__ 
     b[i] = scale[u / 4];
   }
 #pragma unroll
-  for (int i = 0; i < kQuantUnits; i++) {
+  for (int i = 0; i < UNITS; i++) {
     if (u0 + 256 * i >= units) continue;
     const int64_t at = (first + u0 + 256 * i) * 8;
     const float s = mx_scale_value(b[i]);
@@ -683,8 +670,8 @@ hipError_t product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, co
 
 template <bool F8>
 hipError_t quantize(const void* x, int xt, int64_t units, uint8_t* codes, uint8_t* scale, int per, int padded, hipStream_t s) {
-  return in_pieces(units, 256 * kQuantUnits, 256, [&](int64_t u0, int64_t c) {
-    const dim3 grid(static_cast<unsigned>((c + 256 * kQuantUnits - 1) / (256 * kQuantUnits)));
+  return in_pieces(units, 256, 256, [&](int64_t u0, int64_t c) {
+    const dim3 grid(static_cast<unsigned>((c + 255) / 256));
     switch (xt) {
       case QBLK_F32: k_quant_mx<QBLK_F32, F8><<<grid, 256, 0, s>>>(x, u0, c, codes, scale, per, padded); break;
       case QBLK_F16: k_quant_mx<QBLK_F16, F8><<<grid, 256, 0, s>>>(x, u0, c, codes, scale, per, padded); break;
@@ -700,17 +687,29 @@ hipError_t quantize_rows(const void* v, int vt, int64_t rows, int64_t k, bool f8
   return f8 ? quantize<true>(v, vt, rows * per, codes, scale, per, padded, s) : quantize<false>(v, vt, rows * per, codes, scale, per, padded, s);
 }
 
-template <bool F8>
-hipError_t dequant(const uint8_t* codes, const uint8_t* scale, int64_t units, void* out, int ot, hipStream_t s) {
-  return in_pieces(units, 256 * kQuantUnits, 256, [&](int64_t u0, int64_t c) {
-    const dim3 grid(static_cast<unsigned>((c + 256 * kQuantUnits - 1) / (256 * kQuantUnits)));
-    switch (ot) {
-      case QBLK_F32: k_dequant_mx<QBLK_F32, F8><<<grid, 256, 0, s>>>(codes, scale, u0, c, out); break;
-      case QBLK_F16: k_dequant_mx<QBLK_F16, F8><<<grid, 256, 0, s>>>(codes, scale, u0, c, out); break;
-      default: k_dequant_mx<QBLK_BF16, F8><<<grid, 256, 0, s>>>(codes, scale, u0, c, out); break;
-    }
+template <int OT, bool F8, int UNITS>
+hipError_t dequant_go(const uint8_t* codes, const uint8_t* scale, int64_t units, void* out, hipStream_t s) {
+  return in_pieces(units, 256 * UNITS, 256, [&](int64_t u0, int64_t c) {
+    k_dequant_mx<OT, F8, UNITS><<<dim3(static_cast<unsigned>((c + 256 * UNITS - 1) / (256 * UNITS))), 256, 0, s>>>(codes, scale, u0, c, out);
     return hipGetLastError();
   });
+}
+// Four units a lane for much that is written in 16 bits (us, one and four: 14336 x 4096 e2m1
+// to bf16 35.2, 29.6, e4m3 34.1, 33.0; 4096 x 4096 8.8, 9.0; 64 x 4096 2.1, 3.1; to fp32
+// 52.1, 62.8 and 53.7, 68.5, 5.1 TB/s).
+template <int OT, bool F8>
+hipError_t dequant_units(const uint8_t* codes, const uint8_t* scale, int64_t units, void* out, hipStream_t s) {
+  if constexpr (OT != QBLK_F32)
+    if (units > int64_t(1) << 21) return dequant_go<OT, F8, 4>(codes, scale, units, out, s);
+  return dequant_go<OT, F8, 1>(codes, scale, units, out, s);
+}
+template <bool F8>
+hipError_t dequant(const uint8_t* codes, const uint8_t* scale, int64_t units, void* out, int ot, hipStream_t s) {
+  switch (ot) {
+    case QBLK_F32: return dequant_units<QBLK_F32, F8>(codes, scale, units, out, s);
+    case QBLK_F16: return dequant_units<QBLK_F16, F8>(codes, scale, units, out, s);
+    default: return dequant_units<QBLK_BF16, F8>(codes, scale, units, out, s);
+  }
 }
 
 }  // namespace

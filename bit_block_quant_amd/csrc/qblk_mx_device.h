@@ -74,16 +74,6 @@ __device__ __forceinline__ void mx_codes(const float v[N], uint32_t b, uint32_t*
   }
 }
 
-// 4 e2m1 codes: 16 bits
-__device__ __forceinline__ uint32_t mx_codes4(const float v[4], uint32_t b) {
-  const float r = __builtin_bit_cast(float, (254u - (b < 254u ? b : 253u)) << 23);
-  float q[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) q[i] = b == 255u ? 0.0f : __builtin_amdgcn_fmed3f(v[i] * r, -kF4Max, kF4Max);
-  const uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, q[0], q[1], 1.0f, 0);
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[2], q[3], 1.0f, 1);
-}
-
 // 8 elements with their scale as bf16
 __device__ __forceinline__ bf16x8_n wide4(uint32_t c, float s) {
   const bf16x2_n p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0);
