@@ -290,19 +290,21 @@ hipError_t norm(const NormArgs& all, int64_t n, hipStream_t s) {
   });
 }
 
-// Few rows: as many threads a row as it has work for; with more rows than fill the card
-// fewer, which wait for each other less (us, rows of 4096 bf16 with a residual, 256 and
-// 512 threads: 1 row 4.8, 3.6; 333 6.9, 5.9; 4096 26.9, 28.4; 1501 rows of 11008, 512 and
-// 1024 threads: 35.5, 42.5).
+// Few rows: as many threads a row as it has work for; with more rows than compute units
+// fewer, which wait for each other less (us, rows of 4096 bf16, 256 and 512 threads: 1 row with a
+// residual 4.8, 3.6; 300 5.1, 5.1; 1000 8.8, 9.0, without a residual 6.0, 6.6; 1501 rows of
+// 11008, 512 and 1024 threads: 35.5, 42.5).  With a residual a lane's 32 values and as many of
+// it take too many registers (8192 rows of 8192, 256 and 512 threads: 91.2, 84.1; without a
+// residual 43.7, 45.9).
 template <int XT>
 hipError_t norm_width(const NormArgs& a, int64_t n, hipStream_t s) {
   const int units = a.hidden / 8;
-  const bool few = n <= 4 * cu_count();
+  const bool few = n <= cu_count();
   if (units <= 64) return norm<XT, 64, 1, false>(a, n, s);
   if (units <= 256) return norm<XT, 256, 1, false>(a, n, s);
   if (units <= 512) return few ? norm<XT, 512, 1, false>(a, n, s) : norm<XT, 256, 2, false>(a, n, s);
-  if (units <= 1024) return few ? norm<XT, 512, 2, false>(a, n, s) : norm<XT, 256, 4, false>(a, n, s);
-  if (units <= 2048) return n <= cu_count() ? norm<XT, 1024, 2, false>(a, n, s) : norm<XT, 512, 4, false>(a, n, s);
+  if (units <= 1024) return a.residual || n <= 4 * cu_count() ? norm<XT, 512, 2, false>(a, n, s) : norm<XT, 256, 4, false>(a, n, s);
+  if (units <= 2048) return few ? norm<XT, 1024, 2, false>(a, n, s) : norm<XT, 512, 4, false>(a, n, s);
   return norm<XT, 1024, 4, true>(a, n, s);
 }
 
