@@ -465,8 +465,13 @@ hipError_t few_product(const FewArgs& a, bool f8, hipStream_t s) {
 }
 
 // Whether a product quantizes its x inside every workgroup: that saves a launch, but each
-// of them does it again.
-bool fused_quant(int64_t n, int64_t k) { return n <= 4 && n * k <= 32768; }  // (always fits into LDS)
+// of them does it again, up to 8 tokens where they are few (us, in two launches and in one,
+// e4m3: 4096 x 4096, 1 token 6.6, 4.8, 4 tokens 6.6, 5.4, 8 tokens 7.6, 6.9; 2048 x 2048, 8
+// tokens 5.7, 4.5, 16 tokens 6.7, 6.9; 22016 x 4096, 1 token 14.6, 11.7, 8 tokens 17.3, 18.9;
+// 4096 x 14336, 4 tokens 12.3, 13.7).  Such an x always fits into LDS.
+bool fused_quant(int64_t m, int64_t n, int64_t k) {
+  return n * k <= 32768 && (n <= 4 || (n <= 8 && (m + 15) / 16 <= cu_count()));
+}
 
 hipError_t fused_product(const FewArgs& a, int xt, bool f8, hipStream_t s) {
   switch (xt) {
@@ -740,7 +745,7 @@ hipError_t launch_gemm_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int
 
 // Codes of x in rows of whole stages where the tile kernel reads them.
 int64_t linear_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
-  if (fused_quant(n, k)) return 0;
+  if (fused_quant(m, n, k)) return 0;
   const bool few = use_few(m, k, n, f8, false);
   const int splits = few ? 1 : most_splits(m, k, n, f8);
   return align256(n * (few ? (f8 ? k : k / 2) : padded_row(k, f8))) + align256(n * (k / kMxBlock)) +
@@ -749,7 +754,7 @@ int64_t linear_mxfp4_workspace(int64_t m, int64_t k, int64_t n, bool f8) {
 
 hipError_t launch_linear_mxfp4(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t k, const void* x, int xt,
                                bool f8, int64_t n, void* y, int yt, void* work, hipStream_t s) {
-  if (fused_quant(n, k))
+  if (fused_quant(m, n, k))
     return fused_product(FewArgs{w, ws, x, nullptr, y, 0, static_cast<int>(m), static_cast<int>(k), static_cast<int>(n), yt, 0}, xt, f8, s);
   const bool few = use_few(m, k, n, f8, f8 && yt == QBLK_F32);
   const int64_t row = few ? (f8 ? k : k / 2) : padded_row(k, f8);

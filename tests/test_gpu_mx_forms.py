@@ -123,14 +123,15 @@ def test_tiles_of_every_tail(q, k, name):  # noqa: F811
 
 # (m, k, n): 16 waves or 8, one to three workgroups a compute unit, several turns of 16 rows, 32 tokens
 FEW = [(300, 4096, 1), (4100, 2080, 3), (20003, 1056, 3), (700, 992, 16), (12345, 288, 9), (5003, 8192, 16), (700, 6144, 16),
-       (2000, 1056, 28), (300, 2400, 25), (40001, 512, 2), (12805, 288, 4), (12005, 4096, 10), (700, 992, 20)]
+       (2000, 1056, 28), (300, 2400, 25), (40001, 512, 2), (12805, 288, 4), (12005, 4096, 10), (700, 992, 20),
+       (4000, 4096, 8), (300, 2080, 6)]
 
 
 @pytest.mark.parametrize("name,dtype", [("mxfp4", "f32"), ("mxfp4", "f16"), ("mxfp8", "bf16"), ("mxfp8", "f32")])
 @pytest.mark.parametrize("m,k,n", FEW)
 def test_few_tokens(q, m, k, n, name, dtype):  # noqa: F811
     run(q, m, k, n, name, dtype)
-    if n <= 4:
+    if n <= 8:
         run(q, m, k, n, name, dtype, linear=True)
 
 
