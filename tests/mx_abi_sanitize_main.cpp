@@ -72,7 +72,7 @@ int main() {
   uint8_t* const S = buf + 1025;  // scales of blocks: any byte
   float* const S4 = reinterpret_cast<float*>(buf + 1028);
   void* const B = buf + 2048;
-  void* const Y = buf + 3072;
+  void* const Y = buf + 5120;
   void* const W = buf + 4096;
   void* const MIS = buf + 8;
   const int64_t kMax = (int64_t(1) << 31) - 1;
