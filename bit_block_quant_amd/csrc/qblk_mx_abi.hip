@@ -147,6 +147,10 @@ qblk_status_t qblk_rmsnorm(const qblk_rmsnorm_t* a, qblk_stream_t stream) {
     else
       QBLK_TRY(check_ptr4(a->scale, work));
   }
+  if (a->act == QBLK_ACT_I8 && a->hidden == 0 && a->n > 0) {  // rows without columns: scales of 0
+    QBLK_TRY(check_ptr4(a->scale, true));
+    return from_hip(qblk::launch_zero_bytes(a->scale, a->n * 4, static_cast<hipStream_t>(stream)));
+  }
   if (!work) return QBLK_OK;
   qblk::NormArgs k;
   k.x = a->x;

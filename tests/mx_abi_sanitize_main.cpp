@@ -210,6 +210,10 @@ int main() {
     LAUNCHES(qblk_rmsnorm(&c, s), "rmsnorm", 3);
     c.hidden = 52;
     REJECTS(qblk_rmsnorm(&c, s), QBLK_ERR_SHAPE);
+    c.hidden = 0;  // rows without columns have a scale each
+    LAUNCHES(qblk_rmsnorm(&c, s), "zero", 12);
+    c.scale = nullptr;
+    REJECTS(qblk_rmsnorm(&c, s), QBLK_ERR_NULL);
   }
   if (g_fail == 0) printf("clean\n");
   return g_fail != 0;

@@ -195,6 +195,17 @@ def test_narrow_norms(q, h):  # noqa: F811
         assert torch.all((y.double() - ref).abs() <= D * ref.abs())
 
 
+def test_norm_without_columns(q):  # noqa: F811
+    """As quantize_act_i8 of no columns: a scale of 0 for each row."""
+    x, w = torch.empty(3, 0, device="cuda"), torch.empty(0, device="cuda")
+    scale = torch.full((3,), 7.0, device="cuda")
+    q.rmsnorm(x, w, quant=q.ACT_I8, scale=scale)
+    assert torch.equal(scale, q.quantize_act_i8(x)[1]) and torch.equal(scale, torch.zeros(3, device="cuda"))
+    for quant in (None, q.ACT_F8, q.ACT_MXFP8, q.ACT_MXFP4):
+        r = q.rmsnorm(x, w, x, quant=quant, y=True)
+        assert r.y.shape == (3, 0) and r.total.shape == (3, 0)
+
+
 # ------------------------------------------------------------ past 2^32 bytes
 def test_weights_past_32_bits(q):  # noqa: F811
     """4.3e9 bytes of codes: few tokens and many, rows at both ends and at 2^32 bytes."""
