@@ -360,6 +360,7 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
     for (int i = 0; i < S::ScaleLoads; i++) sv[i] = few_scales(sp[i] + so[i], in_row, nb);
   }
   put_scales(0, g0);
+  __builtin_amdgcn_s_waitcnt(vm_lgkm0(0));  // (a barrier alone does not promise that copies to LDS have landed)
   __syncthreads();
   read_scales(0, 0, 0);
   shift_scales(0);
@@ -417,6 +418,7 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
     if (g + 3 < g1) stage(g + 3, std::integral_constant<int, 3>());
     group ^= 1;
   }
+  __builtin_amdgcn_s_waitcnt(vm_lgkm0(0));
   __syncthreads();  // the last copies have landed: LDS may be used again, and left
 
   // Lane (r, h) holds token r and rows 8 (e >> 2) + 4 h + (e & 3) of each 32 x 32.  32
