@@ -168,10 +168,11 @@ def _need(t, name, dtypes=None, min_numel=None, numel=None, ndim=None, dim1=None
     every other argument of the call lives on (None for the first one)."""
     if not isinstance(t, torch.Tensor) and not hasattr(t, "is_cuda"):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    dev = t.device
     if not t.is_cuda:
-        raise ValueError(f"{name}: must be a GPU tensor (got device {t.device})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the other arguments on {device}")
+        raise ValueError(f"{name}: must be a GPU tensor (got device {dev})")
+    if device is not None and dev != device:
+        raise ValueError(f"{name}: on {dev}, the other arguments on {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous (the kernels index it as a dense row-major array)")
     if dtypes is not None and t.dtype not in dtypes:
@@ -184,7 +185,7 @@ def _need(t, name, dtypes=None, min_numel=None, numel=None, ndim=None, dim1=None
         raise ValueError(f"{name}: expected {numel} elements, got {t.numel()}")
     if min_numel is not None and t.numel() < min_numel:
         raise ValueError(f"{name}: holds {t.numel()} elements, the call needs {min_numel}")
-    return t.device
+    return dev
 
 
 # 0.1 us; torch.cuda.current_device() takes 0.3, to see first whether there is a GPU (a
