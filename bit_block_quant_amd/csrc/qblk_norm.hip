@@ -7,9 +7,9 @@
 //   per row, or MXFP8 / MXFP4, each by the rule of its own quantizer
 //
 // The codes are made from the fp32 y: rounding it to 16 bits first would move them.  For
-// the same reason the squares' partial sums meet in 64 bits and the root's reciprocal is
-// kept as a sum of two fp32 numbers: y is then t * weight, rounded once (16-bit inputs:
-// not at all), times it, rounded once.
+// the same reason the squares, eight at a time in fp32, are added up in 64 bits and the root's
+// reciprocal is kept as a sum of two fp32 numbers: y is then t * weight, rounded once (16-bit
+// inputs: not at all), times it.
 #include <type_traits>
 
 #include "qblk_mx_device.h"
@@ -77,25 +77,55 @@ __device__ __forceinline__ void round_store(float v[8], void* to, int64_t at) {
   }
 }
 
-// The sum (or, MAX, the largest) over `waves` waves' lanes, in every lane; `part` holds
-// a number for each wave and is free again afterwards.
-template <bool MAX, class N>
-__device__ __forceinline__ N row_total(N v, N* part, int waves, int wave) {
-  auto join = [](N a, N b) {
-    if constexpr (MAX)
-      return max_nan(a, b);
-    else
-      return a + b;
-  };
+// The row's sum from its threads' sums of eight squares, in every lane.  How many threads a
+// row has goes by the number of rows (norm_width), what is added to what does not: rows of
+// one width are taken by 2 TH threads with V / 2 units each or by TH with V (HALF), whose
+// thread t stands for t and t + TH of the others.  Its two sums are joined over the lanes apart,
+// as two waves would (the lower half of the lanes takes on the one, the upper the other), and
+// meet as those waves' do behind the barrier.
+template <int WAVES, int V, bool HALF>
+__device__ __forceinline__ double row_sum(const double own[V], double* part, int wave) {
+  const int lane = threadIdx.x & 63;
+  double v = own[0];
+  if constexpr (HALF) {
+    double w = own[1];
 #pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) v = join(v, __shfl_xor(v, m, kWave));
+    for (int j = 2; j < V; j += 2) {
+      v += own[j];
+      w += own[j + 1];
+    }
+    const double give = lane & 32 ? v : w;
+    v = (lane & 32 ? w : v) + __shfl_xor(give, 32, kWave);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor(v, m, kWave);
+    v += __shfl_xor(v, 32, kWave);
+  } else {
+#pragma unroll
+    for (int j = 1; j < V; j++) v += own[j];
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, kWave);
+  }
+  if constexpr (WAVES > 1) {
+    if (lane == 0) part[wave] = v;
+    __syncthreads();
+    auto pair = [&](int i) { return HALF ? part[i] : part[i] + part[i + WAVES / 2]; };
+    v = pair(0);
+#pragma unroll
+    for (int i = 1; i < (HALF ? WAVES : WAVES / 2); i++) v += pair(i);
+  }
+  return v;
+}
+
+// The largest (NaN if one is) over `waves` waves' lanes, in every lane.
+__device__ __forceinline__ float row_max(float v, float* part, int waves, int wave) {
+#pragma unroll
+  for (int m = 1; m < kWave; m <<= 1) v = max_nan(v, __shfl_xor(v, m, kWave));
   if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) part[wave] = v;
   __syncthreads();
   v = part[0];
 #pragma unroll
-  for (int i = 1; i < waves; i++) v = join(v, part[i]);
-  __syncthreads();
+  for (int i = 1; i < waves; i++) v = max_nan(v, part[i]);
   return v;
 }
 
@@ -105,9 +135,10 @@ __device__ __forceinline__ N row_total(N v, N* part, int waves, int wave) {
 // One row by TH threads, V units of 8 values each (unit t, t + TH, ...); rows
 // of one wave: four to a workgroup.  Rows wider than 8 TH V values (LOOP) are read a
 // second time for the output.
-template <int XT, int TH, int V, bool LOOP>
+template <int XT, int TH, int V, bool HALF, bool LOOP>
 __global__ __launch_bounds__(TH < 256 ? 256 : TH) void k_rmsnorm(NormArgs p) {
   __shared__ double part[TH / kWave];
+  __shared__ float part_max[TH / kWave];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rows = TH < 256 ? 256 / TH : 1;
   const int64_t row = p.row0 + static_cast<int64_t>(blockIdx.x) * rows + (TH < 256 ? wave : 0);
@@ -155,7 +186,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void k_rmsnorm(NormArgs p) {
     wr[j] = u < units ? fetch8(p.weight, p.wt == QBLK_F32, 8 * static_cast<int64_t>(u)) : none;
   }
   float v[V][8];
-  float own = 0.0f;
+  double own[V];
 #pragma unroll
   for (int j = 0; j < V; j++) {
     const int u = t + j * TH;
@@ -165,17 +196,16 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void k_rmsnorm(NormArgs p) {
 #pragma unroll
       for (int i = 0; i < 8; i++) v[j][i] = 0.0f;
     }
-    own += squares(v[j]);
+    own[j] = squares(v[j]);
   }
-  double sum = own;
   if constexpr (LOOP) {
     for (int u = t + V * TH; u < units; u += TH) {
       float o[8];
       total(u, fetch8(p.x, kWide, base + 8 * u), add ? fetch8(p.residual, kWide, base + 8 * u) : none, o);
-      sum += squares(o);
+      own[0] += squares(o);
     }
   }
-  sum = row_total<false>(sum, part, TH / kWave, wave);
+  const double sum = row_sum<TH / kWave, V, HALF>(own, part, wave);
   const double root = 1.0 / __builtin_sqrt(sum / p.hidden + p.eps);
   const float r1 = static_cast<float>(root), r2 = static_cast<float>(root - r1);  // (an infinite root: r2 NaN, as 0 * it)
 
@@ -223,7 +253,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void k_rmsnorm(NormArgs p) {
         top = largest(a[0], top);
       }
     }
-    top = row_total<true>(top, reinterpret_cast<float*>(part), TH / kWave, wave) / 127.0f;
+    top = row_max(top, part_max, TH / kWave, wave) / 127.0f;
     if (t == 0) static_cast<float*>(p.scale)[row] = top;
   }
   // The codes of unit u.  Whole waves take part: groups of 16 lanes and quads are on or off together.
@@ -281,14 +311,14 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void k_rmsnorm(NormArgs p) {
   }
 }
 
-template <int XT, int TH, int V, bool LOOP>
+template <int XT, int TH, int V, bool HALF, bool LOOP = false>
 hipError_t norm(const NormArgs& all, int64_t n, hipStream_t s) {
   constexpr int rows = TH < 256 ? 256 / TH : 1, threads = TH < 256 ? 256 : TH;
   return in_pieces(n, rows, threads, [&](int64_t r0, int64_t c) {
     NormArgs a = all;
     a.row0 = r0;
     a.end = r0 + c;
-    k_rmsnorm<XT, TH, V, LOOP><<<dim3(static_cast<unsigned>((c + rows - 1) / rows)), threads, 0, s>>>(a);
+    k_rmsnorm<XT, TH, V, HALF, LOOP><<<dim3(static_cast<unsigned>((c + rows - 1) / rows)), threads, 0, s>>>(a);
     return hipGetLastError();
   });
 }
@@ -305,10 +335,10 @@ hipError_t norm_width(const NormArgs& a, int64_t n, hipStream_t s) {
   const bool few = n <= cu_count();
   if (units <= 64) return norm<XT, 64, 1, false>(a, n, s);
   if (units <= 256) return norm<XT, 256, 1, false>(a, n, s);
-  if (units <= 512) return few ? norm<XT, 512, 1, false>(a, n, s) : norm<XT, 256, 2, false>(a, n, s);
-  if (units <= 1024) return a.residual || n <= 4 * cu_count() ? norm<XT, 512, 2, false>(a, n, s) : norm<XT, 256, 4, false>(a, n, s);
-  if (units <= 2048) return few ? norm<XT, 1024, 2, false>(a, n, s) : norm<XT, 512, 4, false>(a, n, s);
-  return norm<XT, 1024, 4, true>(a, n, s);
+  if (units <= 512) return few ? norm<XT, 512, 1, false>(a, n, s) : norm<XT, 256, 2, true>(a, n, s);
+  if (units <= 1024) return a.residual || n <= 4 * cu_count() ? norm<XT, 512, 2, false>(a, n, s) : norm<XT, 256, 4, true>(a, n, s);
+  if (units <= 2048) return few ? norm<XT, 1024, 2, false>(a, n, s) : norm<XT, 512, 4, true>(a, n, s);
+  return norm<XT, 1024, 4, false, true>(a, n, s);
 }
 
 }  // namespace

@@ -471,7 +471,8 @@ qblk_status_t qblk_linear_mxfp4(const uint8_t* w, const uint8_t* wscale,
  * overlap any input or one another.  weight has `hidden` values of type wt in
  * {F32, F16, BF16}; eps >= 0 (QBLK_ERR_SHAPE).  Squares are fp32: |t| and |t * weight|
  * have to stay below 1.8e19, and with eps = 0 a row's root mean square above 1e-18; a row
- * of zeros with eps = 0 gives NaN.  hidden at most 2^24. */
+ * of zeros with eps = 0 gives NaN.  A row's results do not depend on the rows beside it.
+ * hidden at most 2^24. */
 typedef struct {
   int64_t n, hidden;
   const void* x;
