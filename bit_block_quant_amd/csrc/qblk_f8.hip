@@ -9,6 +9,7 @@
 //
 // A scale covers 128 columns on both sides, so the inner sum over a group is
 // formed on the matrix cores from the bare codes and scaled once, in fp32.
+#include "qblk_lds.h"
 #include "qblk_quant_device.h"
 
 namespace qblk {
@@ -839,9 +840,8 @@ hipError_t few(const uint8_t* w, const float* ws, int64_t m, int64_t k, const Fe
   const size_t G = static_cast<size_t>(k / kGroup);
   const size_t lds = static_cast<size_t>(WAVES) * few_region(T, NR) +
                      (XSRC == kCodes ? 0 : (n * G * 4 + 15) / 16 * 16 + n * (static_cast<size_t>(k) + 16));
-  static const hipError_t allowed =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(k_f8_few<T, NR, WAVES, GATE, XSRC>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+  static std::atomic<uint64_t> done{0};
+  const hipError_t allowed = allow_lds(done, reinterpret_cast<const void*>(k_f8_few<T, NR, WAVES, GATE, XSRC>), 128 * 1024);
   if (allowed != hipSuccess) return allowed;
   log_launch("f8 few%s rows=%lld k=%lld n=%lld T=%d NR=%d waves=%d x=%d lds=%zu", GATE ? " gate" : "", (long long)m,
              (long long)k, (long long)n, T, NR, WAVES, XSRC, lds);
@@ -948,8 +948,8 @@ Cut tile_cut(const Plan& plan, int64_t m, int64_t k, int64_t n, bool exact) {
 template <int NT, bool GATE, bool SPLIT, bool EXACT>
 hipError_t tile_go(const TileArgs& a, int splits, hipStream_t s) {
   constexpr size_t lds = sizeof(TileLds<NT>);
-  static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(k_f8_tile<NT, GATE, SPLIT, EXACT>),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  static std::atomic<uint64_t> done{0};
+  const hipError_t allowed = allow_lds(done, reinterpret_cast<const void*>(k_f8_tile<NT, GATE, SPLIT, EXACT>), lds);
   if (allowed != hipSuccess) return allowed;
   k_f8_tile<NT, GATE, SPLIT, EXACT><<<dim3(static_cast<unsigned>(a.row_tiles * a.tok_tiles), static_cast<unsigned>(splits)),
                                      512, lds, s>>>(a);

@@ -7,6 +7,7 @@
 //
 // The matrix cores take both scales with the codes: in a K = 128 instruction a
 // lane holds 32 columns, which is one block, and its scales.
+#include "qblk_lds.h"
 #include "qblk_mx_device.h"
 #include "qblk_mx_tile.h"
 
@@ -428,8 +429,8 @@ FewShape few_shape(int64_t m, int k, int64_t n, bool f8) {
 template <int T, int WAVES, bool F8, bool EXACT, int XSRC>
 hipError_t few_go(FewArgs a, int per_cu, hipStream_t s) {
   const size_t lds = static_cast<size_t>(few_lds(T, WAVES, a.k, a.n, F8));
-  static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx_few<T, WAVES, F8, EXACT, XSRC>),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, kFewLds);
+  static std::atomic<uint64_t> done{0};
+  const hipError_t allowed = allow_lds(done, reinterpret_cast<const void*>(k_mx_few<T, WAVES, F8, EXACT, XSRC>), kFewLds);
   if (allowed != hipSuccess) return allowed;
   const int64_t most = static_cast<int64_t>(cu_count()) * per_cu, tiles = (static_cast<int64_t>(a.m) + 15) / 16;
   a.rows = static_cast<int>(tiles <= most ? 16 : (a.m + most - 1) / most);

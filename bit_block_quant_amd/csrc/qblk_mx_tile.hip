@@ -16,6 +16,7 @@
 // SIMDs, so wide tiles where there are enough of them.
 #include <type_traits>
 
+#include "qblk_lds.h"
 #include "qblk_mx_device.h"
 #include "qblk_mx_tile.h"
 
@@ -503,8 +504,8 @@ __global__ __launch_bounds__(S::THREADS) void k_mx_tile(MxTileArgs p) {
 
 template <class S, bool SPLIT>
 hipError_t go(const MxTileArgs& a, int splits, hipStream_t s) {
-  static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx_tile<S, SPLIT>),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, S::Lds);
+  static std::atomic<uint64_t> done{0};
+  const hipError_t allowed = allow_lds(done, reinterpret_cast<const void*>(k_mx_tile<S, SPLIT>), S::Lds);
   if (allowed != hipSuccess) return allowed;
   k_mx_tile<S, SPLIT><<<dim3(static_cast<unsigned>(a.row_tiles * a.tok_tiles), static_cast<unsigned>(splits)), S::THREADS, S::Lds, s>>>(a);
   return hipGetLastError();
