@@ -641,8 +641,6 @@ hipError_t tile_product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t 
     const MxTile tile = kMxTiles[shape];
     a.first_row_tile = static_cast<int>(first / tile.rows);
     a.row_tiles = static_cast<int>((rows + tile.rows - 1) / tile.rows);
-    log_launch("mx tile f%d m=%lld k=%lld n=%lld rows=%lld+%lld tile=%dx%d", f8 ? 8 : 4, (long long)m, (long long)k, (long long)n,
-               (long long)first, (long long)rows, tile.rows, tile.tokens);
     // in pieces of the tokens: a launch of 2^23 tiles would pass 32 bits of threads
     return in_pieces((n + tile.tokens - 1) / tile.tokens, 1, 512 * static_cast<int64_t>(a.row_tiles), [&](int64_t tt, int64_t count) {
       const int64_t t0 = tt * tile.tokens, left = n - t0;
@@ -664,7 +662,6 @@ hipError_t tile_product(const uint8_t* w, const uint8_t* ws, int64_t m, int64_t 
   const MxTile tile = kMxTiles[plan.shape];
   a.row_tiles = static_cast<int>((m + tile.rows - 1) / tile.rows);
   a.tok_tiles = static_cast<int>((n + tile.tokens - 1) / tile.tokens);
-  log_launch("mx tile f%d m=%lld k=%lld n=%lld tile=%dx%d splits=%d", f8 ? 8 : 4, (long long)m, (long long)k, (long long)n, tile.rows, tile.tokens, plan.splits);
   const hipError_t e = exact ? mx_tile_exact(plan.shape, a, plan.splits, s) : mx_tile(plan.shape, f8, a, plan.splits, s);
   return e == hipSuccess ? launch_join(a.part, m, n, plan.splits, y, yt, s) : e;
 }

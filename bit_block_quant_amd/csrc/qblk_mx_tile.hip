@@ -507,6 +507,8 @@ hipError_t go(const MxTileArgs& a, int splits, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
   const hipError_t allowed = allow_lds(done, reinterpret_cast<const void*>(k_mx_tile<S, SPLIT>), S::Lds);
   if (allowed != hipSuccess) return allowed;
+  log_launch("mx tile %s %dx%d stages=%d%s m=%d k=%d n=%d tiles=%dx%d from=%d splits=%d", S::KIND == kF4 ? "f4" : S::KIND == kF8 ? "f8" : "exact",
+             S::BM, S::BN, S::STAGES, SPLIT ? " split" : "", a.m, a.k, a.n, a.row_tiles, a.tok_tiles, a.first_row_tile, splits);
   k_mx_tile<S, SPLIT><<<dim3(static_cast<unsigned>(a.row_tiles * a.tok_tiles), static_cast<unsigned>(splits)), S::THREADS, S::Lds, s>>>(a);
   return hipGetLastError();
 }
