@@ -601,13 +601,12 @@ def _need_mxfp4(codes, scale, name, device=None):
 def _need_mx(codes, scale, name, device=None):
     """MX codes of either kind with their scales; returns (device, rows, k, kind).  Bytes
     (uint8) are MXFP4 pairs, float8_e4m3fn MXFP8."""
-    if getattr(codes, "dtype", None) == torch.uint8:
-        return _need_mxfp4(codes, scale, name, device) + (ACT_MXFP4,)
     dev = _need(codes, name, (torch.uint8, F8), ndim=2, device=device)
-    rows, k = codes.shape
+    kind = ACT_MXFP4 if codes.dtype == torch.uint8 else ACT_MXFP8
+    rows, k = codes.shape[0], codes.shape[1] * (2 if kind == ACT_MXFP4 else 1)
     _mx_cols(k, name)
     _need(scale, f"{name} scale", _E8M0_IN, numel=rows * (k // 32), device=dev)
-    return dev, rows, k, ACT_MXFP8
+    return dev, rows, k, kind
 
 
 def _codes_like(act, n, k):

@@ -18,16 +18,11 @@ namespace {
 constexpr int kMxBlock = 32;
 constexpr float kF4Max = 6.0f;
 
-// the largest of 4 or 8 neighbouring lanes, in each of them (as bits: a NaN is above infinity)
+// the largest of 4 neighbouring lanes, in each of them (as bits: a NaN is above infinity)
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0xB1, 0xF, 0xF, true));
   v = v > o ? v : o;
   o = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xF, 0xF, true));
-  return v > o ? v : o;
-}
-__device__ __forceinline__ uint32_t oct_max(uint32_t v) {
-  v = quad_max(v);
-  const uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x141, 0xF, 0xF, true));
   return v > o ? v : o;
 }
 
@@ -49,8 +44,7 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t top) {
   return e == 255u ? 255u : (e > low ? e - low : 0u);
 }
 
-// The codes of N values (a multiple of 8; 4 for e4m3) under the scale byte b:
-// four bits each, or a byte.
+// The codes of N values (a multiple of 8) under the scale byte b: four bits each, or a byte.
 template <bool F8, int N>
 __device__ __forceinline__ void mx_codes(const float v[N], uint32_t b, uint32_t* out) {
   const float r = __builtin_bit_cast(float, (254u - (b < 254u ? b : 253u)) << 23);  // 2^-e
