@@ -414,8 +414,9 @@ qblk_status_t qblk_moe(const qblk_moe_t* args, qblk_stream_t stream);
  * activations are formed by the 8-bit matrix instructions, which drop of the
  * products of 8 neighbouring columns what lies below 2^-13 of the largest.  A token
  * with a NaN block has NaN results, and so has a row of W with one.  With MXFP8
- * and F32 an element has to be a bf16 number (2^-133 to 2^128; what is smaller
- * counts as 0).
+ * and F32 elements are taken as bf16 numbers: multiples of 2^-133 (others, of
+ * blocks under the lowest scales, may move by that much) below 2^128 (all that the
+ * quantizers make; others are infinite).
  * m at most 2^26, k at most 2^23 (QBLK_ERR_SHAPE).
  *
  * Codes are 16-byte aligned, the scales' bytes at any address; workspaces as for
