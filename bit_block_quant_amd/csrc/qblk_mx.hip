@@ -122,8 +122,9 @@ __global__ __launch_bounds__(256) void k_dequant_mx(const uint8_t* __restrict__ 
 // below 2^-13 of it, which an fp32 result shows; both operands are widened to
 // bf16 with their scales instead (an element times its scale is a bf16 number) and
 // multiplied there, where sums are exact to fp32 rounding.  (e2m1 by e2m1: the
-// products of a block are whole multiples of 1/4 up to 36 of one scale, and the
-// scaled instructions' sums were found equal to fp32 sums of them.)
+// products of a block are whole multiples of 1/4 up to 36 of one scale, and the scaled
+// instructions' sums are those of fp32 additions of blocks: exact under one scale, else within 4
+// units of 2^-24 of the sum of magnitudes over 4096 columns.)
 // XSRC: kCodes, x as codes and scales; else the element type of x, which every
 // workgroup quantizes itself (one launch less; for few values, see fused_quant).
 constexpr int kCodes = 3;
@@ -504,7 +505,8 @@ constexpr bool has_shape(int shape, bool f8) { return f8 || shape != 1; }
 // the rest of a workgroup's time, and of a split its join.  Fitted to 2300 times of 90
 // products of either kind (9 matrices, 20 to 3000 tokens, every shape, 1 to 16
 // splits, weights from memory): the choice is 0.5% (e2m1) and 1.6% (e4m3) behind the best
-// form on average, at worst 18% (11008 x 4096, 160 tokens: 22.5 us for 19.1).
+// form on average, at worst 18% (11008 x 4096, 160 tokens: 22.5 us for 19.1).  More tokens lie
+// outside the fit (14336 x 4096, 4096 tokens, e2m1: a round of 256 x 256 takes 36 us for an estimated 29).
 double tile_us(int64_t tiles, int shape, int64_t per, int64_t splits, int64_t out, bool f8, int64_t cus) {
   constexpr double both[2][6] = {{1.68, 1.27, 0.72, 1.16, 0.91, 0.59}, {1.28, 0.76, 0.575, 0.85, 0.60, 0.46}};
   constexpr double alone[2][3] = {{0.61, 0.505, 0.39}, {0.505, 0.34, 0.29}};

@@ -8,9 +8,11 @@
 // of a lane's blocks lie together.  Results are summed by the
 // matrix cores alone, scales included.
 //
-// Large products are bound by power (8192^3: e2m1 261 us, 4.2 PFLOP/s, e4m3 399, 2.75; with
-// zeros as operands 219 and 338) and by copies and the results' stores beside the matrix
-// instructions; some hundred tokens by the copies into LDS (5003 x 11008, 333 tokens, e2m1: 22
+// Large products (8192^3: e2m1 261 us, 4.2 PFLOP/s, e4m3 399, 2.75; the instructions alone
+// sustain 6.9 and 4.2) have matrix instructions in half (e2m1) to two thirds (e4m3) of the
+// cycles: a unit's one workgroup of 256 x 256 waits at a barrier a stage, and its tile's first
+// copies and last stores stand alone.  Power takes the clock down besides (zeros as operands: 219
+// and 338 us).  Some hundred tokens are bound by the copies into LDS (5003 x 11008, 333 tokens, e2m1: 22
 // us, 11 TB/s out of L2).  What bounds the shapes: at BM x BN results a stage a unit copies
 // 128 (BM + BN) bytes of e2m1 for BM BN / 1024 matrix instructions of each of its four
 // SIMDs, so wide tiles where there are enough of them.

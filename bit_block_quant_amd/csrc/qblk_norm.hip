@@ -129,8 +129,9 @@ __device__ __forceinline__ float row_max(float v, float* part, int waves, int wa
   return v;
 }
 
-// Memory bound, one pass (16384 rows of 4096 bf16 with a residual, to MXFP8: 84.0 us, 5.6 TB/s;
-// 4096 rows 24 to 26 us; one row 2.9: a launch and one round trip).  All loads of a row go
+// Memory bound, one pass (16384 rows of 4096 bf16 with a residual, to MXFP8: 84 to 90 us, 5.2 to
+// 5.6 TB/s; 4096 rows 24 to 26 us; one row 2.7: a launch and one round trip).  1024 rows of 32768: 61
+// us for 45 of bytes, since 113 registers leave room for one workgroup of 1024 threads a unit.  All loads of a row go
 // out before the first use, the weights' too.
 // One row by TH threads, V units of 8 values each (unit t, t + TH, ...); rows
 // of one wave: four to a workgroup.  Rows wider than 8 TH V values (LOOP) are read a
