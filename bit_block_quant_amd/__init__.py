@@ -718,7 +718,7 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, quant=ACT_F8, out=None, scale=No
     Norm(codes, scale, total, y): total is t (None without a residual; give `total`, which may
     be x or residual, to place it), y the normed values in x's type (always with quant=None, else
     where `y` is a tensor, or True for a new one).  A row's results do not depend on the rows
-    beside it."""
+    beside it.  Other outputs must not overlap an input or one another."""
     if quant not in (None, ACT_F8, ACT_I8, ACT_MXFP8, ACT_MXFP4):
         raise ValueError(f"quant: expected one of ACTS' values or None, got {quant!r}")
     dev = _need(x, "x", _FLOAT_IN, ndim=2)
