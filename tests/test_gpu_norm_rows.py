@@ -10,11 +10,12 @@ behind that, the division, eps and the root are in 64 bits, the root's reciproca
 t * weight is one rounding (none for 16-bit t and weights), the product with the root's two
 parts at most 2 more: 7 u, or 6 u.
 """
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_mx import TYPES, act, q  # noqa: E402, F401
+from test_gpu_mx import E2M1, E4M3, TYPES, act, q  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -75,3 +76,24 @@ def test_near_the_formula_from_16_bits(q, h):  # noqa: F811
         t = x.double()
         ref = (t / t.square().mean(1, keepdim=True).sqrt() * w.double()).abs().amax(1) / 127
         assert torch.all((got - ref).abs() <= 7 * U * ref)  # 6 u, and the division
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["mxfp4", "mxfp8"])
+def test_on_borders_and_beside_them(q, name, dtype):  # noqa: F811
+    """x of +-2: y is +-weight, exactly on the middle of two codes, on a power of two, or an ulp
+    beside it; zeros and rows of blocks of zeros too.  The quantizer's own bytes."""
+    rng = np.random.default_rng(1)
+    h = 8192
+    table = np.array(E2M1 if name == "mxfp4" else E4M3)
+    points = np.concatenate([(table[1:] + table[:-1]) / 2, table, [table[-1] * 1.125]]).astype(np.float32)
+    w = rng.choice(points, (h // 32, 32))
+    w = np.where(rng.random(w.shape) < 0.6, np.nextafter(w, np.float32(rng.choice([-1e30, 1e30], w.shape))), w).astype(np.float32)
+    w *= 2.0 ** rng.integers(-40, 40, (h // 32, 1))
+    w[5::16] = 0
+    w = torch.from_numpy(w.astype(np.float32).reshape(-1)).cuda()
+    sign = torch.from_numpy(rng.choice([-1.0, 1.0], (40, h)).astype(np.float32)).cuda()
+    r = q.rmsnorm((2 * sign).to(TYPES[dtype]), w, eps=0.0, quant=act(q, name))
+    codes, scale = getattr(q, f"quantize_{name}")(sign * w)
+    assert torch.equal(r.scale.view(torch.uint8), scale.view(torch.uint8))
+    assert torch.equal(r.codes.view(torch.uint8), codes.view(torch.uint8))
